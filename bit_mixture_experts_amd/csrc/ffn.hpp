@@ -1,0 +1,171 @@
+// Pieces shared by the forward and backward kernels of the dense gated feed-forward block.
+#pragma once
+
+#include "dense_gemm.hpp"
+#include "internal.hpp"
+#include "mx.hpp"
+
+namespace moe4 {
+
+// Row of the [2I, H] gate/up stack that row r of a tile of gate/up pairs takes: the tile's
+// 32-row MFMA tiles alternate between 32 gate rows and the up rows of the same pairs, so that
+// a lane holds both halves of a pair at the same place of neighbouring accumulators.
+__device__ __forceinline__ int pair_row(int layout, int I, int j0, int r) {
+  const int j = j0 + (r >> 6) * 32 + (r & 31);
+  if (j >= I) return -1;
+  const bool up = (r >> 5) & 1;
+  return layout == MOE4_GU_HALVES ? (up ? I + j : j) : 2 * j + (up ? 1 : 0);
+}
+
+// The activation and its gradients. Comparisons, not fmin/fmax, so that a NaN stays one.
+struct FfnAct {
+  int act;
+  float alpha, limit;
+  __device__ __forceinline__ float apply(float g, float u) const {
+    if (act == MOE4_ACT_SWIGLU) return g * sigmoidf_(g) * u;
+    const float gc = g > limit ? limit : g;
+    const float uc = u > limit ? limit : u < -limit ? -limit : u;
+    return (uc + 1.0f) * gc * sigmoidf_(alpha * gc);
+  }
+  // h, and dg, du for an upstream gradient dh; beyond a clamp's border the gradient is zero,
+  // on the border it passes
+  __device__ __forceinline__ void backward(float g, float u, float dh, float& h, float& dg,
+                                           float& du) const {
+    if (act == MOE4_ACT_SWIGLU) {
+      const float s = sigmoidf_(g), gs = g * s;
+      h = gs * u;
+      du = dh * gs;
+      dg = dh * u * (s + gs * (1.0f - s));
+    } else {
+      const float gc = g > limit ? limit : g;
+      const float uc = u > limit ? limit : u < -limit ? -limit : u;
+      const float s = sigmoidf_(alpha * gc), gs = gc * s, lin = uc + 1.0f;
+      h = lin * gs;
+      dg = g > limit ? 0.0f : dh * lin * (s + alpha * gs * (1.0f - s));
+      du = u > limit || u < -limit ? 0.0f : dh * gs;
+    }
+  }
+};
+
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, float* v) {
+  const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo(x[i]);
+    v[2 * i + 1] = bf16hi(x[i]);
+  }
+}
+__device__ __forceinline__ void load8_f32(const float* p, float* v) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ u32x4 pack8_bf16(const float* v) {
+  u32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  return x;
+}
+__device__ __forceinline__ void store8_f32(float* p, const float* v) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+// 8 values of a tensor that is bf16 or fp32 (a uniform branch)
+__device__ __forceinline__ void load8_dt(const void* p, int dtype, int64_t i, float* v) {
+  if (dtype == MOE4_DTYPE_F32) load8_f32(static_cast<const float*>(p) + i, v);
+  else load8_bf16(static_cast<const uint16_t*>(p) + i, v);
+}
+__device__ __forceinline__ void store8_dt(void* p, int dtype, int64_t i, const float* v) {
+  if (dtype == MOE4_DTYPE_F32) store8_f32(static_cast<float*>(p) + i, v);
+  else *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = pack8_bf16(v);
+}
+
+// One product of the block and what its epilogue does: out[b][a] = sum_k A B (+ bias[a]) (+
+// add[b][a]), a < na, b < nb.
+struct FfnProduct {
+  Operand A, B;
+  int64_t na_s, nb_s;   // bytes of the operands' scales (MXFP8)
+  int K, na, nb;
+  const uint16_t* bias;
+  const void* add;
+  int add_dtype;
+  void* out;
+  int out_dtype;
+};
+
+template <typename S, int MA, int MB, bool FP8>
+__device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, int ib,
+                                                 uint8_t* lds) {
+  const int a0 = ia * S::BA, b0 = ib * S::BB;
+  Loader<MA, S::BA, S::kThreads> la;
+  Loader<MB, S::BB, S::kThreads> lb;
+  constexpr int es = FP8 ? 1 : 2;
+  if constexpr (MA == kOpRow) {
+    const int n = min(S::BA, p.na - a0);
+    la.init_row(p.A, es, p.K, a0, n, [=](int r) { return r < n ? r : -1; });
+  } else {
+    la.init_col(p.A, p.K, a0);
+  }
+  if constexpr (MB == kOpRow) {
+    const int n = min(S::BB, p.nb - b0);
+    lb.init_row(p.B, es, p.K, b0, n, [=](int r) { return r < n ? r : -1; });
+  } else {
+    lb.init_col(p.B, p.K, b0);
+  }
+  MxState<FP8> mx;
+  if constexpr (FP8) mx = {p.A.s, p.B.s, p.na_s, p.nb_s};
+  f32x16 acc[S::TA][S::TB];
+  gemm_loop<S, MA, MB, FP8>(
+      acc, lds, la, lb, p.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
+      [&](int r) { return b0 + r < p.nb ? b0 + r : -1; });
+  for_each8<S, false>(acc, lds, [&](int row, int a, float* v) {
+    const int b = b0 + row, c = a0 + a;
+    if (b >= p.nb || c >= p.na) return;
+    const int64_t at = (int64_t)b * p.na + c;
+    if (p.bias) {
+      float x[8];
+      load8_bf16(p.bias + c, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += x[i];
+    }
+    if (p.add) {
+      float x[8];
+      load8_dt(p.add, p.add_dtype, at, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += x[i];
+    }
+    store8_dt(p.out, p.out_dtype, at, v);
+  });
+}
+
+template <typename S, int MA, int MB, bool FP8>
+__global__ __launch_bounds__(S::kThreads, 2) void k_ffn_product(const FfnProduct p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
+  const int na = (p.na + S::BA - 1) / S::BA, nb = (p.nb + S::BB - 1) / S::BB;
+  int ia, ib;
+  tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
+  ffn_product_tile<S, MA, MB, FP8>(p, ia, ib, stage_mem);
+}
+
+// dynamic LDS above 64 KiB has to be asked for once per kernel and device
+template <typename K>
+inline hipError_t allow_lds(K* kernel, int bytes) {
+  return bytes <= 64 * 1024 ? hipSuccess
+                            : hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename S, int MA, int MB, bool FP8>
+inline hipError_t launch_product(const FfnProduct& p, hipStream_t s) {
+  const int64_t n = (int64_t)((p.na + S::BA - 1) / S::BA) * ((p.nb + S::BB - 1) / S::BB);
+  auto* k = &k_ffn_product<S, MA, MB, FP8>;
+  hipError_t e = allow_lds(k, S::kLds);
+  if (e != hipSuccess) return e;
+  k<<<(uint32_t)n, S::kThreads, S::kLds, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace moe4

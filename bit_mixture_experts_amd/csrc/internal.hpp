@@ -108,6 +108,38 @@ hipError_t launch_expert_backward(const moe4_experts& ex, const uint16_t* x_perm
                                   float* dx_perm, float* dA, float* dB, void* ws,
                                   int* variant, const LaunchEvents& le, hipStream_t s);
 
+// ---- the dense half of the block
+// out[c] (of dtype) = sum over the P rows of part [P, N]
+hipError_t launch_sum_rows(const float* part, int P, int N, void* out, int dtype, hipStream_t s);
+hipError_t launch_add_rmsnorm(const void* x, int x_dtype, const void* res, int res_dtype, void* sum,
+                              const void* w, int w_dtype, int T, int H, float eps, uint16_t* out,
+                              uint8_t* q, uint8_t* qs, float* rstd, hipStream_t s);
+size_t add_rmsnorm_ws_bytes(int64_t T, int H);
+hipError_t launch_add_rmsnorm_backward(const void* dy, int dy_dtype, const void* sv, int s_dtype,
+                                       const void* w, int w_dtype, const float* rstd,
+                                       const void* dres, int T, int H, void* dx, int dx_dtype,
+                                       float* dw, void* ws, hipStream_t st);
+hipError_t launch_quantize_mxfp8(const void* x, int x_dtype, int64_t n, uint8_t* q, uint8_t* qs,
+                                 hipStream_t s);
+size_t ffn_forward_ws_bytes(const moe4_ffn& f, int64_t T);
+size_t ffn_backward_ws_bytes(const moe4_ffn& f, int64_t T);
+int ffn_variant(const moe4_ffn& f, int64_t T);   // the kernel family AUTO picks
+hipError_t launch_ffn_forward(const moe4_ffn& f, const void* x, const uint8_t* x_s, int T,
+                              const void* residual, int residual_dtype, void* out,
+                              int out_dtype, float* save_gu, void* ws, int* variant,
+                              hipStream_t s);
+hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, const float* gu,
+                               const uint16_t* dy, const void* add, int add_dtype, void* dx,
+                               int dx_dtype, void* dw_gu, void* dw_dn, void* db_gu, void* db_dn,
+                               int dw_dtype, void* ws, hipStream_t s);
+size_t grad_ws_bytes(int64_t n);
+int64_t grad_most_numel();
+hipError_t launch_grad_norm(const void* const* in, const int64_t* numel, const int32_t* dtype,
+                            int n, float* norm, void* ws, hipStream_t s);
+hipError_t launch_clip_grads(const void* const* in, void* const* out, const int64_t* numel,
+                             const int32_t* dtype, int n, float max_norm, const float* norm_in,
+                             float* norm_out, void* ws, hipStream_t s);
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace moe4

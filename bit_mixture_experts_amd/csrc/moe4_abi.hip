@@ -613,6 +613,332 @@ int moe4_expert_backward(const moe4_experts* ex, const uint16_t* x_perm, const i
   return rc;
 }
 
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kByteSpan = ((int64_t)1 << 31) - ((int64_t)1 << 24);   // 32-bit byte offsets
+
+#define REQUIRE_DTYPE(d, name)                                                          \
+  do {                                                                                  \
+    if ((d) != MOE4_DTYPE_BF16 && (d) != MOE4_DTYPE_F32)                                \
+      return fail(MOE4_EINVAL, "%s %s (%d)", name, (d) ? "unknown" : "unset", (int)(d)); \
+  } while (0)
+
+int check_norm_shape(int32_t T, int32_t H) {
+  if (T < 0) return fail(MOE4_ESHAPE, "T = %d is negative", T);
+  if (H < 8 || H > 16384 || H % 8)
+    return fail(MOE4_ESHAPE, "H = %d must be a multiple of 8 in [8, 16384]", H);
+  return MOE4_OK;
+}
+
+int check_ffn(const moe4_ffn* f) {
+  if (f == nullptr) return fail(MOE4_EINVAL, "moe4_ffn is NULL");
+  if (f->format != MOE4_FFN_BF16 && f->format != MOE4_FFN_MXFP8)
+    return fail(MOE4_EINVAL, "moe4_ffn.format %s (%d)", f->format ? "unknown" : "unset", f->format);
+  if (f->gu_layout != MOE4_GU_HALVES && f->gu_layout != MOE4_GU_INTERLEAVED)
+    return fail(MOE4_EINVAL, "moe4_ffn.gu_layout %s (%d)", f->gu_layout ? "unknown" : "unset",
+                f->gu_layout);
+  if (f->act != MOE4_ACT_SWIGLU && f->act != MOE4_ACT_SWIGLU_CLAMPED)
+    return fail(MOE4_EINVAL, "moe4_ffn.act %s (%d)", f->act ? "unknown" : "unset", f->act);
+  if (f->variant != MOE4_VARIANT_AUTO && f->variant != MOE4_VARIANT_SKINNY &&
+      f->variant != MOE4_VARIANT_TILED)
+    return fail(MOE4_EINVAL, "moe4_ffn.variant unknown (%d)", f->variant);
+  const int mx = f->format == MOE4_FFN_MXFP8, blk = mx ? 32 : 8;
+  if (f->H <= 0 || f->H % blk)
+    return fail(MOE4_ESHAPE, "moe4_ffn.H = %d is not a positive multiple of %d", f->H, blk);
+  if (f->I <= 0 || f->I % blk)
+    return fail(MOE4_ESHAPE, "moe4_ffn.I = %d is not a positive multiple of %d", f->I, blk);
+  const int64_t wide = f->H > 2 * (int64_t)f->I ? f->H : 2 * (int64_t)f->I;
+  if (2 * (int64_t)f->I * f->H * (mx ? 1 : 2) >= kByteSpan)
+    return fail(MOE4_ESHAPE, "moe4_ffn: 2*I*H = %lld; a weight must stay under 2 GiB",
+                (long long)(2 * (int64_t)f->I * f->H));
+  if (256 * 2 * wide >= kByteSpan)
+    return fail(MOE4_ESHAPE, "moe4_ffn: max(H, 2I) = %lld; 256 rows must stay under 2 GiB",
+                (long long)wide);
+  REQUIRE_PTR(f->w_gu, "moe4_ffn.w_gu");
+  REQUIRE_PTR(f->w_dn, "moe4_ffn.w_dn");
+  REQUIRE_ALIGN(f->w_gu, 16, "moe4_ffn.w_gu");
+  REQUIRE_ALIGN(f->w_dn, 16, "moe4_ffn.w_dn");
+  if (mx) {
+    REQUIRE_PTR(f->gu_s, "moe4_ffn.gu_s");
+    REQUIRE_PTR(f->dn_s, "moe4_ffn.dn_s");
+    REQUIRE_ALIGN(f->gu_s, 4, "moe4_ffn.gu_s");
+    REQUIRE_ALIGN(f->dn_s, 4, "moe4_ffn.dn_s");
+  } else if (f->gu_s || f->dn_s) {
+    return fail(MOE4_EINVAL, "moe4_ffn: scales given for bf16 weights");
+  }
+  REQUIRE_ALIGN(f->gu_bias, 16, "moe4_ffn.gu_bias");
+  REQUIRE_ALIGN(f->dn_bias, 16, "moe4_ffn.dn_bias");
+  if (f->act == MOE4_ACT_SWIGLU_CLAMPED && (!(f->act_limit > 0.0f) || !(f->act_alpha > 0.0f)))
+    return fail(MOE4_EINVAL,
+                "moe4_ffn.act_alpha/act_limit must be positive for the clamped GLU (got %g, %g)",
+                (double)f->act_alpha, (double)f->act_limit);
+  return MOE4_OK;
+}
+
+int check_ffn_tokens(const moe4_ffn* f, int32_t T) {
+  if (T < 0) return fail(MOE4_ESHAPE, "T = %d is negative", T);
+  if (f->variant == MOE4_VARIANT_SKINNY && T > 1 << 20)
+    return fail(MOE4_ESHAPE, "T = %d: the skinny variant takes at most 2^20 tokens", T);
+  const int64_t wide = f->H > f->I ? f->H : f->I;
+  if (f->format == MOE4_FFN_MXFP8 && T * (wide / 32) >= kByteSpan)
+    return fail(MOE4_ESHAPE, "T = %d: the activations' scales must stay under 2 GiB", T);
+  // workgroups of the smallest tiles, 256 threads each, in one 32-bit launch
+  if (((int64_t)T + 127) / 128 * ((2 * wide + 127) / 128) >= (int64_t)1 << 23)
+    return fail(MOE4_ESHAPE, "T = %d with max(H, I) = %lld is beyond one launch", T,
+                (long long)wide);
+  return MOE4_OK;
+}
+
+int check_grads(const void* const* grads, void* const* outs, const int64_t* numel,
+                const int32_t* dtype, int32_t n) {
+  if (n < 0 || n > 1 << 20) return fail(MOE4_ESHAPE, "n = %d outside [0, 2^20]", n);
+  if (n == 0) return MOE4_OK;
+  REQUIRE_PTR(grads, "grads");
+  REQUIRE_PTR(numel, "numel");
+  REQUIRE_PTR(dtype, "dtype");
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] < 0 || numel[i] > moe4::grad_most_numel())
+      return fail(MOE4_ESHAPE, "numel[%d] = %lld outside [0, 2^36]", i, (long long)numel[i]);
+    if (dtype[i] != MOE4_DTYPE_BF16 && dtype[i] != MOE4_DTYPE_F32)
+      return fail(MOE4_EINVAL, "dtype[%d] %s (%d)", i, dtype[i] ? "unknown" : "unset", dtype[i]);
+    if (numel[i] == 0) continue;
+    if (grads[i] == nullptr || (outs && outs[i] == nullptr))
+      return fail(MOE4_EINVAL, "%s[%d] is NULL", grads[i] ? "outs" : "grads", i);
+    if (!aligned(grads[i], 16) || (outs && !aligned(outs[i], 16)))
+      return fail(MOE4_EALIGN, "%s[%d] is not 16-byte aligned",
+                  aligned(grads[i], 16) ? "outs" : "grads", i);
+  }
+  return MOE4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe4_add_rmsnorm(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype,
+                     void* sum_out, const void* weight, int32_t w_dtype, int32_t T, int32_t H,
+                     float eps, uint16_t* out, uint8_t* out_q, uint8_t* out_s, float* rstd,
+                     void* stream) {
+  int rc = check_norm_shape(T, H);
+  if (rc) return rc;
+  REQUIRE_DTYPE(x_dtype, "x_dtype");
+  REQUIRE_DTYPE(w_dtype, "w_dtype");
+  if (residual) REQUIRE_DTYPE(res_dtype, "res_dtype");
+  if (!(eps >= 0.0f)) return fail(MOE4_EINVAL, "eps = %g must not be negative", (double)eps);
+  if (sum_out && !residual && T > 0)
+    return fail(MOE4_EINVAL, "sum_out given without a residual");
+  if ((out_q == nullptr) != (out_s == nullptr))
+    return fail(MOE4_EINVAL, "out_q and out_s must be given together");
+  if (out_q && H % 32)
+    return fail(MOE4_ESHAPE, "H = %d must be a multiple of 32 for an MXFP8 output", H);
+  if (T == 0) return ok();
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(weight, "weight");
+  if (!out && !out_q) return fail(MOE4_EINVAL, "out and out_q are both NULL");
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(residual, 16, "residual");
+  REQUIRE_ALIGN(sum_out, 16, "sum_out");
+  REQUIRE_ALIGN(weight, 16, "weight");
+  REQUIRE_ALIGN(out, 16, "out");
+  REQUIRE_ALIGN(out_q, 16, "out_q");
+  REQUIRE_ALIGN(rstd, 4, "rstd");
+  return launched(moe4::launch_add_rmsnorm(x, x_dtype, residual, res_dtype, sum_out, weight,
+                                           w_dtype, T, H, eps, out, out_q, out_s, rstd,
+                                           (hipStream_t)stream),
+                  "moe4_add_rmsnorm");
+}
+
+size_t moe4_add_rmsnorm_workspace_size(int32_t T, int32_t H) {
+  if (check_norm_shape(T, H) != MOE4_OK) return 0;
+  ok();
+  const size_t need = moe4::add_rmsnorm_ws_bytes(T, H);
+  return need < 256 ? 256 : need;
+}
+
+int moe4_add_rmsnorm_backward(const void* dy, int32_t dy_dtype, const void* s, int32_t s_dtype,
+                              const void* weight, int32_t w_dtype, const float* rstd,
+                              const void* dres, int32_t T, int32_t H, void* dx, int32_t dx_dtype,
+                              float* dweight, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_norm_shape(T, H);
+  if (rc) return rc;
+  REQUIRE_DTYPE(dy_dtype, "dy_dtype");
+  REQUIRE_DTYPE(s_dtype, "s_dtype");
+  REQUIRE_DTYPE(w_dtype, "w_dtype");
+  REQUIRE_DTYPE(dx_dtype, "dx_dtype");
+  if (T > 0) {
+    REQUIRE_PTR(dy, "dy");
+    REQUIRE_PTR(s, "s");
+    REQUIRE_PTR(weight, "weight");
+    REQUIRE_PTR(rstd, "rstd");
+    REQUIRE_PTR(dx, "dx");
+  }
+  REQUIRE_ALIGN(dy, 16, "dy");
+  REQUIRE_ALIGN(s, 16, "s");
+  REQUIRE_ALIGN(weight, 16, "weight");
+  REQUIRE_ALIGN(rstd, 4, "rstd");
+  REQUIRE_ALIGN(dres, 16, "dres");
+  REQUIRE_ALIGN(dx, 16, "dx");
+  REQUIRE_ALIGN(dweight, 16, "dweight");
+  if (dweight && T > 0) {
+    rc = check_ws(ws, ws_bytes, moe4::add_rmsnorm_ws_bytes(T, H), "moe4_add_rmsnorm_backward");
+    if (rc) return rc;
+  }
+  if (T == 0 && !dweight) return ok();
+  return launched(moe4::launch_add_rmsnorm_backward(dy, dy_dtype, s, s_dtype, weight, w_dtype,
+                                                    rstd, dres, T, H, dx, dx_dtype, dweight, ws,
+                                                    (hipStream_t)stream),
+                  "moe4_add_rmsnorm_backward");
+}
+
+int moe4_quantize_mxfp8(const void* x, int32_t x_dtype, int64_t R, int64_t K, uint8_t* q,
+                        uint8_t* s, void* stream) {
+  REQUIRE_DTYPE(x_dtype, "x_dtype");
+  if (R < 0) return fail(MOE4_ESHAPE, "R = %lld is negative", (long long)R);
+  if (K < 0 || K % 32)
+    return fail(MOE4_ESHAPE, "K = %lld is not a non-negative multiple of 32", (long long)K);
+  if (K && R > ((int64_t)1 << 40) / K)
+    return fail(MOE4_ESHAPE, "R * K is beyond the supported 2^40");
+  if (R == 0 || K == 0) return ok();
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(q, "q");
+  REQUIRE_PTR(s, "s");
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(q, 16, "q");
+  return launched(moe4::launch_quantize_mxfp8(x, x_dtype, R * K, q, s, (hipStream_t)stream),
+                  "moe4_quantize_mxfp8");
+}
+
+size_t moe4_ffn_workspace_size(const moe4_ffn* f, int32_t T, int32_t backward) {
+  if (check_ffn(f) != MOE4_OK || check_ffn_tokens(f, T) != MOE4_OK) return 0;
+  ok();
+  const size_t need = backward ? moe4::ffn_backward_ws_bytes(*f, T) : moe4::ffn_forward_ws_bytes(*f, T);
+  return need < 256 ? 256 : need;
+}
+
+int moe4_ffn_forward(const moe4_ffn* f, const void* x, const uint8_t* x_s, int32_t T,
+                     const void* residual, int32_t res_dtype, void* out, int32_t out_dtype,
+                     float* save_gu, void* ws, size_t ws_bytes, void* stream) {
+  g_variant = 0;
+  int rc = check_ffn(f);
+  if (rc) return rc;
+  rc = check_ffn_tokens(f, T);
+  if (rc) return rc;
+  REQUIRE_DTYPE(out_dtype, "out_dtype");
+  if (residual) REQUIRE_DTYPE(res_dtype, "res_dtype");
+  if (x_s && f->format == MOE4_FFN_BF16)
+    return fail(MOE4_EINVAL, "x_s given for a bf16 block");
+  if (T == 0) return ok();
+  REQUIRE_PTR(x, "x");
+  if (f->format == MOE4_FFN_MXFP8) REQUIRE_PTR(x_s, "x_s");
+  REQUIRE_PTR(out, "out");
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(x_s, 4, "x_s");
+  REQUIRE_ALIGN(residual, 16, "residual");
+  REQUIRE_ALIGN(out, 16, "out");
+  REQUIRE_ALIGN(save_gu, 16, "save_gu");
+  rc = check_ws(ws, ws_bytes, moe4::ffn_forward_ws_bytes(*f, T), "moe4_ffn_forward");
+  if (rc) return rc;
+  int variant = 0;
+  hipError_t e = moe4::launch_ffn_forward(*f, x, x_s, T, residual, res_dtype, out, out_dtype,
+                                          save_gu, ws, &variant, (hipStream_t)stream);
+  rc = launched(e, "moe4_ffn_forward");
+  if (rc == MOE4_OK) g_variant = variant;
+  return rc;
+}
+
+int moe4_ffn_backward(const moe4_ffn* f, const uint16_t* x, int32_t T, const float* save_gu,
+                      const uint16_t* dy, const void* dx_add, int32_t add_dtype, void* dx,
+                      int32_t dx_dtype, void* dw_gu, void* dw_dn, void* db_gu, void* db_dn,
+                      int32_t dw_dtype, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_ffn(f);
+  if (rc) return rc;
+  if (f->format != MOE4_FFN_BF16)
+    return fail(MOE4_EUNSUPPORTED, "moe4_ffn_backward: bf16 blocks only (format %d)", f->format);
+  rc = check_ffn_tokens(f, T);
+  if (rc) return rc;
+  if (dx) REQUIRE_DTYPE(dx_dtype, "dx_dtype");
+  if (dx_add) {
+    if (!dx && T > 0) return fail(MOE4_EINVAL, "dx_add given without dx");
+    REQUIRE_DTYPE(add_dtype, "add_dtype");
+  }
+  const bool params = dw_gu || dw_dn || db_gu || db_dn;
+  if (params) REQUIRE_DTYPE(dw_dtype, "dw_dtype");
+  if (T > 0 && (dx || params)) {
+    REQUIRE_PTR(dy, "dy");
+    REQUIRE_PTR(save_gu, "save_gu");
+    if (dw_gu) REQUIRE_PTR(x, "x");
+  }
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(save_gu, 16, "save_gu");
+  REQUIRE_ALIGN(dy, 16, "dy");
+  REQUIRE_ALIGN(dx_add, 16, "dx_add");
+  REQUIRE_ALIGN(dx, 16, "dx");
+  REQUIRE_ALIGN(dw_gu, 16, "dw_gu");
+  REQUIRE_ALIGN(dw_dn, 16, "dw_dn");
+  REQUIRE_ALIGN(db_gu, 16, "db_gu");
+  REQUIRE_ALIGN(db_dn, 16, "db_dn");
+  hipStream_t s = (hipStream_t)stream;
+  if (T == 0) {
+    // no token: zero gradients (by a fill kernel, so that the call can be captured)
+    const int words = dw_dtype == MOE4_DTYPE_F32 ? 1 : 2;   // elements of a 4-byte word
+    const struct { void* p; int n; } z[] = {{dw_gu, 2 * f->I * f->H}, {dw_dn, f->H * f->I},
+                                            {db_gu, 2 * f->I}, {db_dn, f->H}};
+    for (const auto& q : z) {
+      if (!q.p) continue;
+      rc = launched(moe4::launch_zero_i32(static_cast<int32_t*>(q.p), q.n / words, s),
+                    "moe4_ffn_backward");
+      if (rc) return rc;
+    }
+    return ok();
+  }
+  if (!dx && !params) return ok();
+  rc = check_ws(ws, ws_bytes, moe4::ffn_backward_ws_bytes(*f, T), "moe4_ffn_backward");
+  if (rc) return rc;
+  return launched(moe4::launch_ffn_backward(*f, x, T, save_gu, dy, dx_add, add_dtype, dx, dx_dtype,
+                                            dw_gu, dw_dn, db_gu, db_dn, dw_dtype, ws, s),
+                  "moe4_ffn_backward");
+}
+
+size_t moe4_grad_workspace_size(int32_t n) {
+  if (n < 0 || n > 1 << 20) {
+    fail(MOE4_ESHAPE, "moe4_grad_workspace_size: n = %d outside [0, 2^20]", n);
+    return 0;
+  }
+  ok();
+  return moe4::grad_ws_bytes(n);
+}
+
+int moe4_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                   int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_grads(grads, nullptr, numel, dtype, n);
+  if (rc) return rc;
+  REQUIRE_PTR(norm, "norm");
+  REQUIRE_ALIGN(norm, 4, "norm");
+  rc = check_ws(ws, ws_bytes, moe4::grad_ws_bytes(n), "moe4_grad_norm");
+  if (rc) return rc;
+  return launched(moe4::launch_grad_norm(grads, numel, dtype, n, norm, ws, (hipStream_t)stream),
+                  "moe4_grad_norm");
+}
+
+int moe4_clip_grads(const void* const* grads, void* const* outs, const int64_t* numel,
+                    const int32_t* dtype, int32_t n, float max_norm, const float* norm_in,
+                    float* norm_out, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_grads(grads, outs, numel, dtype, n);
+  if (rc) return rc;
+  if (!(max_norm > 0.0f)) return fail(MOE4_EINVAL, "max_norm = %g must be positive", (double)max_norm);
+  REQUIRE_ALIGN(norm_in, 4, "norm_in");
+  REQUIRE_ALIGN(norm_out, 4, "norm_out");
+  if (!norm_in) {
+    rc = check_ws(ws, ws_bytes, moe4::grad_ws_bytes(n), "moe4_clip_grads");
+    if (rc) return rc;
+  }
+  return launched(moe4::launch_clip_grads(grads, outs, numel, dtype, n, max_norm, norm_in, norm_out,
+                                          ws, (hipStream_t)stream),
+                  "moe4_clip_grads");
+}
+
 size_t moe4_workspace_size(const moe4_experts* ex, int32_t T, int32_t k) {
   if (check_experts(ex) != MOE4_OK) return 0;
   if (T < 0 || k < 1 || k > ex->E || (int64_t)T * k >= ((int64_t)1 << 31)) {

@@ -31,6 +31,7 @@ MOE4_ACT_SWIGLU, MOE4_ACT_SWIGLU_CLAMPED = 1, 2
 MOE4_VARIANT_AUTO, MOE4_VARIANT_SKINNY, MOE4_VARIANT_TILED = 0, 1, 2
 MOE4_DTYPE_BF16, MOE4_DTYPE_F32 = 1, 2
 MOE4_NOALLOC_SCRATCH_BYTES = 16 << 20
+MOE4_FFN_BF16, MOE4_FFN_MXFP8 = 1, 2
 
 # every symbol declared in include/moe4.h
 EXPORTS = ("moe4_quantize_nf4", "moe4_compress_absmax", "moe4_expand_absmax",
@@ -38,6 +39,10 @@ EXPORTS = ("moe4_quantize_nf4", "moe4_compress_absmax", "moe4_expand_absmax",
            "moe4_router_logits", "moe4_route", "moe4_route_backward", "moe4_permute",
            "moe4_gather_rows", "moe4_route_permute", "moe4_expert_forward", "moe4_expert_forward_gather", "moe4_expert_forward_noalloc", "moe4_combine",
            "moe4_expert_backward",
+           "moe4_add_rmsnorm", "moe4_add_rmsnorm_backward", "moe4_add_rmsnorm_workspace_size",
+           "moe4_quantize_mxfp8", "moe4_ffn_forward", "moe4_ffn_backward",
+           "moe4_ffn_workspace_size", "moe4_grad_norm", "moe4_clip_grads",
+           "moe4_grad_workspace_size",
            "moe4_workspace_size", "moe4_set_timing_events", "moe4_last_error",
            "moe4_last_variant")
 
@@ -60,8 +65,22 @@ class Moe4Experts(ctypes.Structure):
     ]
 
 
+class Moe4Ffn(ctypes.Structure):
+    """Mirror of the C struct moe4_ffn."""
+    _fields_ = [
+        ("format", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
+        ("gu_layout", ctypes.c_int32), ("act", ctypes.c_int32),
+        ("act_alpha", ctypes.c_float), ("act_limit", ctypes.c_float), ("variant", ctypes.c_int32),
+        ("w_gu", ctypes.c_void_p), ("gu_s", ctypes.c_void_p),
+        ("w_dn", ctypes.c_void_p), ("dn_s", ctypes.c_void_p),
+        ("gu_bias", ctypes.c_void_p), ("dn_bias", ctypes.c_void_p),
+    ]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _P = ctypes.POINTER(Moe4Experts)
+_PF = ctypes.POINTER(Moe4Ffn)
+_f32c = ctypes.c_float
 _SIGS = {
     "moe4_quantize_nf4": ([_vp, _i64, _i32, _vp, _vp, _vp], ctypes.c_int),
     "moe4_decode_mxfp4": ([_vp, _vp, _i64, _i64, _vp, _vp], ctypes.c_int),
@@ -84,6 +103,20 @@ _SIGS = {
     "moe4_combine": ([_vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp], ctypes.c_int),
     "moe4_expert_backward": ([_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
                              ctypes.c_int),
+    "moe4_add_rmsnorm": ([_vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _f32c, _vp, _vp, _vp,
+                          _vp, _vp], ctypes.c_int),
+    "moe4_add_rmsnorm_backward": ([_vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp,
+                                   _i32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "moe4_add_rmsnorm_workspace_size": ([_i32, _i32], ctypes.c_size_t),
+    "moe4_quantize_mxfp8": ([_vp, _i32, _i64, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "moe4_ffn_forward": ([_PF, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _sz, _vp],
+                         ctypes.c_int),
+    "moe4_ffn_backward": ([_PF, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp,
+                           _i32, _vp, _sz, _vp], ctypes.c_int),
+    "moe4_ffn_workspace_size": ([_PF, _i32, _i32], ctypes.c_size_t),
+    "moe4_grad_norm": ([_vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "moe4_clip_grads": ([_vp, _vp, _vp, _vp, _i32, _f32c, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "moe4_grad_workspace_size": ([_i32], ctypes.c_size_t),
     "moe4_workspace_size": ([_P, _i32, _i32], ctypes.c_size_t),
     "moe4_set_timing_events": ([_vp, _i32], ctypes.c_int),
     "moe4_last_error": ([], ctypes.c_char_p),
@@ -362,3 +395,246 @@ def moe4_workspace_size(ex, T, k):
     if n == 0:
         raise Moe4Error(MOE4_EINVAL, moe4_last_error())
     return n
+
+
+# ---- the dense half of the block: norm, MXFP8, feed-forward block, gradient clipping.
+# These check every size against the others (the kernels trust them) and that all tensors,
+# and the stream, are on the current device.
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _dt(t):
+    return 0 if t is None else MOE4_DTYPE_F32 if t.dtype == torch.float32 else MOE4_DTYPE_BF16
+
+
+class _Call:
+    """Pointers of one call's tensors: shape, dtype, contiguity and device checked."""
+
+    def __init__(self, fn):
+        self.fn = fn
+        self.dev = None
+
+    def ptr(self, t, name, shape, dtypes):
+        if t is None:
+            return None
+        p = _ptr(t, dtypes, name)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+        self.place(t, name)
+        return p
+
+    def place(self, t, name):
+        d = t.get_device()
+        if self.dev is None:
+            self.dev = d
+            if d != torch.cuda.current_device():
+                raise ValueError(f"{self.fn}: {name} is on device {d}, the current device is "
+                                 f"{torch.cuda.current_device()}")
+        elif d != self.dev:
+            raise ValueError(f"{self.fn}: {name} is on device {d}, other tensors on {self.dev}")
+
+    def ws(self, ws):
+        if ws is None:
+            return None, 0
+        p = _ptr(ws, None, "ws")
+        self.place(ws, "ws")
+        return p, ws.numel() * ws.element_size()
+
+    def stream(self, stream):
+        d = getattr(stream, "device_index", None)
+        if d is not None and self.dev is not None and d != self.dev:
+            raise ValueError(f"{self.fn}: the stream is on device {d}, the tensors on {self.dev}")
+        return _stream(stream)
+
+
+def moe4_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, out_q=None, out_s=None,
+                     rstd=None, stream=None):
+    """s = x + residual (rounded to the residual's type; sum_out), y = s * rstd * weight, as bf16
+    (out) and, or, MXFP8 (out_q u8 or float8_e4m3fn [T, H], out_s u8 or float8_e8m0fnu [T, H/32]).
+    x, residual bf16 or f32 [T, H]; weight bf16 or f32 [H]; rstd f32 [T]."""
+    c = _Call("add_rmsnorm")
+    T, H = sh = tuple(x.shape)
+    if sum_out is not None and residual is not None and sum_out.dtype != residual.dtype:
+        raise TypeError("sum_out must have the residual's dtype")
+    px = c.ptr(x, "x", sh, _FLOATS)
+    _check(_lib.moe4_add_rmsnorm(
+        px, _dt(x), c.ptr(residual, "residual", sh, _FLOATS), _dt(residual),
+        c.ptr(sum_out, "sum_out", sh, _FLOATS), c.ptr(weight, "weight", (H,), _FLOATS), _dt(weight),
+        T, H, eps, c.ptr(out, "out", sh, _BF16), c.ptr(out_q, "out_q", sh, _CODES),
+        c.ptr(out_s, "out_s", (T, H // 32), _SCALES), c.ptr(rstd, "rstd", (T,), _F32),
+        c.stream(stream)))
+
+
+def moe4_add_rmsnorm_workspace_size(T, H):
+    n = _lib.moe4_add_rmsnorm_workspace_size(T, H)
+    if n == 0:
+        raise Moe4Error(MOE4_ESHAPE, moe4_last_error())
+    return n
+
+
+def moe4_add_rmsnorm_backward(dy, s, weight, rstd, dx, dres=None, dweight=None, ws=None,
+                              stream=None):
+    """Gradient of moe4_add_rmsnorm: dx (of x and of the residual alike; dres, of dx's dtype, is
+    added) and dweight f32 [H]. s: the forward's sum_out (its x without a residual)."""
+    c = _Call("add_rmsnorm_backward")
+    T, H = sh = tuple(s.shape)
+    if dres is not None and dres.dtype != dx.dtype:
+        raise TypeError("dres must have dx's dtype")
+    ps = c.ptr(s, "s", sh, _FLOATS)
+    pw, nw = c.ws(ws)
+    _check(_lib.moe4_add_rmsnorm_backward(
+        c.ptr(dy, "dy", sh, _FLOATS), _dt(dy), ps, _dt(s), c.ptr(weight, "weight", (H,), _FLOATS),
+        _dt(weight), c.ptr(rstd, "rstd", (T,), _F32), c.ptr(dres, "dres", sh, _FLOATS), T, H,
+        c.ptr(dx, "dx", sh, _FLOATS), _dt(dx), c.ptr(dweight, "dweight", (H,), _F32), pw, nw,
+        c.stream(stream)))
+
+
+def moe4_quantize_mxfp8(x, q, s, stream=None):
+    """x bf16 or f32 [..., K] -> q (u8 or float8_e4m3fn) [..., K], s (u8 or float8_e8m0fnu)
+    [..., K/32]."""
+    c = _Call("quantize_mxfp8")
+    sh = tuple(x.shape)
+    K = sh[-1]
+    R = x.numel() // K if K else 0
+    _check(_lib.moe4_quantize_mxfp8(c.ptr(x, "x", sh, _FLOATS), _dt(x), R, K,
+                                    c.ptr(q, "q", sh, _CODES),
+                                    c.ptr(s, "s", sh[:-1] + (K // 32,), _SCALES), c.stream(stream)))
+
+
+class Ffn:
+    """Owns references to a dense feed-forward block's tensors and the C descriptor (moe4_ffn).
+    fmt MOE4_FFN_BF16: w_gu bf16 [2I, H], w_dn bf16 [H, I]; MOE4_FFN_MXFP8: codes of the same
+    shapes with scales gu_s [2I, H/32], dn_s [H, I/32] (moe4_quantize_mxfp8)."""
+
+    def __init__(self, fmt, w_gu, w_dn, *, gu_layout, act, H, I, gu_s=None, dn_s=None,
+                 gu_bias=None, dn_bias=None, act_alpha=1.702, act_limit=7.0,
+                 variant=MOE4_VARIANT_AUTO):
+        c = _Call("Ffn")
+        wdt = _CODES if fmt == MOE4_FFN_MXFP8 else _BF16
+        self.tensors = (w_gu, w_dn, gu_s, dn_s, gu_bias, dn_bias)
+        self.desc = Moe4Ffn(
+            format=fmt, H=H, I=I, gu_layout=gu_layout, act=act, act_alpha=act_alpha,
+            act_limit=act_limit, variant=variant,
+            w_gu=c.ptr(w_gu, "w_gu", (2 * I, H), wdt),
+            gu_s=c.ptr(gu_s, "gu_s", (2 * I, H // 32), _SCALES),
+            w_dn=c.ptr(w_dn, "w_dn", (H, I), wdt),
+            dn_s=c.ptr(dn_s, "dn_s", (H, I // 32), _SCALES),
+            gu_bias=c.ptr(gu_bias, "gu_bias", (2 * I,), _BF16),
+            dn_bias=c.ptr(dn_bias, "dn_bias", (H,), _BF16))
+        self.H, self.I = H, I
+        self.device = w_gu.get_device()
+        self.ref = ctypes.byref(self.desc)
+
+    def with_variant(self, variant):
+        d = Moe4Ffn()
+        ctypes.pointer(d)[0] = self.desc
+        d.variant = variant
+        out = object.__new__(Ffn)
+        out.__dict__.update(self.__dict__)
+        out.desc, out.ref = d, ctypes.byref(d)
+        return out
+
+
+def _ffn_call(fn, ffn):
+    c = _Call(fn)
+    c.place(ffn.tensors[0], "w_gu")
+    return c
+
+
+def moe4_ffn_workspace_size(ffn, T, backward=False):
+    n = _lib.moe4_ffn_workspace_size(ffn.ref, T, int(bool(backward)))
+    if n == 0:
+        raise Moe4Error(MOE4_EINVAL, moe4_last_error())
+    return n
+
+
+def moe4_ffn_forward(ffn, x, out, x_s=None, residual=None, save_gu=None, ws=None, stream=None):
+    """out [T, H] (bf16 or f32) = the block on x (bf16, or MXFP8 codes with scales x_s) +
+    residual (bf16 or f32); save_gu f32 [T, 2I]: the pre-activations for the backward pass."""
+    c = _ffn_call("ffn_forward", ffn)
+    T, H = x.shape[0], ffn.H
+    mx = ffn.desc.format == MOE4_FFN_MXFP8
+    pw, nw = c.ws(ws)
+    _check(_lib.moe4_ffn_forward(
+        ffn.ref, c.ptr(x, "x", (T, H), _CODES if mx else _BF16),
+        c.ptr(x_s, "x_s", (T, H // 32), _SCALES), T,
+        c.ptr(residual, "residual", (T, H), _FLOATS), _dt(residual),
+        c.ptr(out, "out", (T, H), _FLOATS), _dt(out),
+        c.ptr(save_gu, "save_gu", (T, 2 * ffn.I), _F32), pw, nw, c.stream(stream)))
+
+
+def moe4_ffn_backward(ffn, x, save_gu, dy, dx=None, dx_add=None, dw_gu=None, dw_dn=None,
+                      db_gu=None, db_dn=None, ws=None, stream=None):
+    """Gradients of moe4_ffn_forward (bf16 blocks) from dy bf16 [T, H]: dx (bf16 or f32; dx_add is
+    added), dw_gu, dw_dn, db_gu, db_dn (one dtype, bf16 or f32); each may be None."""
+    c = _ffn_call("ffn_backward", ffn)
+    T, H, I = dy.shape[0], ffn.H, ffn.I
+    given = [t for t in (dw_gu, dw_dn, db_gu, db_dn) if t is not None]
+    if any(t.dtype != given[0].dtype for t in given):
+        raise TypeError("the weights' and biases' gradients must have one dtype")
+    pw, nw = c.ws(ws)
+    _check(_lib.moe4_ffn_backward(
+        ffn.ref, c.ptr(x, "x", (T, H), _BF16), T, c.ptr(save_gu, "save_gu", (T, 2 * I), _F32),
+        c.ptr(dy, "dy", (T, H), _BF16), c.ptr(dx_add, "dx_add", (T, H), _FLOATS), _dt(dx_add),
+        c.ptr(dx, "dx", (T, H), _FLOATS), _dt(dx), c.ptr(dw_gu, "dw_gu", (2 * I, H), _FLOATS),
+        c.ptr(dw_dn, "dw_dn", (H, I), _FLOATS), c.ptr(db_gu, "db_gu", (2 * I,), _FLOATS),
+        c.ptr(db_dn, "db_dn", (H,), _FLOATS), _dt(given[0]) if given else 0, pw, nw,
+        c.stream(stream)))
+
+
+class GradList:
+    """Owns references to a list of gradients (bf16 or f32, any shapes) and the host arrays that
+    moe4_grad_norm and moe4_clip_grads read. outs: where moe4_clip_grads writes (same shapes and
+    dtypes), None for in place. Build it anew when a gradient is another tensor."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        n = self.n = len(self.grads)
+        if self.outs is not None and len(self.outs) != n:
+            raise ValueError("GradList: outs and grads differ in length")
+        c = _Call("GradList")
+        self._in, self._numel = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+        self._dtype = (ctypes.c_int32 * n)()
+        self._out = None if outs is None else (ctypes.c_void_p * n)()
+        for i, g in enumerate(self.grads):
+            self._in[i] = c.ptr(g, f"grads[{i}]", tuple(g.shape), _FLOATS)
+            self._numel[i], self._dtype[i] = g.numel(), _dt(g)
+            if self.outs is not None:
+                self._out[i] = c.ptr(self.outs[i], f"outs[{i}]", tuple(g.shape), (g.dtype,))
+
+
+def moe4_grad_workspace_size(grads):
+    n = _lib.moe4_grad_workspace_size(grads.n)
+    if n == 0:
+        raise Moe4Error(MOE4_ESHAPE, moe4_last_error())
+    return n
+
+
+def _grad_call(fn, grads):
+    c = _Call(fn)
+    if grads.n:
+        c.place(grads.grads[0], "grads[0]")
+    return c
+
+
+def moe4_grad_norm(grads, norm, ws, stream=None):
+    """norm f32 [1]: the global norm of a GradList."""
+    c = _grad_call("grad_norm", grads)
+    pw, nw = c.ws(ws)
+    _check(_lib.moe4_grad_norm(grads._in, grads._numel, grads._dtype, grads.n,
+                               c.ptr(norm, "norm", (1,), _F32), pw, nw, c.stream(stream)))
+
+
+def moe4_clip_grads(grads, max_norm, norm_out=None, ws=None, norm_in=None, stream=None):
+    """Scales a GradList by min(1, max_norm / (norm + 1e-6)); the norm is norm_in where given,
+    else the list's own; norm_out f32 [1] takes the norm used."""
+    c = _grad_call("clip_grads", grads)
+    pw, nw = c.ws(ws)
+    _check(_lib.moe4_clip_grads(grads._in, grads._out, grads._numel, grads._dtype, grads.n,
+                                max_norm, c.ptr(norm_in, "norm_in", (1,), _F32),
+                                c.ptr(norm_out, "norm_out", (1,), _F32), pw, nw,
+                                c.stream(stream)))

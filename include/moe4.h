@@ -411,6 +411,179 @@ int moe4_expert_backward(const moe4_experts* ex, const uint16_t* x_perm, const i
                          const uint16_t* dy_perm, float* dx_perm, float* dA, float* dB,
                          void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The dense half of a mixture-of-experts block, next to the routed experts:
+ * the norm in front of the router, the feed-forward block that every token
+ * passes (a shared expert), the 8-bit form of both, and the clipping of the
+ * adapters' gradients. Activations are bf16; a tensor whose type is an
+ * argument is bf16 or fp32 (MOE4_DTYPE_*, no default). Sizes are in elements.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Residual addition and root-mean-square norm:
+ *   s = x + residual, rounded to the residual's type (s = x without one)
+ *   rstd[t] = 1 / sqrt(mean_h s[t, h]^2 + eps)            (fp32 sums)
+ *   y[t, h] = s[t, h] * rstd[t] * weight[h]
+ * The row that is normalised is the rounded one, which sum_out holds for the
+ * next layer and for the backward pass. y is written as bf16 (out), as MXFP8
+ * (out_q and out_s, see moe4_quantize_mxfp8, each value rounded once from
+ * fp32), or both. Squares are summed in fp32: a row whose sum of squares
+ * passes fp32's range gives rstd 0.
+ *   x [T, H] of x_dtype; residual [T, H] of res_dtype or NULL; weight [H] of
+ *   w_dtype; eps >= 0; 8 <= H <= 16384, a multiple of 8 (32 with out_q)
+ *   sum_out [T, H] of res_dtype or NULL (needs residual; may be the residual
+ *   itself, or x where its type is the same)
+ *   out bf16 [T, H] or NULL; out_q u8 [T, H] and out_s u8 [T, H/32], both or
+ *   neither; rstd f32 [T] or NULL; at least one of out and out_q
+ *   x, residual, sum_out, weight, out, out_q 16-byte aligned
+ */
+int moe4_add_rmsnorm(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype,
+                     void* sum_out, const void* weight, int32_t w_dtype, int32_t T, int32_t H,
+                     float eps, uint16_t* out, uint8_t* out_q, uint8_t* out_s, float* rstd,
+                     void* stream);
+
+/*
+ * Its backward pass. With n = s * rstd and p = weight * dy:
+ *   dx[t, h] = rstd[t] * (p - n * mean_h(p * n)) (+ dres[t, h])
+ *   dweight[h] = sum_t dy[t, h] * n[t, h]      (fp32, in a fixed order)
+ * dx is the gradient of x and of the residual alike; dres is the gradient that
+ * reaches s past the norm (the stream's own), of dx's type.
+ *   dy [T, H] of dy_dtype; s [T, H] of s_dtype (sum_out of the forward, or x);
+ *   weight [H] of w_dtype; rstd f32 [T] from the forward; dres [T, H] of
+ *   dx_dtype or NULL; dx [T, H] out of dx_dtype (may be dres, or dy or s where
+ *   the type is the same); dweight f32 [H] out or NULL
+ *   ws: at least moe4_add_rmsnorm_workspace_size bytes (256-byte aligned) with
+ *   dweight, else unused; all tensors but rstd 16-byte aligned
+ */
+int moe4_add_rmsnorm_backward(const void* dy, int32_t dy_dtype, const void* s, int32_t s_dtype,
+                              const void* weight, int32_t w_dtype, const float* rstd,
+                              const void* dres, int32_t T, int32_t H, void* dx, int32_t dx_dtype,
+                              float* dweight, void* ws, size_t ws_bytes, void* stream);
+/* 0 if T or H is invalid */
+size_t moe4_add_rmsnorm_workspace_size(int32_t T, int32_t H);
+
+/*
+ * MXFP8 quantisation of rows of bf16 or fp32: e4m3 codes in blocks of 32 along
+ * the row, one e8m0 scale (the power of two 2^(byte - 127)) per block. The
+ * scale is the smallest power of two, from 2^-127 on, that brings the block's
+ * largest magnitude to at most 448, so no code saturates; codes are value /
+ * scale rounded to nearest even. A block that holds an infinity or a NaN takes
+ * scale byte 255 (NaN) and codes 0x7F (NaN).
+ *   x [R, K] of x_dtype (16-byte aligned); K % 32 == 0
+ *   q u8 [R, K] out (16-byte aligned), s u8 [R, K/32] out
+ */
+int moe4_quantize_mxfp8(const void* x, int32_t x_dtype, int64_t R, int64_t K, uint8_t* q,
+                        uint8_t* s, void* stream);
+
+/* weight format of a dense feed-forward block (no default) */
+enum { MOE4_FFN_BF16 = 1, MOE4_FFN_MXFP8 = 2 };
+
+/*
+ * A dense gated feed-forward block: gate and up projections fused as in
+ * moe4_experts (gu_layout, act, act_alpha, act_limit as there), then the down
+ * projection. Row n of a weight is output feature n.
+ *   BF16:  w_gu bf16 [2I, H], w_dn bf16 [H, I]; gu_s, dn_s NULL
+ *   MXFP8: w_gu u8 [2I, H], gu_s u8 [2I, H/32], w_dn u8 [H, I], dn_s u8
+ *          [H, I/32] (moe4_quantize_mxfp8's codes and scales)
+ *   gu_bias bf16 [2I], dn_bias bf16 [H]: each optional
+ *   variant: MOE4_VARIANT_*; AUTO picks by the number of tokens
+ * Bounds (else MOE4_ESHAPE): H and I positive multiples of 8 (BF16) or 32
+ * (MXFP8); a weight and 256 rows of activations under 2^31 - 2^24 bytes.
+ * All pointers 16-byte aligned (the scales 4).
+ */
+typedef struct moe4_ffn {
+  int32_t format;
+  int32_t H, I;
+  int32_t gu_layout;
+  int32_t act;
+  float act_alpha, act_limit;
+  int32_t variant;
+  const void* w_gu;
+  const uint8_t* gu_s;
+  const void* w_dn;
+  const uint8_t* dn_s;
+  const uint16_t* gu_bias;
+  const uint16_t* dn_bias;
+} moe4_ffn;
+
+/*
+ * Forward:
+ *   gu = x W_gu^T + b_gu;  h = act(gate, up);  out = h W_dn^T + b_dn + residual
+ * Products are summed in fp32 on the matrix cores. h, the second product's
+ * operand, is rounded once to bf16 (BF16) or quantised to MXFP8 (MXFP8); out is
+ * rounded once, after the residual's addition. A NaN pre-activation stays one.
+ *   x [T, H]: bf16, x_s NULL (BF16); u8 codes with x_s u8 [T, H/32] (MXFP8)
+ *   residual [T, H] of res_dtype or NULL; out [T, H] of out_dtype (may be the
+ *   residual where the types are the same)
+ *   save_gu f32 [T, 2I] or NULL: the pre-activations, in the rows' layout, for
+ *   the backward pass
+ *   ws: at least moe4_ffn_workspace_size(f, T, 0) bytes (256-byte aligned)
+ *   x, residual, out, save_gu 16-byte aligned (x_s 4)
+ */
+int moe4_ffn_forward(const moe4_ffn* f, const void* x, const uint8_t* x_s, int32_t T,
+                     const void* residual, int32_t res_dtype, void* out, int32_t out_dtype,
+                     float* save_gu, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward (BF16 blocks; MXFP8 is refused with MOE4_EUNSUPPORTED):
+ *   dH = dY W_dn;  dGU = act'(gu) * dH;  dx = dGU W_gu (+ dx_add)
+ *   dw_dn = dY^T h;  dw_gu = dGU^T x;  db_dn = sum_t dY;  db_gu = sum_t dGU
+ * with h recomputed from save_gu. dGU and h are rounded once to bf16, the
+ * operand type of the products that read them; every sum is fp32, in a fixed
+ * order. Any output may be NULL and is then not computed.
+ *   x bf16 [T, H] (needed for dw_gu); save_gu f32 [T, 2I]; dy bf16 [T, H]
+ *   dx [T, H] of dx_dtype; dx_add [T, H] of add_dtype or NULL: a gradient of x
+ *   from elsewhere (the routed experts'), added in fp32 (may be dx where the
+ *   types are the same)
+ *   dw_gu [2I, H], dw_dn [H, I], db_gu [2I], db_dn [H]: of dw_dtype (needed
+ *   where one of them is given); written, not accumulated; zeros for T = 0
+ *   ws: at least moe4_ffn_workspace_size(f, T, 1) bytes (256-byte aligned)
+ *   all tensors 16-byte aligned
+ */
+int moe4_ffn_backward(const moe4_ffn* f, const uint16_t* x, int32_t T, const float* save_gu,
+                      const uint16_t* dy, const void* dx_add, int32_t add_dtype, void* dx,
+                      int32_t dx_dtype, void* dw_gu, void* dw_dn, void* db_gu, void* db_dn,
+                      int32_t dw_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe4_ffn_forward (backward == 0) or moe4_ffn_backward at T
+ * tokens; 0 if the descriptor or T is invalid. */
+size_t moe4_ffn_workspace_size(const moe4_ffn* f, int32_t T, int32_t backward);
+
+/*
+ * Global norm of a list of gradients: norm[0] = sqrt(sum_i sum_e g_i[e]^2) as
+ * fp32, the squares summed in fp64 in a fixed order (right for any finite
+ * gradients, however large or small).
+ *   grads, numel, dtype: host arrays of n entries, read during the call:
+ *   device pointers (16-byte aligned; NULL where numel is 0), elements (0 <=
+ *   numel <= 2^36), MOE4_DTYPE_*; 0 <= n <= 2^20
+ *   norm f32 [1] out (device)
+ *   ws: at least moe4_grad_workspace_size(n) bytes (256-byte aligned)
+ */
+int moe4_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                   int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Clipping by the global norm: outs[i] = grads[i] * min(1, max_norm / (norm +
+ * 1e-6)), rounded once to the gradient's type. Where the norm is an infinity
+ * or a NaN the gradients pass unchanged: the caller reads the norm and drops
+ * the step.
+ *   grads, numel, dtype, n, ws as moe4_grad_norm
+ *   outs: host array of n device pointers (16-byte aligned; outs[i] may be
+ *   grads[i]), or NULL for all in place
+ *   max_norm: positive
+ *   norm_in f32 [1] (device) or NULL: the norm to clip by, where it spans more
+ *   than this list (other ranks' shards); NULL computes it here
+ *   norm_out f32 [1] (device) or NULL: the norm used
+ *   ws may be NULL with norm_in
+ */
+int moe4_clip_grads(const void* const* grads, void* const* outs, const int64_t* numel,
+                    const int32_t* dtype, int32_t n, float max_norm, const float* norm_in,
+                    float* norm_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe4_grad_norm and moe4_clip_grads for a list of n
+ * gradients; 0 if n is invalid. */
+size_t moe4_grad_workspace_size(int32_t n);
+
 /*
  * Optional launch timing, for measurement. After this call the calling
  * thread's moe4_expert_forward records events[0] / events[1] (hipEvent_t
@@ -431,8 +604,8 @@ size_t moe4_workspace_size(const moe4_experts* ex, int32_t T, int32_t k);
 /* Message of the calling thread's last failure ("" after success). */
 const char* moe4_last_error(void);
 
-/* Kernel family of the calling thread's last moe4_expert_forward or
- * moe4_expert_backward: MOE4_VARIANT_SKINNY or MOE4_VARIANT_TILED (0 if none
+/* Kernel family of the calling thread's last moe4_expert_forward,
+ * moe4_expert_backward or moe4_ffn_forward: MOE4_VARIANT_SKINNY or MOE4_VARIANT_TILED (0 if none
  * ran), so callers can assert which kernel engaged. */
 int moe4_last_variant(void);
 
