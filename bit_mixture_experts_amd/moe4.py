@@ -411,41 +411,50 @@ def _dt(t):
 
 
 class _Call:
-    """Pointers of one call's tensors: shape, dtype, contiguity and device checked."""
+    """Pointers of one call's tensors: shape, dtype, contiguity and device checked. A decode
+    step's kernels are a few microseconds long, so the way without an error is kept short."""
+    __slots__ = ("fn", "dev")
 
     def __init__(self, fn):
         self.fn = fn
-        self.dev = None
+        self.dev = -2   # none yet (a CPU tensor's is -1)
 
     def ptr(self, t, name, shape, dtypes):
         if t is None:
             return None
-        p = _ptr(t, dtypes, name)
-        if tuple(t.shape) != shape:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.get_device() != self.dev:
+            self.place(t, name)
+        if t.dtype not in dtypes or not t.is_contiguous():
+            _ptr(t, dtypes, name)
+        if t.shape != shape:
             raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
-        self.place(t, name)
-        return p
+        return t.data_ptr()
 
     def place(self, t, name):
+        if not t.is_cuda:
+            raise TypeError(f"{name} must live on the GPU")
         d = t.get_device()
-        if self.dev is None:
-            self.dev = d
-            if d != torch.cuda.current_device():
-                raise ValueError(f"{self.fn}: {name} is on device {d}, the current device is "
-                                 f"{torch.cuda.current_device()}")
-        elif d != self.dev:
+        if self.dev >= 0 and d != self.dev:
             raise ValueError(f"{self.fn}: {name} is on device {d}, other tensors on {self.dev}")
+        if d != torch.cuda.current_device():
+            raise ValueError(f"{self.fn}: {name} is on device {d}, the current device is "
+                             f"{torch.cuda.current_device()}")
+        self.dev = d
 
     def ws(self, ws):
         if ws is None:
             return None, 0
-        p = _ptr(ws, None, "ws")
-        self.place(ws, "ws")
-        return p, ws.numel() * ws.element_size()
+        if ws.get_device() != self.dev:
+            self.place(ws, "ws")
+        return _ptr(ws, None, "ws"), ws.numel() * ws.element_size()
 
     def stream(self, stream):
-        d = getattr(stream, "device_index", None)
-        if d is not None and self.dev is not None and d != self.dev:
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(max(self.dev, 0))
+        d = getattr(stream, "device_index", self.dev)
+        if d != self.dev:
             raise ValueError(f"{self.fn}: the stream is on device {d}, the tensors on {self.dev}")
         return _stream(stream)
 
@@ -456,7 +465,7 @@ def moe4_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, out_
     (out) and, or, MXFP8 (out_q u8 or float8_e4m3fn [T, H], out_s u8 or float8_e8m0fnu [T, H/32]).
     x, residual bf16 or f32 [T, H]; weight bf16 or f32 [H]; rstd f32 [T]."""
     c = _Call("add_rmsnorm")
-    T, H = sh = tuple(x.shape)
+    T, H = sh = x.shape
     if sum_out is not None and residual is not None and sum_out.dtype != residual.dtype:
         raise TypeError("sum_out must have the residual's dtype")
     px = c.ptr(x, "x", sh, _FLOATS)
@@ -480,7 +489,7 @@ def moe4_add_rmsnorm_backward(dy, s, weight, rstd, dx, dres=None, dweight=None, 
     """Gradient of moe4_add_rmsnorm: dx (of x and of the residual alike; dres, of dx's dtype, is
     added) and dweight f32 [H]. s: the forward's sum_out (its x without a residual)."""
     c = _Call("add_rmsnorm_backward")
-    T, H = sh = tuple(s.shape)
+    T, H = sh = s.shape
     if dres is not None and dres.dtype != dx.dtype:
         raise TypeError("dres must have dx's dtype")
     ps = c.ptr(s, "s", sh, _FLOATS)
