@@ -375,19 +375,32 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
   wait_vmcnt<0>();   // the zeros of the tiles past the last, before the stages are used again
 }
 
-// Epilogue: hands every value of the tile to f(b, a, v) as 8 consecutive a of one row b in one
-// lane (PAIR: 8 gate and 8 up values whose MFMA tiles are neighbours, f(b, j, g, u) with j the
-// pair's place in the tile), in an order that makes a wave's stores whole row segments.
+// Epilogue: hands every value of the tile to f(b, a, v, pre) as 8 consecutive a of one row b in
+// one lane (PAIR: 8 gate and 8 up values whose MFMA tiles are neighbours, f(b, j, g, u) with j
+// the pair's place in the tile), in an order that makes a wave's stores whole row segments.
 // Through LDS, 32 rows b of the wave at a time as fp32 [32][TA * 32]: the 16-byte chunk c of
 // row b sits at c ^ (b & 15), which spreads the 16 rows of a write over the banks.
-template <typename S, bool PAIR, typename F>
-__device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uint8_t* lds, F f) {
+// load(b, a) gives pre, what f reads from memory for the same values: it is asked for two
+// turns ahead of f, so that its latency hides behind the turns between.
+template <typename S, bool PAIR, typename L, typename F>
+__device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uint8_t* lds, L load,
+                                          F f) {
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
   const int wa = w % S::WA, wb = w / S::WA, l = lane_id();
   constexpr int W = S::TA * 32;              // fp32 values of a row
   constexpr int kKey = W / 4 >= 16 ? 15 : W / 4 - 1;
   static_assert(S::kWaves * 32 * W * 4 <= S::kLds, "staging fits the stages");
+  constexpr int kPer = PAIR ? W / 16 : W / 8;   // lanes of a row
+  constexpr int kRows = 64 / kPer, kTurns = 32 / kRows, kAll = kTurns * S::TB;
   uint8_t* st = lds + w * 32 * W * 4;
+  const int c = l % kPer;
+  // turn n = (u, i): the tile's row of the lane, and its first a (PAIR: its first pair)
+  auto row_at = [&](int n) { return wb * S::TB * 32 + n * kRows + l / kPer; };
+  const int a_at = PAIR ? wa * (W / 2) + 32 * (c / 4) + 8 * (c % 4) : wa * W + 8 * c;
+  using Pre = decltype(load(0, 0));
+  Pre pre[2];
+  pre[0] = load(row_at(0), a_at);
+  pre[1] = load(row_at(1), a_at);
   lds_barrier();   // every wave is done with the k loop's stages
 #pragma unroll
   for (int u = 0; u < S::TB; ++u) {
@@ -398,8 +411,8 @@ __device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uin
       for (int q = 0; q < 4; ++q) {
         const f32x4 v = {acc[t][u][4 * q], acc[t][u][4 * q + 1], acc[t][u][4 * q + 2],
                          acc[t][u][4 * q + 3]};
-        const int c = 8 * t + 2 * q + (l >> 5);
-        *reinterpret_cast<f32x4*>(st + b * W * 4 + ((c ^ (b & kKey)) * 16)) = v;
+        const int ch = 8 * t + 2 * q + (l >> 5);
+        *reinterpret_cast<f32x4*>(st + b * W * 4 + ((ch ^ (b & kKey)) * 16)) = v;
       }
     wait_lgkm0();
     asm volatile("" ::: "memory");
@@ -412,27 +425,28 @@ __device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uin
         for (int i = 0; i < 4; ++i) v[4 * h + i] = x[i];
       }
     };
-    constexpr int kPer = PAIR ? W / 16 : W / 8;   // lanes of a row
-    constexpr int kRows = 64 / kPer;
 #pragma unroll
-    for (int i = 0; i < 32 / kRows; ++i) {
-      const int bb = i * kRows + l / kPer, c = l % kPer;
-      const int row = (wb * S::TB + u) * 32 + bb;
+    for (int i = 0; i < kTurns; ++i) {
+      const int n = u * kTurns + i, bb = i * kRows + l / kPer;
+      const Pre mine = pre[n & 1];
+      if (n + 2 < kAll) pre[n & 1] = load(row_at(n + 2), a_at);
       if constexpr (PAIR) {
         const int p = c / 4, j = 8 * (c % 4);   // pair group (two MFMA tiles), place in it
         float g[8], uu[8];
         get(bb, 64 * p + j, g);
         get(bb, 64 * p + 32 + j, uu);
-        f(row, wa * (W / 2) + 32 * p + j, g, uu);
+        f(row_at(n), a_at, g, uu);
       } else {
         float v[8];
         get(bb, 8 * c, v);
-        f(row, wa * W + 8 * c, v);
+        f(row_at(n), a_at, v, mine);
       }
     }
     wait_lgkm0();
     asm volatile("" ::: "memory");
   }
 }
+
+struct NoPre {};
 
 }  // namespace moe4

@@ -83,6 +83,11 @@ __device__ __forceinline__ void store8_dt(void* p, int dtype, int64_t i, const f
   else *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = pack8_bf16(v);
 }
 
+// 8 values as they lie in memory (bf16: the first half)
+struct Raw16 {
+  u32x4 v[2];
+};
+
 // One product of the block and what its epilogue does: out[b][a] = sum_k A B (+ bias[a]) (+
 // add[b][a]), a < na, b < nb.
 struct FfnProduct {
@@ -121,24 +126,41 @@ __device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, in
   gemm_loop<S, MA, MB, FP8>(
       acc, lds, la, lb, p.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
       [&](int r) { return b0 + r < p.nb ? b0 + r : -1; });
-  for_each8<S, false>(acc, lds, [&](int row, int a, float* v) {
-    const int b = b0 + row, c = a0 + a;
-    if (b >= p.nb || c >= p.na) return;
-    const int64_t at = (int64_t)b * p.na + c;
-    if (p.bias) {
-      float x[8];
-      load8_bf16(p.bias + c, x);
+  const bool add32 = p.add_dtype == MOE4_DTYPE_F32;
+  for_each8<S, false>(
+      acc, lds,
+      [&](int row, int a) {
+        Raw16 r;
+        const int b = b0 + row, c = a0 + a;
+        if (p.add && b < p.nb && c < p.na) {
+          const int64_t at = (int64_t)b * p.na + c;
+          if (add32) {
+            const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(p.add) + at);
+            r.v[0] = q[0];
+            r.v[1] = q[1];
+          } else {
+            r.v[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.add) + at);
+          }
+        }
+        return r;
+      },
+      [&](int row, int a, float* v, const Raw16& r) {
+        const int b = b0 + row, c = a0 + a;
+        if (b >= p.nb || c >= p.na) return;
+        if (p.bias) {
+          float x[8];
+          load8_bf16(p.bias + c, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += x[i];
-    }
-    if (p.add) {
-      float x[8];
-      load8_dt(p.add, p.add_dtype, at, x);
+          for (int i = 0; i < 8; ++i) v[i] += x[i];
+        }
+        if (p.add) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += x[i];
-    }
-    store8_dt(p.out, p.out_dtype, at, v);
-  });
+          for (int i = 0; i < 8; ++i)
+            v[i] += add32 ? __uint_as_float(r.v[i / 4][i % 4])
+                          : (i & 1 ? bf16hi(r.v[0][i / 2]) : bf16lo(r.v[0][i / 2]));
+        }
+        store8_dt(p.out, p.out_dtype, (int64_t)b * p.na + c, v);
+      });
 }
 
 template <typename S, int MA, int MB, bool FP8>
@@ -148,6 +170,17 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_product(const FfnProduct
   int ia, ib;
   tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
   ffn_product_tile<S, MA, MB, FP8>(p, ia, ib, stage_mem);
+}
+
+// f(layout, activation) as compile-time constants
+template <typename F>
+inline hipError_t with_kind(int layout, int act, F f) {
+  using H = std::integral_constant<int, MOE4_GU_HALVES>;
+  using N = std::integral_constant<int, MOE4_GU_INTERLEAVED>;
+  using S = std::integral_constant<int, MOE4_ACT_SWIGLU>;
+  using C = std::integral_constant<int, MOE4_ACT_SWIGLU_CLAMPED>;
+  if (layout == MOE4_GU_HALVES) return act == MOE4_ACT_SWIGLU ? f(H{}, S{}) : f(H{}, C{});
+  return act == MOE4_ACT_SWIGLU ? f(N{}, S{}) : f(N{}, C{});
 }
 
 // dynamic LDS above 64 KiB has to be asked for once per kernel and device

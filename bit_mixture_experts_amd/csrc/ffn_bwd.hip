@@ -10,14 +10,21 @@ namespace {
 
 struct DhArgs {
   Operand W, dY;
-  int T, H, I, layout;
+  int T, H, I;
   FfnAct act;
   const float* gu;      // [T, 2I]
   uint16_t* dgu;        // [T, 2I]
   uint16_t* h;          // [T, I] or null (no gradient of W_dn wanted)
+  float* part;          // [row tiles][2I] column sums of dGU, or null
 };
 
-template <typename S>
+// the saved pre-activations of 8 pairs: gate and up (halves), or pairs in turn (interleaved)
+struct RawGu {
+  u32x4 v[4];
+};
+
+// LAYOUT, ACT: the block's (their branches would double the epilogue's code four times over)
+template <typename S, int LAYOUT, int ACT>
 __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
   const int na = (a.I + S::BA - 1) / S::BA, nb = (a.T + S::BB - 1) / S::BB;
@@ -31,30 +38,121 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
   f32x16 acc[S::TA][S::TB];
   gemm_loop<S, kOpCol, kOpRow, false>(
       acc, stage_mem, la, lb, a.H, MxState<false>{}, [](int) { return -1; }, [](int) { return -1; });
-  for_each8<S, false>(acc, stage_mem, [&](int row, int jj, float* dh) {
-    const int t = t0 + row, j = j0 + jj;
-    if (row >= nt || j >= a.I) return;
-    const int64_t base = (int64_t)t * 2 * a.I;
-    float g[8], u[8], h[8], d[16];
-    if (a.layout == MOE4_GU_HALVES) {
-      load8_f32(a.gu + base + j, g);
-      load8_f32(a.gu + base + a.I + j, u);
+  constexpr bool halves = LAYOUT == MOE4_GU_HALVES;
+  const FfnAct act = {ACT, a.act.alpha, a.act.limit};
+  // where the lane's two runs of 8 pre-activations start in a row
+  auto col0 = [&](int j) { return halves ? j : 2 * j; };
+  auto col1 = [&](int j) { return halves ? a.I + j : 2 * j + 8; };
+  float sums[16] = {};   // of dGU over the lane's rows, in fp32 before the rounding
+  for_each8<S, false>(
+      acc, stage_mem,
+      [&](int row, int jj) {
+        RawGu r;
+        const int j = j0 + jj;
+        if (row < nt && j < a.I) {
+          const float* p = a.gu + (int64_t)(t0 + row) * 2 * a.I;
+          const u32x4* q = reinterpret_cast<const u32x4*>(p + col0(j));
+          const u32x4* s = reinterpret_cast<const u32x4*>(p + col1(j));
+          r.v[0] = q[0];
+          r.v[1] = q[1];
+          r.v[2] = s[0];
+          r.v[3] = s[1];
+        }
+        return r;
+      },
+      [&](int row, int jj, float* dh, const RawGu& r) {
+        const int j = j0 + jj;
+        if (row >= nt || j >= a.I) return;
+        const int64_t t = t0 + row;
+        float x[16], h[8], d[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a.act.backward(g[i], u[i], dh[i], h[i], d[i], d[8 + i]);
-      *reinterpret_cast<u32x4*>(a.dgu + base + j) = pack8_bf16(d);
-      *reinterpret_cast<u32x4*>(a.dgu + base + a.I + j) = pack8_bf16(d + 8);
-    } else {
-      float x[16];
-      load8_f32(a.gu + base + 2 * j, x);
-      load8_f32(a.gu + base + 2 * j + 8, x + 8);
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r.v[i / 4][i % 4]);
+        if (halves) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        a.act.backward(x[2 * i], x[2 * i + 1], dh[i], h[i], d[2 * i], d[2 * i + 1]);
-      *reinterpret_cast<u32x4*>(a.dgu + base + 2 * j) = pack8_bf16(d);
-      *reinterpret_cast<u32x4*>(a.dgu + base + 2 * j + 8) = pack8_bf16(d + 8);
-    }
-    if (a.h) *reinterpret_cast<u32x4*>(a.h + (int64_t)t * a.I + j) = pack8_bf16(h);
-  });
+          for (int i = 0; i < 8; ++i) act.backward(x[i], x[8 + i], dh[i], h[i], d[i], d[8 + i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            act.backward(x[2 * i], x[2 * i + 1], dh[i], h[i], d[2 * i], d[2 * i + 1]);
+        }
+        uint16_t* o = a.dgu + t * 2 * a.I;
+        *reinterpret_cast<u32x4*>(o + col0(j)) = pack8_bf16(d);
+        *reinterpret_cast<u32x4*>(o + col1(j)) = pack8_bf16(d + 8);
+        if (a.h) *reinterpret_cast<u32x4*>(a.h + t * a.I + j) = pack8_bf16(h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[i] += d[i];
+      });
+  if (!a.part) return;
+  // the lane's sums, over the wave's rows (lanes of the same columns), then over its WB waves in
+  // order through LDS
+  constexpr int W = S::TA * 32, kPer = W / 8;
+  const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+  const int wa = w % S::WA, wb = w / S::WA;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int m = kPer; m < 64; m <<= 1) sums[i] += __shfl_xor(sums[i], m, kWave);
+  f32x4* red = reinterpret_cast<f32x4*>(stage_mem);   // [wb][wa][kPer][4]
+  __syncthreads();
+  if (l < kPer) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      red[((wb * S::WA + wa) * kPer + l) * 4 + i] =
+          f32x4{sums[4 * i], sums[4 * i + 1], sums[4 * i + 2], sums[4 * i + 3]};
+  }
+  __syncthreads();
+  if (wb != 0 || l >= kPer) return;
+  const int j = j0 + wa * W + 8 * l;
+  if (j >= a.I) return;
+  float* o = a.part + (int64_t)ib * 2 * a.I;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f32x4 s = red[(wa * kPer + l) * 4 + i];
+#pragma unroll
+    for (int v = 1; v < S::WB; ++v) s += red[((v * S::WA + wa) * kPer + l) * 4 + i];
+    *reinterpret_cast<f32x4*>(o + (i < 2 ? col0(j) + 4 * i : col1(j) + 4 * (i - 2))) = s;
+  }
+}
+
+// The products that follow dGU, in one launch: their tiles are dealt product by product,
+// longest reduction first, so that the chip is full until the last of them (one launch each
+// left most CUs idle in its last round). Each product's run of workgroups starts at a
+// multiple of 8 (an XCD each): ids past a product's tiles have nothing to do.
+struct GradArgs {
+  FfnProduct p[3];
+  int first[4];     // first workgroup of each, and the end
+  int col_b[3];     // whether B is a col operand (a weight's gradient) or a row one (dX)
+};
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, 2) void k_ffn_grads(const GradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
+  const int q = (int)blockIdx.x < a.first[1] ? 0 : (int)blockIdx.x < a.first[2] ? 1 : 2;
+  const FfnProduct& p = a.p[q];
+  const int na = (p.na + S::BA - 1) / S::BA, nb = (p.nb + S::BB - 1) / S::BB;
+  const int id = blockIdx.x - a.first[q];
+  if (id >= na * nb) return;
+  int ia, ib;
+  tile_of(xcd_remap(id, na * nb), na, nb, ia, ib);
+  if (a.col_b[q]) ffn_product_tile<S, kOpCol, kOpCol, false>(p, ia, ib, stage_mem);
+  else ffn_product_tile<S, kOpCol, kOpRow, false>(p, ia, ib, stage_mem);
+}
+
+template <typename S>
+int64_t tiles_of(const FfnProduct& p) {
+  return (int64_t)((p.na + S::BA - 1) / S::BA) * ((p.nb + S::BB - 1) / S::BB);
+}
+
+template <typename S>
+hipError_t launch_grads(GradArgs a, int n, hipStream_t s) {
+  auto* k = &k_ffn_grads<S>;
+  hipError_t e = allow_lds(k, S::kLds);
+  if (e != hipSuccess) return e;
+  a.first[0] = 0;
+  for (int i = 0; i < 3; ++i)
+    a.first[i + 1] = a.first[i] + (i < n ? (int)((tiles_of<S>(a.p[i]) + 7) / 8 * 8) : 0);
+  k<<<a.first[3], S::kThreads, S::kLds, s>>>(a);
+  return hipGetLastError();
 }
 
 // Column sums of a bf16 matrix [T, N]: part p of P sums its rows in fp32 into part[p][N].
@@ -64,6 +162,7 @@ __global__ __launch_bounds__(256) void k_col_sums(const uint16_t* m, int T, int 
   const int r0 = (int)((int64_t)T * blockIdx.y / gridDim.y);
   const int r1 = (int)((int64_t)T * (blockIdx.y + 1) / gridDim.y);
   float s[8] = {};
+#pragma unroll 8
   for (int r = r0; r < r1; ++r) {
     float v[8];
     load8_bf16(m + (int64_t)r * N + c, v);
@@ -84,16 +183,9 @@ hipError_t col_sums(const uint16_t* m, int T, int N, float* part, void* out, int
   return e != hipSuccess ? e : launch_sum_rows(part, P, N, out, dtype, s);
 }
 
-template <int MA, int MB>
-hipError_t product(const FfnProduct& p, hipStream_t s) {
-  const int64_t big = (int64_t)((p.na + 255) / 256) * ((p.nb + 255) / 256);
-  return big >= 192 ? launch_product<Tile256, MA, MB, false>(p, s)
-                    : launch_product<Tile128, MA, MB, false>(p, s);
-}
-
-template <typename S>
+template <typename S, int LAYOUT, int ACT>
 hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
-  auto* k = &k_ffn_dh<S>;
+  auto* k = &k_ffn_dh<S, LAYOUT, ACT>;
   hipError_t e = allow_lds(k, S::kLds);
   if (e != hipSuccess) return e;
   const int64_t n = (int64_t)((a.I + S::BA - 1) / S::BA) * ((a.T + S::BB - 1) / S::BB);
@@ -103,53 +195,75 @@ hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t ffn_backward_ws_bytes(const moe4_ffn& f, int64_t T) {
-  const int n = 2 * f.I > f.H ? 2 * f.I : f.H;
-  return align_up((size_t)T * 2 * f.I * 2, 256) + align_up((size_t)T * f.I * 2, 256) +
-         align_up((size_t)kColParts * n * 4, 256);
-}
+// workspace: dGU, h, the partial sums of the two biases' gradients
+struct BwdWs {
+  size_t h, part_gu, part_dn, end;
+  BwdWs(const moe4_ffn& f, int64_t T) {
+    h = align_up((size_t)T * 2 * f.I * 2, 256);
+    part_gu = h + align_up((size_t)T * f.I * 2, 256);
+    part_dn = part_gu + align_up((size_t)((T + 127) / 128) * 2 * f.I * 4, 256);
+    end = part_dn + align_up((size_t)kColParts * f.H * 4, 256);
+  }
+};
+
+size_t ffn_backward_ws_bytes(const moe4_ffn& f, int64_t T) { return BwdWs(f, T).end; }
 
 hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, const float* gu,
                                const uint16_t* dy, const void* add, int add_dtype, void* dx,
                                int dx_dtype, void* dw_gu, void* dw_dn, void* db_gu, void* db_dn,
                                int dw_dtype, void* ws, hipStream_t s) {
   const int H = f.H, I = f.I;
+  const BwdWs at(f, T);
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   uint16_t* dgu = reinterpret_cast<uint16_t*>(w8);
-  uint16_t* h = reinterpret_cast<uint16_t*>(w8 + align_up((size_t)T * 2 * I * 2, 256));
-  float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) +
-                                         align_up((size_t)T * I * 2, 256));
+  uint16_t* h = reinterpret_cast<uint16_t*>(w8 + at.h);
+  float* part_gu = reinterpret_cast<float*>(w8 + at.part_gu);
+  float* part_dn = reinterpret_cast<float*>(w8 + at.part_dn);
   hipError_t e = hipSuccess;
   if (dx || dw_gu || dw_dn || db_gu) {
-    DhArgs a = {{f.w_dn, nullptr, I, I}, {dy, nullptr, H, T}, T,  H, I, f.gu_layout,
-                {f.act, f.act_alpha, f.act_limit}, gu, dgu, dw_dn ? h : nullptr};
-    const int64_t big = (int64_t)((I + 255) / 256) * ((T + 255) / 256);
-    e = big >= 192 ? launch_dh<Tile256>(a, s) : launch_dh<Tile128>(a, s);
+    DhArgs a = {{f.w_dn, nullptr, I, I}, {dy, nullptr, H, T}, T, H, I,
+                {f.act, f.act_alpha, f.act_limit}, gu, dgu, dw_dn ? h : nullptr,
+                db_gu ? part_gu : nullptr};
+    const bool big = (int64_t)((I + 255) / 256) * ((T + 255) / 256) >= 192;
+    e = with_kind(f.gu_layout, f.act, [&](auto l, auto c) {
+      constexpr int L = decltype(l)::value, A = decltype(c)::value;
+      return big ? launch_dh<Tile256, L, A>(a, s) : launch_dh<Tile128, L, A>(a, s);
+    });
+    if (e != hipSuccess) return e;
+    if (db_gu) {
+      const int rows = big ? Tile256::BB : Tile128::BB;
+      e = launch_sum_rows(part_gu, (T + rows - 1) / rows, 2 * I, db_gu, dw_dtype, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  GradArgs g = {};
+  int n = 0;
+  auto put = [&](const FfnProduct& p, bool col_b) {
+    // longest reduction first
+    int i = n++;
+    for (; i > 0 && g.p[i - 1].K < p.K; --i) {
+      g.p[i] = g.p[i - 1];
+      g.col_b[i] = g.col_b[i - 1];
+    }
+    g.p[i] = p;
+    g.col_b[i] = col_b;
+  };
+  if (dx)
+    put({{f.w_gu, nullptr, H, H}, {dgu, nullptr, 2 * I, T}, 0, 0, 2 * I, H, T, nullptr, add,
+         add_dtype, dx, dx_dtype}, false);
+  if (dw_gu)
+    put({{x, nullptr, H, H}, {dgu, nullptr, 2 * I, 2 * I}, 0, 0, T, H, 2 * I, nullptr, nullptr, 0,
+         dw_gu, dw_dtype}, true);
+  if (dw_dn)
+    put({{h, nullptr, I, I}, {dy, nullptr, H, H}, 0, 0, T, I, H, nullptr, nullptr, 0, dw_dn,
+         dw_dtype}, true);
+  if (n) {
+    int64_t big = 0;
+    for (int i = 0; i < n; ++i) big += tiles_of<Tile256>(g.p[i]);
+    e = big >= 192 ? launch_grads<Tile256>(g, n, s) : launch_grads<Tile128>(g, n, s);
     if (e != hipSuccess) return e;
   }
-  if (dx) {
-    FfnProduct p = {{f.w_gu, nullptr, H, H}, {dgu, nullptr, 2 * I, T}, 0, 0, 2 * I, H, T,
-                    nullptr, add, add_dtype, dx, dx_dtype};
-    e = product<kOpCol, kOpRow>(p, s);
-    if (e != hipSuccess) return e;
-  }
-  if (dw_gu) {
-    FfnProduct p = {{x, nullptr, H, H}, {dgu, nullptr, 2 * I, 2 * I}, 0, 0, T, H, 2 * I,
-                    nullptr, nullptr, 0, dw_gu, dw_dtype};
-    e = product<kOpCol, kOpCol>(p, s);
-    if (e != hipSuccess) return e;
-  }
-  if (dw_dn) {
-    FfnProduct p = {{h, nullptr, I, I}, {dy, nullptr, H, H}, 0, 0, T, I, H,
-                    nullptr, nullptr, 0, dw_dn, dw_dtype};
-    e = product<kOpCol, kOpCol>(p, s);
-    if (e != hipSuccess) return e;
-  }
-  if (db_gu) {
-    e = col_sums(dgu, T, 2 * I, part, db_gu, dw_dtype, s);
-    if (e != hipSuccess) return e;
-  }
-  return db_dn ? col_sums(dy, T, H, part, db_dn, dw_dtype, s) : hipSuccess;
+  return db_dn ? col_sums(dy, T, H, part_dn, db_dn, dw_dtype, s) : hipSuccess;
 }
 
 }  // namespace moe4

@@ -84,8 +84,10 @@ __device__ __forceinline__ void store_h8(const GateUpArgs& a, int t, int j, bool
   }
 }
 
-template <typename S, bool FP8>
-__global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(const GateUpArgs a) {
+template <typename S, bool FP8, int LAYOUT, int ACT>
+__global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(GateUpArgs a) {
+  a.layout = LAYOUT;
+  a.act.act = ACT;
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
   constexpr int kPairs = S::BA / 2, es = FP8 ? 1 : 2;
   const int na = (a.I + kPairs - 1) / kPairs, nb = (a.T + S::BB - 1) / S::BB;
@@ -103,7 +105,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(const GateUpArgs
   gemm_loop<S, kOpRow, kOpRow, FP8>(
       acc, stage_mem, la, lb, a.H, mx, [&](int r) { return pair_row(a.layout, a.I, j0, r); },
       [&](int r) { return r < nt ? t0 + r : -1; });
-  for_each8<S, true>(acc, stage_mem, [&](int row, int jj, float* g, float* u) {
+  for_each8<S, true>(acc, stage_mem, [](int, int) { return NoPre{}; },
+                     [&](int row, int jj, float* g, float* u) {
     const int t = t0 + row, j = j0 + jj;
     const bool on = row < nt && j < a.I;
     if (on) finish8(a, t, j, g, u);
@@ -291,12 +294,14 @@ hipError_t launch_skinny(const GateUpArgs& g, const FfnProduct& d, hipStream_t s
 
 template <typename S, bool FP8>
 hipError_t launch_tiled(const GateUpArgs& g, const FfnProduct& d, hipStream_t s) {
-  auto* k = &k_ffn_gate_up<S, FP8>;
-  hipError_t e = allow_lds(k, S::kLds);
-  if (e != hipSuccess) return e;
   const int64_t n = (int64_t)((g.I + S::BA / 2 - 1) / (S::BA / 2)) * ((g.T + S::BB - 1) / S::BB);
-  k<<<(uint32_t)n, S::kThreads, S::kLds, s>>>(g);
-  e = hipGetLastError();
+  hipError_t e = with_kind(g.layout, g.act.act, [&](auto l, auto c) {
+    auto* k = &k_ffn_gate_up<S, FP8, decltype(l)::value, decltype(c)::value>;
+    hipError_t r = allow_lds(k, S::kLds);
+    if (r != hipSuccess) return r;
+    k<<<(uint32_t)n, S::kThreads, S::kLds, s>>>(g);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return e;
   return launch_product<S, kOpRow, kOpRow, FP8>(d, s);
 }
