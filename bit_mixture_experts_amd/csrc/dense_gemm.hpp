@@ -153,22 +153,16 @@ struct Loader {
       off[i] = col < o.rows ? (uint32_t)(k * ldb) + 2 * col : (uint32_t)kOob;
     }
   }
-  // loads of k-tile kt into the operand's part of a stage
+  // load i of k-tile kt into the operand's part of a stage
   template <bool ASM>
-  __device__ __forceinline__ void issue(int kt, uint8_t* lds) const {
-    uint8_t* dst = lds + __builtin_amdgcn_readfirstlane(wave_id()) * 1024;
+  __device__ __forceinline__ void issue(int kt, int i, uint8_t* lds) const {
+    uint8_t* dst = lds + __builtin_amdgcn_readfirstlane(wave_id()) * 1024 + i * THREADS * 16;
     if constexpr (MODE == kOpRow) {
       const int k0 = kt * 128;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_lds16<ASM>(base, size, dst + i * THREADS * 16,
-                        k0 + chunk < kb ? off[i] + k0 : (uint32_t)kOob);
+      load_lds16<ASM>(base, size, dst, k0 + chunk < kb ? off[i] + k0 : (uint32_t)kOob);
     } else {
       const int left = max(min(kb - kt * 64, 64), 0);
-      const uint8_t* p = base + (int64_t)kt * 64 * ldb;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_lds16<ASM>(p, (uint32_t)(left * ldb), dst + i * THREADS * 16, off[i]);
+      load_lds16<ASM>(base + (int64_t)kt * 64 * ldb, (uint32_t)(left * ldb), dst, off[i]);
     }
   }
 };
@@ -308,14 +302,25 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
-  la.template issue<kAsm>(0, lds);
-  lb.template issue<kAsm>(0, lds + kA);
+  // A k-tile's loads go out a few at a time between the MFMAs: half of them in the last step of
+  // the tile whose stage they take, half in the next tile's first step. Sent in one go they
+  // filled the memory pipeline's queue, and the waves stood at their next load instead of
+  // multiplying (forward of 4096 tokens at H 4096, I 8192: 675 us, and 641 spread). Tiles past the last load
+  // zeros: no branch in the loop, which the compiler would sink the MFMAs before it past.
+  constexpr int kLa = Loader<MA, S::BA, S::kThreads>::kLoads;
+  constexpr int kLoads = kLa + Loader<MB, S::BB, S::kThreads>::kLoads, kHalf = kLoads / 2;
+  auto issue = [&](int kt, int i0, int i1, uint8_t* st) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < i0 || i >= i1) continue;
+      if (i < kLa) la.template issue<kAsm>(kt, i, st);
+      else lb.template issue<kAsm>(kt, i - kLa, st + kA);
+    }
+  };
+  issue(0, 0, kLoads, lds);
   wait_vmcnt<0>();
   lds_barrier();
-  // (tiles past the last load zeros: no branch in the loop, which the compiler would sink the
-  // MFMAs before it past)
-  la.template issue<kAsm>(1, lds + S::kStage);
-  lb.template issue<kAsm>(1, lds + S::kStage + kA);
+  issue(1, 0, kHalf, lds + S::kStage);
 #pragma unroll
   for (int t = 0; t < kRing; ++t) fa[t] = read_a(lds, t, 0);
 #pragma unroll
@@ -335,8 +340,6 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
       wait_vmcnt<0>();
       wait_lgkm0();
       lds_barrier();
-      la.template issue<kAsm>(kt + 2, cur);
-      lb.template issue<kAsm>(kt + 2, cur + kA);
     };
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -368,6 +371,13 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
         }
         // the operand kRing tiles on: of this step, or of the next
         a = t + kRing < S::TA ? read_a(cur, t + kRing, s) : read_a(from, t + kRing - S::TA, sn);
+        // loads of the tile after next once its stage is free, the rest in the next tile
+        constexpr int kSlots = FP8 ? kRing : S::TA;   // groups of MFMAs behind the barrier
+        const int slot = t - (S::TA - kSlots);
+        if (last && slot >= 0)
+          issue(kt + 2, kHalf * slot / kSlots, kHalf * (slot + 1) / kSlots, cur);
+        if (s == 0)
+          issue(kt + 1, kHalf + kHalf * t / S::TA, kHalf + kHalf * (t + 1) / S::TA, nxt);
         __builtin_amdgcn_sched_barrier(0);
       }
     }

@@ -155,30 +155,39 @@ hipError_t launch_grads(GradArgs a, int n, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Column sums of a bf16 matrix [T, N]: part p of P sums its rows in fp32 into part[p][N].
+// Column sums of a bf16 matrix [T, N]: workgroup (x, p) sums part p's rows of 512 columns in
+// fp32 into part[p][N]; its four waves take every fourth row and meet in LDS.
 __global__ __launch_bounds__(256) void k_col_sums(const uint16_t* m, int T, int N, float* part) {
-  const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
-  if (c >= N) return;
+  __shared__ __attribute__((aligned(16))) f32x4 red[4][2][64];
+  const int l = lane_id(), w = wave_id(), c = (blockIdx.x * 64 + l) * 8;
   const int r0 = (int)((int64_t)T * blockIdx.y / gridDim.y);
   const int r1 = (int)((int64_t)T * (blockIdx.y + 1) / gridDim.y);
   float s[8] = {};
-#pragma unroll 8
-  for (int r = r0; r < r1; ++r) {
-    float v[8];
-    load8_bf16(m + (int64_t)r * N + c, v);
+  if (c < N) {
+#pragma unroll 16
+    for (int r = r0 + w; r < r1; r += 4) {
+      float v[8];
+      load8_bf16(m + (int64_t)r * N + c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += v[i];
+      for (int i = 0; i < 8; ++i) s[i] += v[i];
+    }
   }
-  store8_f32(part + (int64_t)blockIdx.y * N + c, s);
+  red[w][0][l] = f32x4{s[0], s[1], s[2], s[3]};
+  red[w][1][l] = f32x4{s[4], s[5], s[6], s[7]};
+  __syncthreads();
+  if (w < 2 && c < N) {
+    const f32x4 v = red[0][w][l] + red[1][w][l] + red[2][w][l] + red[3][w][l];
+    *reinterpret_cast<f32x4*>(part + (int64_t)blockIdx.y * N + c + 4 * w) = v;
+  }
 }
 
-constexpr int kColParts = 256;
+constexpr int kColParts = 128;
 int col_parts(int T) { return T < kColParts ? (T > 0 ? T : 1) : kColParts; }
 
 hipError_t col_sums(const uint16_t* m, int T, int N, float* part, void* out, int dtype,
                     hipStream_t s) {
   const int P = col_parts(T);
-  k_col_sums<<<dim3((N + 2047) / 2048, P), 256, 0, s>>>(m, T, N, part);
+  k_col_sums<<<dim3((N + 511) / 512, P), 256, 0, s>>>(m, T, N, part);
   hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : launch_sum_rows(part, P, N, out, dtype, s);
 }
