@@ -9,12 +9,15 @@
 // rows of what is in memory).
 //
 // One workgroup makes a BA x BB tile of C with WA x WB waves of TA x TB 32x32 MFMA tiles.
-// k runs in tiles of 128 bytes per row (64 bf16 or 128 e4m3 values) through two LDS stages,
-// filled by direct loads (no register round trip).
+// k runs in tiles of 128 bytes per row (64 bf16 values) through two LDS stages, or of 64 bytes
+// (64 e4m3 values) through four, filled by direct loads (no register round trip). An e4m3
+// tile is multiplied in half the time of a bf16 one of the same bytes, so its loads need to
+// be further ahead; for bf16 the shorter rows cost more (twice the requests) than the depth
+// gave.
 //
 //  * Row operand: LDS [rows][128 B]; the 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7),
 //    so that the 16 rows of an operand read hit 16 different 16-byte bank groups (two rows
-//    share a 256-byte bank line).
+//    share a 256-byte bank line). 64-byte rows: c ^ ((r >> 2) & 3) (four rows a line).
 //  * Col operand: LDS [64 k][rows * 2 B] as in memory; the MFMA wants 8 consecutive k of one
 //    row in a lane, which ds_read_b64_tr_b16 delivers: 16 lanes read a 4 (k) x 16 (row)
 //    block of 8 bytes each and get its transpose. The 32-byte unit u of row k sits at
@@ -24,7 +27,7 @@
 // in the last step of a k-tile those of the next tile's first step, behind the tile's one
 // barrier. The barrier says two things at once: every wave's loads of tile kt + 1 have
 // landed (each waits for its own first), and every wave has read all of tile kt, whose stage
-// then takes the loads of tile kt + 2.
+// then takes the loads of the tile as many on as there are stages.
 #pragma once
 
 #include <type_traits>
@@ -55,8 +58,8 @@ struct TileShape {
   static constexpr int WA = WA_, WB = WB_, TA = TA_, TB = TB_;
   static constexpr int BA = WA * TA * 32, BB = WB * TB * 32;
   static constexpr int kWaves = WA * WB, kThreads = kWaves * 64;
-  static constexpr int kStage = (BA + BB) * 128;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLds = 2 * (BA + BB) * 128;   // the stages, of either kind
+  static constexpr int kLdsMx = kLds + 2 * (BA + BB) * 4;   // with two pairs of k-tiles' scales
 };
 using Tile256 = TileShape<2, 4, 4, 2>;   // 256 x 256, eight waves, one workgroup per CU
 using Tile128 = TileShape<2, 2, 2, 2>;   // 128 x 128, four waves, two workgroups per CU
@@ -107,12 +110,12 @@ __device__ __forceinline__ void load_lds16(const void* p, uint32_t bytes, uint8_
   }
 }
 
-// Loader of one operand: N rows (a or b axis) per k-tile.
-template <int MODE, int N, int THREADS>
+// Loader of one operand: N rows (a or b axis) and RB bytes of k (col: RB / 2 rows of k) per
+// k-tile.
+template <int MODE, int N, int THREADS, int RB>
 struct Loader {
-  static constexpr int kLoads = N * 128 / (16 * THREADS);
-  static_assert(kLoads * 16 * THREADS == N * 128, "whole loads per thread");
-  static constexpr int kRowB = MODE == kOpRow ? 128 : 2 * N;   // LDS bytes of a row
+  static constexpr int kLoads = N * RB / (16 * THREADS);
+  static_assert(kLoads * 16 * THREADS == N * RB, "whole loads per thread");
   const uint8_t* base;    // first element of the tile (row) or of column 0 of k row 0 (col)
   uint32_t size;          // row: bytes from base the tile may read
   int64_t ldb;            // bytes from row to row
@@ -131,9 +134,9 @@ struct Loader {
     kb = K * es;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int piece = i * THREADS + t, r = piece >> 3;
-      const int c = (piece & 7) ^ ((r >> 1) & 7);
-      chunk = c * 16;   // the same for every i: loads are THREADS / 8 rows apart, a multiple of 16
+      const int piece = i * THREADS + t, r = piece / (RB / 16);
+      const int c = RB == 128 ? (piece & 7) ^ ((r >> 1) & 7) : (piece & 3) ^ ((r >> 2) & 3);
+      chunk = c * 16;   // the same for every i: loads are a multiple of 16 rows apart
       const int rr = row_of(r);
       off[i] = rr >= 0 ? (uint32_t)(rr * ldb) + c * 16 : (uint32_t)kOob;
     }
@@ -158,24 +161,25 @@ struct Loader {
   __device__ __forceinline__ void issue(int kt, int i, uint8_t* lds) const {
     uint8_t* dst = lds + __builtin_amdgcn_readfirstlane(wave_id()) * 1024 + i * THREADS * 16;
     if constexpr (MODE == kOpRow) {
-      const int k0 = kt * 128;
+      const int k0 = kt * RB;
       load_lds16<ASM>(base, size, dst, k0 + chunk < kb ? off[i] + k0 : (uint32_t)kOob);
     } else {
-      const int left = max(min(kb - kt * 64, 64), 0);
-      load_lds16<ASM>(base + (int64_t)kt * 64 * ldb, (uint32_t)(left * ldb), dst, off[i]);
+      constexpr int kRows = RB / 2;
+      const int left = max(min(kb - kt * kRows, kRows), 0);
+      load_lds16<ASM>(base + (int64_t)kt * kRows * ldb, (uint32_t)(left * ldb), dst, off[i]);
     }
   }
 };
 
 // LDS reader of one operand: T 32-row MFMA tiles of a wave, rows w0 ...
-template <int MODE, int N, int T>
+template <int MODE, int N, int T, int RB>
 struct Reader {
   int a[MODE == kOpRow ? 1 : T];
   __device__ __forceinline__ void init(int w0) {
     const int l = lane_id();
     if constexpr (MODE == kOpRow) {
       const int r = l & 31;
-      a[0] = (w0 + r) * 128 + (((l >> 5) ^ ((r >> 1) & 7)) * 16);
+      a[0] = (w0 + r) * RB + (((l >> 5) ^ (RB == 128 ? (r >> 1) & 7 : (r >> 2) & 3)) * 16);
     } else {
       const int k = (l >> 5) * 8 + ((l >> 2) & 3);
 #pragma unroll
@@ -188,60 +192,66 @@ struct Reader {
   // the lane's 8 bf16 of MFMA tile t, step s (16 k)
   __device__ __forceinline__ bf16x8 bf16(const uint8_t* lds, int t, int s) const {
     if constexpr (MODE == kOpRow) {
-      return *reinterpret_cast<const bf16x8*>(lds + (a[0] ^ (s * 32)) + t * 4096);
+      return *reinterpret_cast<const bf16x8*>(lds + (a[0] ^ (s * 32)) + t * 32 * RB);
     } else {
       const s16x4 lo = lds_tr16(lds + a[t] + s * 16 * 2 * N);
       const s16x4 hi = lds_tr16(lds + a[t] + s * 16 * 2 * N + 4 * 2 * N);
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
-  // the lane's 32 e4m3 of MFMA tile t, step s (64 k): the matrix instruction takes k = 32 c +
-  // 16 (lane / 32) .. + 15 in its c-th 16 bytes
-  __device__ __forceinline__ i32x8 fp8(const uint8_t* lds, int t, int s) const {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + (a[0] ^ (s * 64)) + t * 4096);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + (a[0] ^ (s * 64) ^ 32) + t * 4096);
+  // the lane's 32 e4m3 of MFMA tile t (64 k): the matrix instruction takes k = 32 c + 16 (lane /
+  // 32) .. + 15 in its c-th 16 bytes
+  __device__ __forceinline__ i32x8 fp8(const uint8_t* lds, int t) const {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + a[0] + t * 32 * RB);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + (a[0] ^ 32) + t * 32 * RB);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
 
-// e8m0 scales of an MXFP8 operand, read per lane: the 4 bytes of a row and k-tile start at
-// any byte, so the two dwords around them are loaded and shifted into one. The last dword
-// may reach up to 3 bytes past the scales' end (never past the aligned dword that holds their
-// last byte). Of the lane's dword, byte 2 s + lane / 32 is step s's: one shift by the lane's
-// half puts it at byte 2 s.
-template <int T>
-struct ScaleReader {
+// e8m0 scales of both MXFP8 operands: thread t of the workgroup reads those of tile row t (A's
+// rows, then B's), two k-tiles' (4 bytes) at a time, and the waves take them from LDS, where
+// each row's lie as one dword. Read by every wave for its own rows they were fetched three
+// times over, a gather of 32 rows to an instruction, and took the memory pipeline longer than
+// the operands did (2048 tokens at H = I = 2880: MX_FIGURES).
+// The 4 bytes start at any byte, so the two dwords around them are loaded and shifted into
+// one. The last dword may reach up to 3 bytes past the scales' end (never past the aligned
+// dword that holds their last byte). Blocks past the row's end (their codes are zeros) take
+// scale 0: the bytes there belong to the next row and may be e8m0 NaNs.
+template <typename S>
+struct ScaleStage {
+  static_assert(S::kThreads == S::BA + S::BB, "a thread for every row");
+  static constexpr int kBytes = S::kThreads * 4;   // of a pair of k-tiles
   rsrc_t r;
-  int nb;              // blocks of a row
-  uint32_t off[T];     // byte of the row's first scale
-  u32x2 raw[T];
-  uint32_t v[T];
-  template <typename RowOf>
-  __device__ __forceinline__ void init(const uint8_t* s, int64_t bytes, int blocks, int w0,
-                                       RowOf row_of) {
-    const int l = lane_id();
-    r = make_rsrc_uniform(s, (uint32_t)((bytes + 3) & ~(int64_t)3));
+  int nb;            // blocks of a row
+  uint32_t off;      // byte of the row's first scale
+  u32x2 raw;
+  template <typename RowA, typename RowB>
+  __device__ __forceinline__ void init(const uint8_t* sa, int64_t na, const uint8_t* sb, int64_t nbytes,
+                                       int blocks, RowA row_a, RowB row_b) {
+    // whole waves belong to one operand
+    const int t = threadIdx.x;
+    const bool is_a = __builtin_amdgcn_readfirstlane(wave_id()) * 64 < S::BA;
+    r = make_rsrc_uniform(is_a ? sa : sb, (uint32_t)(((is_a ? na : nbytes) + 3) & ~(int64_t)3));
     nb = blocks;
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int row = row_of(w0 + 32 * t + (l & 31));
-      off[t] = row >= 0 ? (uint32_t)row * nb : (uint32_t)kOob;
-    }
+    const int row = is_a ? row_a(t) : row_b(t - S::BA);
+    off = row >= 0 ? (uint32_t)row * nb : (uint32_t)kOob;
   }
-  __device__ __forceinline__ void prefetch(int kt) {
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      raw[t] = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)((off[t] & ~3u) + 4 * kt), 0, 0));
+  __device__ __forceinline__ void load(int pair) {
+    raw = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)((off & ~3u) + 4 * pair), 0, 0));
   }
-  // Blocks past the row's end (their codes are zeros) take scale 0: the bytes there belong to
-  // the next row and may be e8m0 NaNs.
-  __device__ __forceinline__ void take(int kt) {
-    const int left = nb - 4 * kt, h = lane_id() >> 5;
-    const uint32_t keep = (h < left ? 0xFFu : 0u) | (2 + h < left ? 0xFF0000u : 0u);
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      v[t] = (uint32_t)((((uint64_t)raw[t][1] << 32) | raw[t][0]) >> (8 * ((off[t] & 3) + h))) & keep;
+  // the loaded scales of a pair of k-tiles into LDS
+  __device__ __forceinline__ void store(u32x2 raw, int pair, uint8_t* lds) const {
+    const int left = nb - 4 * pair;
+    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+    const uint32_t v = (uint32_t)((((uint64_t)raw[1] << 32) | raw[0]) >> (8 * (off & 3))) & keep;
+    typedef uint32_t u32x1 __attribute__((ext_vector_type(1)));
+    reinterpret_cast<u32x1*>(lds)[threadIdx.x] = u32x1{v};
+  }
+  // the dword of tile row `row` (byte 2 h + lane / 32 is the pair's h-th tile's)
+  static __device__ __forceinline__ uint32_t get(const uint8_t* lds, int row) {
+    typedef uint32_t u32x1 __attribute__((ext_vector_type(1)));
+    return reinterpret_cast<const u32x1*>(lds)[row][0];
   }
 };
 
@@ -253,24 +263,30 @@ struct MxState<true> {
   int64_t na, nb;           // their bytes
 };
 
+constexpr int row_bytes(bool fp8) { return fp8 ? 64 : 128; }
+template <typename S, int MODE, int N, bool FP8>
+using OpLoader = Loader<MODE, N, S::kThreads, row_bytes(FP8)>;
+
 // The k loop. acc[ta][tb] += A B^T over all of K. When it returns this wave has no load in
 // flight, but other waves may still be reading: a barrier stands before the stages are used
 // for anything else.
 template <typename S, int MA, int MB, bool FP8, typename RowA, typename RowB>
 __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* lds,
-                                          Loader<MA, S::BA, S::kThreads>& la,
-                                          Loader<MB, S::BB, S::kThreads>& lb, int K,
+                                          OpLoader<S, MA, S::BA, FP8>& la,
+                                          OpLoader<S, MB, S::BB, FP8>& lb, int K,
                                           const MxState<FP8>& mx, RowA row_a, RowB row_b) {
-  constexpr int kSteps = FP8 ? 2 : 4, KT = FP8 ? 128 : 64;
+  constexpr int kRb = row_bytes(FP8), kSub = 128 / kRb;   // k-tiles of 128 bytes of k
+  constexpr int kSteps = FP8 ? 1 : 4, kStages = 2 * kSub;
+  constexpr int kStage = (S::BA + S::BB) * kRb;
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
   const int wa = w % S::WA, wb = w / S::WA;
-  Reader<MA, S::BA, S::TA> ra;
-  Reader<MB, S::BB, S::TB> rb;
+  Reader<MA, S::BA, S::TA, kRb> ra;
+  Reader<MB, S::BB, S::TB, kRb> rb;
   ra.init(wa * S::TA * 32);
   rb.init(wb * S::TB * 32);
-  constexpr int kA = S::BA * 128;   // offset of the B part of a stage
+  constexpr int kA = S::BA * kRb;   // offset of the B part of a stage
   constexpr bool kAsm = MA == kOpCol || MB == kOpCol;
-  const int nk = (K + KT - 1) / KT;
+  const int nk = (K * (FP8 ? 1 : 2) + 127) / 128;   // turns of the loop, 128 bytes of k each
 
   using Frag = std::conditional_t<FP8, i32x8, bf16x8>;
   // bf16: all A operands of a step and the B operands of two. e4m3, with twice the registers
@@ -279,20 +295,33 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
   constexpr int kRing = FP8 ? 2 : S::TA, kB = FP8 ? 1 : 2;
   Frag fa[kRing], fb[kB][S::TB];
   auto read_a = [&](const uint8_t* st, int t, int s) {
-    if constexpr (FP8) return ra.fp8(st, t, s);
+    if constexpr (FP8) return ra.fp8(st, t);
     else return ra.bf16(st, t, s);
   };
   auto read_b = [&](const uint8_t* st, int t, int s) {
-    if constexpr (FP8) return rb.fp8(st + kA, t, s);
+    if constexpr (FP8) return rb.fp8(st + kA, t);
     else return rb.bf16(st + kA, t, s);
   };
-  ScaleReader<FP8 ? S::TA : 1> xa;
-  ScaleReader<FP8 ? S::TB : 1> xb;
+  // e4m3: this pair's scales, shifted for the lane's half, and the next one's as they come
+  ScaleStage<S> sc;
+  uint8_t* const sclds = lds + S::kLds;
+  uint32_t xa[FP8 ? S::TA : 1], xb[FP8 ? S::TB : 1], na[FP8 ? S::TA : 1], nb[FP8 ? S::TB : 1];
+  auto next_scales = [&](int pair) {
+    const uint8_t* p = sclds + (pair & 1) * ScaleStage<S>::kBytes;
+    const int r = lane_id() & 31;
+#pragma unroll
+    for (int t = 0; t < S::TA; ++t) na[t] = sc.get(p, (wa * S::TA + t) * 32 + r);
+#pragma unroll
+    for (int u = 0; u < S::TB; ++u) nb[u] = sc.get(p, S::BA + (wb * S::TB + u) * 32 + r);
+  };
+  u32x2 first;
   if constexpr (FP8) {
-    xa.init(mx.sa, mx.na, K / 32, wa * S::TA * 32, row_a);
-    xb.init(mx.sb, mx.nb, K / 32, wb * S::TB * 32, row_b);
-    xa.prefetch(0);
-    xb.prefetch(0);
+    // both before the operands' loads: the loop then finds as many loads behind the scales'
+    // as it issues itself, and does not wait for more of them
+    sc.init(mx.sa, mx.na, mx.sb, mx.nb, K / 32, row_a, row_b);
+    sc.load(0);
+    first = sc.raw;
+    sc.load(1);
   }
 
 #pragma unroll
@@ -302,13 +331,17 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
-  // A k-tile's loads go out a few at a time between the MFMAs: half of them in the last step of
-  // the tile whose stage they take, half in the next tile's first step. Sent in one go they
-  // filled the memory pipeline's queue, and the waves stood at their next load instead of
-  // multiplying (forward of 4096 tokens at H 4096, I 8192: 675 us, and 641 spread). Tiles past the last load
-  // zeros: no branch in the loop, which the compiler would sink the MFMAs before it past.
-  constexpr int kLa = Loader<MA, S::BA, S::kThreads>::kLoads;
-  constexpr int kLoads = kLa + Loader<MB, S::BB, S::kThreads>::kLoads, kHalf = kLoads / 2;
+  // A k-tile's loads go out a few at a time between the MFMAs, behind the barrier that frees
+  // their stage up to the next one. Sent in one go they filled the memory pipeline's queue, and
+  // the waves stood at their next load instead of multiplying (forward of 4096 tokens at H
+  // 4096, I 8192: 675 us, and 641 spread). Tiles past the last load zeros: no branch in the
+  // loop, which the compiler would sink the MFMAs before it past.
+  constexpr int kLa = OpLoader<S, MA, S::BA, FP8>::kLoads;
+  constexpr int kLoads = kLa + OpLoader<S, MB, S::BB, FP8>::kLoads;
+  // groups of MFMAs between the barrier and the tile's end, and in the next tile's first step
+  // before its barrier; the loads that go out in the first ones
+  constexpr int kAfter = kRing, kBefore = FP8 ? S::TA - kRing : S::TA;
+  constexpr int kEarly = kBefore ? kLoads / 2 : kLoads;
   auto issue = [&](int kt, int i0, int i1, uint8_t* st) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -317,72 +350,96 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
       else lb.template issue<kAsm>(kt, i - kLa, st + kA);
     }
   };
-  issue(0, 0, kLoads, lds);
-  wait_vmcnt<0>();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i, 0, kLoads, lds + i * kStage);
+  issue(kStages - 1, 0, kEarly, lds + (kStages - 1) * kStage);
+  wait_vmcnt<(kStages - 2) * kLoads + kEarly>();
+  if constexpr (FP8) {
+    sc.store(first, 0, sclds);
+    wait_lgkm0();
+  }
   lds_barrier();
-  issue(1, 0, kHalf, lds + S::kStage);
+  if constexpr (FP8) next_scales(0);
 #pragma unroll
   for (int t = 0; t < kRing; ++t) fa[t] = read_a(lds, t, 0);
 #pragma unroll
   for (int t = 0; t < S::TB; ++t) fb[0][t] = read_b(lds, t, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    uint8_t* cur = lds + (kt & 1) * S::kStage;
-    uint8_t* nxt = lds + ((kt + 1) & 1) * S::kStage;
+  for (int kp = 0; kp < nk; ++kp) {
     if constexpr (FP8) {
-      xa.take(kt);
-      xb.take(kt);
-      xa.prefetch(kt + 1);
-      xb.prefetch(kt + 1);
+      const int half = 8 * (lane_id() >> 5);
+#pragma unroll
+      for (int t = 0; t < S::TA; ++t) xa[t] = na[t] >> half;
+#pragma unroll
+      for (int u = 0; u < S::TB; ++u) xb[u] = nb[u] >> half;
+      sc.store(sc.raw, kp + 1, sclds + ((kp + 1) & 1) * ScaleStage<S>::kBytes);
+      sc.load(kp + 2);
     }
-    // the tile's barrier: the wave's loads of the next k-tile have landed, its reads of this
-    // one are done, and so are the others'
-    auto turn = [&]() {
-      wait_vmcnt<0>();
-      wait_lgkm0();
-      lds_barrier();
-    };
+    uint8_t* const base = lds + (kp & 1) * kSub * kStage;
+    uint8_t* const other = lds + ((kp + 1) & 1) * kSub * kStage;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const bool last = s == kSteps - 1;
-      const int sn = (s + 1) % kSteps;
-      // operands of the next step (past the last tile: stale values, read and never used)
-      const uint8_t* from = last ? nxt : cur;
-      if constexpr (!FP8) {
-        if (last) turn();
+    for (int h = 0; h < kSub; ++h) {
+      const int kt = kp * kSub + h;
+      uint8_t* const cur = base + h * kStage;
+      uint8_t* const nxt = h + 1 < kSub ? cur + kStage : other;
+      uint8_t* const prv = h > 0 ? cur - kStage : other + (kSub - 1) * kStage;
+      // the tile's barrier: the wave's loads of the next tile have landed (those of the tiles
+      // after it may be in flight), its reads of this one are done, and so are the others'
+      auto turn = [&]() {
+        wait_vmcnt<(kStages - 2) * kLoads>();
+        wait_lgkm0();
+        lds_barrier();
+        if (FP8 && h == kSub - 1) next_scales(kp + 1);
+      };
 #pragma unroll
-        for (int u = 0; u < S::TB; ++u) fb[(s + 1) % kB][u] = read_b(from, u, sn);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      for (int s = 0; s < kSteps; ++s) {
+        const bool last = s == kSteps - 1;
+        const int sn = (s + 1) % kSteps;
+        // operands of the next step (past the last tile: stale values, read and never used)
+        const uint8_t* from = last ? nxt : cur;
+        if constexpr (!FP8) {
+          if (last) turn();
 #pragma unroll
-      for (int t = 0; t < S::TA; ++t) {
-        Frag& a = fa[t % kRing];
-#pragma unroll
-        for (int u = 0; u < S::TB; ++u) {
-          Frag& b = fb[s % kB][u];
-          if constexpr (FP8)
-            acc[t][u] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                     a, b, acc[t][u], 0, 0, 0, (int)xa.v[t], 0, (int)xb.v[u])
-                               : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                     a, b, acc[t][u], 0, 0, 2, (int)xa.v[t], 2, (int)xb.v[u]);
-          else
-            acc[t][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[t][u], 0, 0, 0);
-          if (FP8 && last && t == S::TA - kRing && u == S::TB - 1) turn();
-          if (FP8 && t == S::TA - 1) b = read_b(from, u, sn);
+          for (int u = 0; u < S::TB; ++u) fb[(s + 1) % kB][u] = read_b(from, u, sn);
         }
-        // the operand kRing tiles on: of this step, or of the next
-        a = t + kRing < S::TA ? read_a(cur, t + kRing, s) : read_a(from, t + kRing - S::TA, sn);
-        // loads of the tile after next once its stage is free, the rest in the next tile
-        constexpr int kSlots = FP8 ? kRing : S::TA;   // groups of MFMAs behind the barrier
-        const int slot = t - (S::TA - kSlots);
-        if (last && slot >= 0)
-          issue(kt + 2, kHalf * slot / kSlots, kHalf * (slot + 1) / kSlots, cur);
-        if (s == 0)
-          issue(kt + 1, kHalf + kHalf * t / S::TA, kHalf + kHalf * (t + 1) / S::TA, nxt);
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < S::TA; ++t) {
+          Frag& a = fa[t % kRing];
+#pragma unroll
+          for (int u = 0; u < S::TB; ++u) {
+            Frag& b = fb[s % kB][u];
+            if constexpr (FP8)
+              acc[t][u] = h == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                       a, b, acc[t][u], 0, 0, 0, (int)xa[t], 0, (int)xb[u])
+                                 : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                       a, b, acc[t][u], 0, 0, 2, (int)xa[t], 2, (int)xb[u]);
+            else
+              acc[t][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[t][u], 0, 0, 0);
+            if (FP8 && t == S::TA - kRing && u == S::TB - 1) turn();
+            if (FP8 && t == S::TA - 1) b = read_b(from, u, sn);
+          }
+          // the operand kRing tiles on: of this step, or of the next
+          a = t + kRing < S::TA ? read_a(cur, t + kRing, s) : read_a(from, t + kRing - S::TA, sn);
+          const int slot = t - (S::TA - kAfter);
+          if (last && slot >= 0)
+            issue(kt + kStages, kEarly * slot / kAfter, kEarly * (slot + 1) / kAfter, cur);
+          if (s == 0 && t < kBefore)
+            issue(kt + kStages - 1, kEarly + (kLoads - kEarly) * t / kBefore,
+                  kEarly + (kLoads - kEarly) * (t + 1) / kBefore, prv);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   }
   wait_vmcnt<0>();   // the zeros of the tiles past the last, before the stages are used again
+}
+
+// the first a (PAIR: pair) of the tile that for_each8 hands this lane
+template <typename S, bool PAIR>
+__device__ __forceinline__ int lane_a() {
+  constexpr int W = S::TA * 32, kPer = PAIR ? W / 16 : W / 8;
+  const int wa = __builtin_amdgcn_readfirstlane(wave_id()) % S::WA, c = lane_id() % kPer;
+  return PAIR ? wa * (W / 2) + 32 * (c / 4) + 8 * (c % 4) : wa * W + 8 * c;
 }
 
 // Epilogue: hands every value of the tile to f(b, a, v, pre) as 8 consecutive a of one row b in
@@ -390,13 +447,14 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
 // the pair's place in the tile), in an order that makes a wave's stores whole row segments.
 // Through LDS, 32 rows b of the wave at a time as fp32 [32][TA * 32]: the 16-byte chunk c of
 // row b sits at c ^ (b & 15), which spreads the 16 rows of a write over the banks.
-// load(b, a) gives pre, what f reads from memory for the same values: it is asked for two
-// turns ahead of f, so that its latency hides behind the turns between.
-template <typename S, bool PAIR, typename L, typename F>
+// load(b, a) gives pre, what f reads from memory for the same values: it is asked for DEPTH
+// turns ahead of f, since one turn is far shorter than a load. a is the same in every turn of
+// a lane.
+template <typename S, bool PAIR, int DEPTH, typename L, typename F>
 __device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uint8_t* lds, L load,
                                           F f) {
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const int wa = w % S::WA, wb = w / S::WA, l = lane_id();
+  const int wb = w / S::WA, l = lane_id();
   constexpr int W = S::TA * 32;              // fp32 values of a row
   constexpr int kKey = W / 4 >= 16 ? 15 : W / 4 - 1;
   static_assert(S::kWaves * 32 * W * 4 <= S::kLds, "staging fits the stages");
@@ -406,11 +464,12 @@ __device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uin
   const int c = l % kPer;
   // turn n = (u, i): the tile's row of the lane, and its first a (PAIR: its first pair)
   auto row_at = [&](int n) { return wb * S::TB * 32 + n * kRows + l / kPer; };
-  const int a_at = PAIR ? wa * (W / 2) + 32 * (c / 4) + 8 * (c % 4) : wa * W + 8 * c;
+  const int a_at = lane_a<S, PAIR>();
   using Pre = decltype(load(0, 0));
-  Pre pre[2];
-  pre[0] = load(row_at(0), a_at);
-  pre[1] = load(row_at(1), a_at);
+  Pre pre[DEPTH];
+#pragma unroll
+  for (int n = 0; n < DEPTH; ++n)
+    if (n < kAll) pre[n] = load(row_at(n), a_at);
   lds_barrier();   // every wave is done with the k loop's stages
 #pragma unroll
   for (int u = 0; u < S::TB; ++u) {
@@ -438,8 +497,8 @@ __device__ __forceinline__ void for_each8(const f32x16 (&acc)[S::TA][S::TB], uin
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int n = u * kTurns + i, bb = i * kRows + l / kPer;
-      const Pre mine = pre[n & 1];
-      if (n + 2 < kAll) pre[n & 1] = load(row_at(n + 2), a_at);
+      const Pre mine = pre[n % DEPTH];
+      if (n + DEPTH < kAll) pre[n % DEPTH] = load(row_at(n + DEPTH), a_at);
       if constexpr (PAIR) {
         const int p = c / 4, j = 8 * (c % 4);   // pair group (two MFMA tiles), place in it
         float g[8], uu[8];

@@ -105,8 +105,8 @@ template <typename S, int MA, int MB, bool FP8>
 __device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, int ib,
                                                  uint8_t* lds) {
   const int a0 = ia * S::BA, b0 = ib * S::BB;
-  Loader<MA, S::BA, S::kThreads> la;
-  Loader<MB, S::BB, S::kThreads> lb;
+  OpLoader<S, MA, S::BA, FP8> la;
+  OpLoader<S, MB, S::BB, FP8> lb;
   constexpr int es = FP8 ? 1 : 2;
   if constexpr (MA == kOpRow) {
     const int n = min(S::BA, p.na - a0);
@@ -127,7 +127,9 @@ __device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, in
       acc, lds, la, lb, p.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
       [&](int r) { return b0 + r < p.nb ? b0 + r : -1; });
   const bool add32 = p.add_dtype == MOE4_DTYPE_F32;
-  for_each8<S, false>(
+  float bias[8] = {};   // the same columns in every turn
+  if (const int c = a0 + lane_a<S, false>(); p.bias && c < p.na) load8_bf16(p.bias + c, bias);
+  for_each8<S, false, 8>(
       acc, lds,
       [&](int row, int a) {
         Raw16 r;
@@ -147,12 +149,8 @@ __device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, in
       [&](int row, int a, float* v, const Raw16& r) {
         const int b = b0 + row, c = a0 + a;
         if (b >= p.nb || c >= p.na) return;
-        if (p.bias) {
-          float x[8];
-          load8_bf16(p.bias + c, x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += x[i];
-        }
+        for (int i = 0; i < 8; ++i) v[i] += bias[i];
         if (p.add) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -195,9 +193,10 @@ template <typename S, int MA, int MB, bool FP8>
 inline hipError_t launch_product(const FfnProduct& p, hipStream_t s) {
   const int64_t n = (int64_t)((p.na + S::BA - 1) / S::BA) * ((p.nb + S::BB - 1) / S::BB);
   auto* k = &k_ffn_product<S, MA, MB, FP8>;
-  hipError_t e = allow_lds(k, S::kLds);
+  constexpr int kBytes = FP8 ? S::kLdsMx : S::kLds;
+  hipError_t e = allow_lds(k, kBytes);
   if (e != hipSuccess) return e;
-  k<<<(uint32_t)n, S::kThreads, S::kLds, s>>>(p);
+  k<<<(uint32_t)n, S::kThreads, kBytes, s>>>(p);
   return hipGetLastError();
 }
 

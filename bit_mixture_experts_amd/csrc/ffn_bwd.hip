@@ -31,8 +31,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
   int ia, ib;
   tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
   const int j0 = ia * S::BA, t0 = ib * S::BB, nt = min(S::BB, a.T - t0);
-  Loader<kOpCol, S::BA, S::kThreads> la;
-  Loader<kOpRow, S::BB, S::kThreads> lb;
+  OpLoader<S, kOpCol, S::BA, false> la;
+  OpLoader<S, kOpRow, S::BB, false> lb;
   la.init_col(a.W, a.H, j0);
   lb.init_row(a.dY, 2, a.H, t0, nt, [=](int r) { return r < nt ? r : -1; });
   f32x16 acc[S::TA][S::TB];
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
   auto col0 = [&](int j) { return halves ? j : 2 * j; };
   auto col1 = [&](int j) { return halves ? a.I + j : 2 * j + 8; };
   float sums[16] = {};   // of dGU over the lane's rows, in fp32 before the rounding
-  for_each8<S, false>(
+  for_each8<S, false, 4>(
       acc, stage_mem,
       [&](int row, int jj) {
         RawGu r;

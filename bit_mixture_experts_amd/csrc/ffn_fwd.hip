@@ -24,28 +24,33 @@ __device__ __forceinline__ int gu_col(int layout, int I, int j, bool up) {
   return layout == MOE4_GU_HALVES ? (up ? I + j : j) : 2 * j + (up ? 1 : 0);
 }
 
-// bias, saved pre-activations and activation of 8 pairs j .. j+7 of token t, in place of g
-__device__ __forceinline__ void finish8(const GateUpArgs& a, int t, int j, float* g, float* u) {
-  if (a.bias) {
-    if (a.layout == MOE4_GU_HALVES) {
-      float x[8], y[8];
-      load8_bf16(a.bias + j, x);
-      load8_bf16(a.bias + a.I + j, y);
+// the biases of 8 pairs j .. j+7: gates, then ups; zeros without
+__device__ __forceinline__ void load_bias8(const GateUpArgs& a, int j, float* b) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] += x[i];
-        u[i] += y[i];
-      }
-    } else {
-      float x[16];
-      load8_bf16(a.bias + 2 * j, x);
-      load8_bf16(a.bias + 2 * j + 8, x + 8);
+  for (int i = 0; i < 16; ++i) b[i] = 0.0f;
+  if (!a.bias || j >= a.I) return;
+  if (a.layout == MOE4_GU_HALVES) {
+    load8_bf16(a.bias + j, b);
+    load8_bf16(a.bias + a.I + j, b + 8);
+  } else {
+    float x[16];
+    load8_bf16(a.bias + 2 * j, x);
+    load8_bf16(a.bias + 2 * j + 8, x + 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] += x[2 * i];
-        u[i] += x[2 * i + 1];
-      }
+    for (int i = 0; i < 8; ++i) {
+      b[i] = x[2 * i];
+      b[8 + i] = x[2 * i + 1];
     }
+  }
+}
+
+// bias, saved pre-activations and activation of 8 pairs j .. j+7 of token t, in place of g
+__device__ __forceinline__ void finish8(const GateUpArgs& a, int t, int j, const float* bias,
+                                        float* g, float* u) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    g[i] += bias[i];
+    u[i] += bias[8 + i];
   }
   if (a.save_gu) {
     float* s = a.save_gu + (int64_t)t * 2 * a.I;
@@ -95,8 +100,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(GateUpArgs a) {
   tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
   const int j0 = ia * kPairs, t0 = ib * S::BB;
   const int nt = min(S::BB, a.T - t0);
-  Loader<kOpRow, S::BA, S::kThreads> la;
-  Loader<kOpRow, S::BB, S::kThreads> lb;
+  OpLoader<S, kOpRow, S::BA, FP8> la;
+  OpLoader<S, kOpRow, S::BB, FP8> lb;
   la.init_row(a.W, es, a.H, 0, 2 * a.I, [&](int r) { return pair_row(a.layout, a.I, j0, r); });
   lb.init_row(a.X, es, a.H, t0, nt, [=](int r) { return r < nt ? r : -1; });
   MxState<FP8> mx;
@@ -105,11 +110,13 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(GateUpArgs a) {
   gemm_loop<S, kOpRow, kOpRow, FP8>(
       acc, stage_mem, la, lb, a.H, mx, [&](int r) { return pair_row(a.layout, a.I, j0, r); },
       [&](int r) { return r < nt ? t0 + r : -1; });
-  for_each8<S, true>(acc, stage_mem, [](int, int) { return NoPre{}; },
-                     [&](int row, int jj, float* g, float* u) {
+  float bias[16];   // the same pairs in every turn
+  load_bias8(a, j0 + lane_a<S, true>(), bias);
+  for_each8<S, true, 1>(acc, stage_mem, [](int, int) { return NoPre{}; },
+                        [&](int row, int jj, float* g, float* u) {
     const int t = t0 + row, j = j0 + jj;
     const bool on = row < nt && j < a.I;
-    if (on) finish8(a, t, j, g, u);
+    if (on) finish8(a, t, j, bias, g, u);
     store_h8<FP8>(a, t, j, on, g);
   });
 }
@@ -246,13 +253,14 @@ __global__ __launch_bounds__(RT * KS * 64) void k_ffn_gate_up_skinny(const GateU
   for (int i = threadIdx.x; i < 16 * NT * RT; i += S::kThreads) {
     const int m = i / RT, jj = 8 * (i % RT);
     const bool on = m < nt && j0 + jj < a.I;
-    float g[8], u[8];
+    float g[8], u[8], bias[16];
+    load_bias8(a, j0 + jj, bias);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       g[q] = S::sum(red, jj + q, m);
       u[q] = S::sum(red, NJ + jj + q, m);
     }
-    if (on) finish8(a, t0 + m, j0 + jj, g, u);
+    if (on) finish8(a, t0 + m, j0 + jj, bias, g, u);
     store_h8<FP8>(a, t0 + m, j0 + jj, on, g);
   }
 }
@@ -297,9 +305,10 @@ hipError_t launch_tiled(const GateUpArgs& g, const FfnProduct& d, hipStream_t s)
   const int64_t n = (int64_t)((g.I + S::BA / 2 - 1) / (S::BA / 2)) * ((g.T + S::BB - 1) / S::BB);
   hipError_t e = with_kind(g.layout, g.act.act, [&](auto l, auto c) {
     auto* k = &k_ffn_gate_up<S, FP8, decltype(l)::value, decltype(c)::value>;
-    hipError_t r = allow_lds(k, S::kLds);
+    constexpr int kBytes = FP8 ? S::kLdsMx : S::kLds;
+    hipError_t r = allow_lds(k, kBytes);
     if (r != hipSuccess) return r;
-    k<<<(uint32_t)n, S::kThreads, S::kLds, s>>>(g);
+    k<<<(uint32_t)n, S::kThreads, kBytes, s>>>(g);
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
