@@ -51,11 +51,19 @@ struct Operand {
   const uint8_t* s;
   int64_t ld;
   int rows;
+  // the same operand from k-tile kt on
+  __device__ __forceinline__ Operand from_row(int kt) const {
+    return {static_cast<const uint8_t*>(p) + (int64_t)kt * 128, s, ld, rows};
+  }
+  __device__ __forceinline__ Operand from_col(int kt) const {
+    return {static_cast<const uint8_t*>(p) + (int64_t)kt * 128 * ld, s, ld, rows};
+  }
 };
 
 template <int WA_, int WB_, int TA_, int TB_>
 struct TileShape {
   static constexpr int WA = WA_, WB = WB_, TA = TA_, TB = TB_;
+  static constexpr bool kSplits = TA * TB < 8;   // whether k may be cut (few tiles: small ones)
   static constexpr int BA = WA * TA * 32, BB = WB * TB * 32;
   static constexpr int kWaves = WA * WB, kThreads = kWaves * 64;
   static constexpr int kLds = 2 * (BA + BB) * 128;   // the stages, of either kind
@@ -63,6 +71,18 @@ struct TileShape {
 };
 using Tile256 = TileShape<2, 4, 4, 2>;   // 256 x 256, eight waves, one workgroup per CU
 using Tile128 = TileShape<2, 2, 2, 2>;   // 128 x 128, four waves, two workgroups per CU
+
+// Part s of S of a product's k axis, in whole k-tiles of 128 bytes: the first one, and how many
+// elements of k the part has. A product with too few tiles for the chip is cut along k; the
+// parts' fp32 sums are joined, in their order, by a launch of their own.
+struct KPart {
+  int kt0, K;
+  __device__ __forceinline__ KPart(int K_, int es, int s, int S) {
+    const int per = 128 / es, nk = (K_ + per - 1) / per;
+    kt0 = (int)((int64_t)nk * s / S);
+    K = min((int)((int64_t)nk * (s + 1) / S) * per, K_) - kt0 * per;
+  }
+};
 
 // Tile (ia, ib) of workgroup id among na x nb: ids that run together on one XCD (a
 // contiguous run of the remapped id) form blocks of kGroup b-tiles, b fastest, so that the 32
@@ -208,11 +228,19 @@ struct Reader {
   }
 };
 
+// The scales of both MXFP8 operands: bytes in all, blocks of a whole row, and the block that the
+// loop's k begins with.
+struct MxScales {
+  const uint8_t *sa, *sb;
+  int64_t na, nb;
+  int pitch, first;
+};
+
 // e8m0 scales of both MXFP8 operands: thread t of the workgroup reads those of tile row t (A's
 // rows, then B's), two k-tiles' (4 bytes) at a time, and the waves take them from LDS, where
 // each row's lie as one dword. Read by every wave for its own rows they were fetched three
 // times over, a gather of 32 rows to an instruction, and took the memory pipeline longer than
-// the operands did (2048 tokens at H = I = 2880: MX_FIGURES).
+// the operands did (gate/up of 2048 tokens at H = I = 2880: 57 us, and 50 through LDS).
 // The 4 bytes start at any byte, so the two dwords around them are loaded and shifted into
 // one. The last dword may reach up to 3 bytes past the scales' end (never past the aligned
 // dword that holds their last byte). Blocks past the row's end (their codes are zeros) take
@@ -222,19 +250,18 @@ struct ScaleStage {
   static_assert(S::kThreads == S::BA + S::BB, "a thread for every row");
   static constexpr int kBytes = S::kThreads * 4;   // of a pair of k-tiles
   rsrc_t r;
-  int nb;            // blocks of a row
-  uint32_t off;      // byte of the row's first scale
+  int nb;            // blocks of a row that the loop runs over
+  uint32_t off;      // byte of the first of them
   u32x2 raw;
   template <typename RowA, typename RowB>
-  __device__ __forceinline__ void init(const uint8_t* sa, int64_t na, const uint8_t* sb, int64_t nbytes,
-                                       int blocks, RowA row_a, RowB row_b) {
+  __device__ __forceinline__ void init(const MxScales& m, int blocks, RowA row_a, RowB row_b) {
     // whole waves belong to one operand
     const int t = threadIdx.x;
     const bool is_a = __builtin_amdgcn_readfirstlane(wave_id()) * 64 < S::BA;
-    r = make_rsrc_uniform(is_a ? sa : sb, (uint32_t)(((is_a ? na : nbytes) + 3) & ~(int64_t)3));
+    r = make_rsrc_uniform(is_a ? m.sa : m.sb, (uint32_t)(((is_a ? m.na : m.nb) + 3) & ~(int64_t)3));
     nb = blocks;
     const int row = is_a ? row_a(t) : row_b(t - S::BA);
-    off = row >= 0 ? (uint32_t)row * nb : (uint32_t)kOob;
+    off = row >= 0 ? (uint32_t)row * m.pitch + m.first : (uint32_t)kOob;
   }
   __device__ __forceinline__ void load(int pair) {
     raw = __builtin_bit_cast(
@@ -255,14 +282,6 @@ struct ScaleStage {
   }
 };
 
-template <bool FP8>
-struct MxState {};
-template <>
-struct MxState<true> {
-  const uint8_t *sa, *sb;   // scales
-  int64_t na, nb;           // their bytes
-};
-
 constexpr int row_bytes(bool fp8) { return fp8 ? 64 : 128; }
 template <typename S, int MODE, int N, bool FP8>
 using OpLoader = Loader<MODE, N, S::kThreads, row_bytes(FP8)>;
@@ -274,7 +293,7 @@ template <typename S, int MA, int MB, bool FP8, typename RowA, typename RowB>
 __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* lds,
                                           OpLoader<S, MA, S::BA, FP8>& la,
                                           OpLoader<S, MB, S::BB, FP8>& lb, int K,
-                                          const MxState<FP8>& mx, RowA row_a, RowB row_b) {
+                                          const MxScales& mx, RowA row_a, RowB row_b) {
   constexpr int kRb = row_bytes(FP8), kSub = 128 / kRb;   // k-tiles of 128 bytes of k
   constexpr int kSteps = FP8 ? 1 : 4, kStages = 2 * kSub;
   constexpr int kStage = (S::BA + S::BB) * kRb;
@@ -318,7 +337,7 @@ __device__ __forceinline__ void gemm_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* 
   if constexpr (FP8) {
     // both before the operands' loads: the loop then finds as many loads behind the scales'
     // as it issues itself, and does not wait for more of them
-    sc.init(mx.sa, mx.na, mx.sb, mx.nb, K / 32, row_a, row_b);
+    sc.init(mx, K / 32, row_a, row_b);
     sc.load(0);
     first = sc.raw;
     sc.load(1);

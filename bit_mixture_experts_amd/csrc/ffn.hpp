@@ -99,33 +99,46 @@ struct FfnProduct {
   int add_dtype;
   void* out;
   int out_dtype;
+  int splits;           // parts of k; 1: the tile's epilogue finishes the output
+  float* part;          // [splits][nb][na] sums to be joined
 };
 
 template <typename S, int MA, int MB, bool FP8>
-__device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, int ib,
+__device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, int ib, int split,
                                                  uint8_t* lds) {
   const int a0 = ia * S::BA, b0 = ib * S::BB;
   OpLoader<S, MA, S::BA, FP8> la;
   OpLoader<S, MB, S::BB, FP8> lb;
   constexpr int es = FP8 ? 1 : 2;
+  const KPart k(p.K, es, split, S::kSplits ? p.splits : 1);
   if constexpr (MA == kOpRow) {
     const int n = min(S::BA, p.na - a0);
-    la.init_row(p.A, es, p.K, a0, n, [=](int r) { return r < n ? r : -1; });
+    la.init_row(p.A.from_row(k.kt0), es, k.K, a0, n, [=](int r) { return r < n ? r : -1; });
   } else {
-    la.init_col(p.A, p.K, a0);
+    la.init_col(p.A.from_col(k.kt0), k.K, a0);
   }
   if constexpr (MB == kOpRow) {
     const int n = min(S::BB, p.nb - b0);
-    lb.init_row(p.B, es, p.K, b0, n, [=](int r) { return r < n ? r : -1; });
+    lb.init_row(p.B.from_row(k.kt0), es, k.K, b0, n, [=](int r) { return r < n ? r : -1; });
   } else {
-    lb.init_col(p.B, p.K, b0);
+    lb.init_col(p.B.from_col(k.kt0), k.K, b0);
   }
-  MxState<FP8> mx;
-  if constexpr (FP8) mx = {p.A.s, p.B.s, p.na_s, p.nb_s};
+  const MxScales mx = {p.A.s, p.B.s, p.na_s, p.nb_s, p.K / 32, k.kt0 * 4};
   f32x16 acc[S::TA][S::TB];
   gemm_loop<S, MA, MB, FP8>(
-      acc, lds, la, lb, p.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
+      acc, lds, la, lb, k.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
       [&](int r) { return b0 + r < p.nb ? b0 + r : -1; });
+  if constexpr (S::kSplits) {
+    if (p.splits > 1) {
+      float* part = p.part + (int64_t)split * p.nb * p.na;
+      for_each8<S, false, 1>(acc, lds, [](int, int) { return NoPre{}; },
+                             [&](int row, int a, float* v, const NoPre&) {
+        const int b = b0 + row, c = a0 + a;
+        if (b < p.nb && c < p.na) store8_f32(part + (int64_t)b * p.na + c, v);
+      });
+      return;
+    }
+  }
   const bool add32 = p.add_dtype == MOE4_DTYPE_F32;
   float bias[8] = {};   // the same columns in every turn
   if (const int c = a0 + lane_a<S, false>(); p.bias && c < p.na) load8_bf16(p.bias + c, bias);
@@ -166,8 +179,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_product(const FfnProduct
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
   const int na = (p.na + S::BA - 1) / S::BA, nb = (p.nb + S::BB - 1) / S::BB;
   int ia, ib;
-  tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
-  ffn_product_tile<S, MA, MB, FP8>(p, ia, ib, stage_mem);
+  const int id = xcd_remap(blockIdx.x, gridDim.x), tile = id % (na * nb);
+  tile_of(tile, na, nb, ia, ib);
+  ffn_product_tile<S, MA, MB, FP8>(p, ia, ib, id / (na * nb), stage_mem);
 }
 
 // f(layout, activation) as compile-time constants
@@ -181,6 +195,23 @@ inline hipError_t with_kind(int layout, int act, F f) {
   return act == MOE4_ACT_SWIGLU ? f(N{}, S{}) : f(N{}, C{});
 }
 
+// Which tiles, by rounds of the chip: a round is 256 tiles of 256 x 256 or 512 of 128 x 128,
+// and one of the small tiles takes two thirds of one of the large (half the work, at three
+// quarters of the rate: each LDS operand feeds half as many MFMAs). Few tokens or a ragged last
+// round go to the small ones. Both sides, large and small tiles, in us: 512 tokens at H 4096, I
+// 8192 271 and 184; 2048 at 2880, 2880 136 and 129; 4096 at 2048, 768 73 and 55; 8192 in
+// MXFP8 at 2880, 2880 283 and 350.
+template <typename S>
+inline int64_t tiles_of(int64_t na, int64_t nb) {
+  return ((na + S::BA - 1) / S::BA) * ((nb + S::BB - 1) / S::BB);
+}
+inline bool large_tiles(int64_t n256, int64_t n128) {
+  return 3 * ((n256 + 255) / 256) <= 2 * ((n128 + 511) / 512);
+}
+inline bool large_tiles_for(int64_t na, int64_t nb) {
+  return large_tiles(tiles_of<Tile256>(na, nb), tiles_of<Tile128>(na, nb));
+}
+
 // dynamic LDS above 64 KiB has to be asked for once per kernel and device
 template <typename K>
 inline hipError_t allow_lds(K* kernel, int bytes) {
@@ -189,9 +220,29 @@ inline hipError_t allow_lds(K* kernel, int bytes) {
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// Parts of k for n tiles of 128 x 128 that leave most of a round (512) empty: as many as fill it,
+// each with at least eight k-tiles of 128 bytes (a part's own first loads, the launch that joins
+// and its reads cost about as much as eight: 1024 tokens at H = I = 512 19 us whole and 25 in
+// parts of four). Us whole and in parts: 128 tokens at H 4096, I 8192 174 and 81, at 2880,
+// 2880 65 and 40; 512 tokens at 4096, 8192 184 and 142.
+inline int k_splits(int64_t n128, int K, int es) {
+  const int nk = (int)(((int64_t)K * es + 127) / 128);
+  const int64_t most = 512 / n128, long_enough = nk / 8;
+  const int64_t s = most < long_enough ? most : long_enough;
+  return s < 2 ? 1 : (int)(s < 16 ? s : 16);
+}
+
+// The sums of split products (those of up to three, one after another), with what their tiles'
+// epilogue would have added: 8 values of a row to a thread.
+struct JoinArgs {
+  FfnProduct p[3];
+  int first[4];   // first workgroup of each, and the end
+};
+hipError_t launch_join(JoinArgs a, int n, hipStream_t s);
+
 template <typename S, int MA, int MB, bool FP8>
 inline hipError_t launch_product(const FfnProduct& p, hipStream_t s) {
-  const int64_t n = (int64_t)((p.na + S::BA - 1) / S::BA) * ((p.nb + S::BB - 1) / S::BB);
+  const int64_t n = tiles_of<S>(p.na, p.nb) * p.splits;
   auto* k = &k_ffn_product<S, MA, MB, FP8>;
   constexpr int kBytes = FP8 ? S::kLdsMx : S::kLds;
   hipError_t e = allow_lds(k, kBytes);

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
   lb.init_row(a.dY, 2, a.H, t0, nt, [=](int r) { return r < nt ? r : -1; });
   f32x16 acc[S::TA][S::TB];
   gemm_loop<S, kOpCol, kOpRow, false>(
-      acc, stage_mem, la, lb, a.H, MxState<false>{}, [](int) { return -1; }, [](int) { return -1; });
+      acc, stage_mem, la, lb, a.H, MxScales{}, [](int) { return -1; }, [](int) { return -1; });
   constexpr bool halves = LAYOUT == MOE4_GU_HALVES;
   const FfnAct act = {ACT, a.act.alpha, a.act.limit};
   // where the lane's two runs of 8 pre-activations start in a row
@@ -130,17 +130,14 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_grads(const GradArgs a) 
   const int q = (int)blockIdx.x < a.first[1] ? 0 : (int)blockIdx.x < a.first[2] ? 1 : 2;
   const FfnProduct& p = a.p[q];
   const int na = (p.na + S::BA - 1) / S::BA, nb = (p.nb + S::BB - 1) / S::BB;
-  const int id = blockIdx.x - a.first[q];
-  if (id >= na * nb) return;
+  int id = blockIdx.x - a.first[q];
+  if (id >= na * nb * p.splits) return;
+  id = xcd_remap(id, na * nb * p.splits);
   int ia, ib;
-  tile_of(xcd_remap(id, na * nb), na, nb, ia, ib);
-  if (a.col_b[q]) ffn_product_tile<S, kOpCol, kOpCol, false>(p, ia, ib, stage_mem);
-  else ffn_product_tile<S, kOpCol, kOpRow, false>(p, ia, ib, stage_mem);
-}
-
-template <typename S>
-int64_t tiles_of(const FfnProduct& p) {
-  return (int64_t)((p.na + S::BA - 1) / S::BA) * ((p.nb + S::BB - 1) / S::BB);
+  tile_of(id % (na * nb), na, nb, ia, ib);
+  const int split = id / (na * nb);
+  if (a.col_b[q]) ffn_product_tile<S, kOpCol, kOpCol, false>(p, ia, ib, split, stage_mem);
+  else ffn_product_tile<S, kOpCol, kOpRow, false>(p, ia, ib, split, stage_mem);
 }
 
 template <typename S>
@@ -150,7 +147,7 @@ hipError_t launch_grads(GradArgs a, int n, hipStream_t s) {
   if (e != hipSuccess) return e;
   a.first[0] = 0;
   for (int i = 0; i < 3; ++i)
-    a.first[i + 1] = a.first[i] + (i < n ? (int)((tiles_of<S>(a.p[i]) + 7) / 8 * 8) : 0);
+    a.first[i + 1] = a.first[i] + (i < n ? (int)((tiles_of<S>(a.p[i].na, a.p[i].nb) * a.p[i].splits + 7) / 8 * 8) : 0);
   k<<<a.first[3], S::kThreads, S::kLds, s>>>(a);
   return hipGetLastError();
 }
@@ -197,21 +194,37 @@ hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
   auto* k = &k_ffn_dh<S, LAYOUT, ACT>;
   hipError_t e = allow_lds(k, S::kLds);
   if (e != hipSuccess) return e;
-  const int64_t n = (int64_t)((a.I + S::BA - 1) / S::BA) * ((a.T + S::BB - 1) / S::BB);
-  k<<<(uint32_t)n, S::kThreads, S::kLds, s>>>(a);
+  k<<<(uint32_t)tiles_of<S>(a.I, a.T), S::kThreads, S::kLds, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// workspace: dGU, h, the partial sums of the two biases' gradients
+// workspace: dGU, h, the partial sums of the two biases' gradients and of products that are
+// split along k: those whose reduction is longer than the share of a workgroup, where all the
+// products' tiles leave most of a round empty
 struct BwdWs {
-  size_t h, part_gu, part_dn, end;
+  size_t h, part_gu, part_dn, part[3], end;
+  int splits[3];   // dX, dW_gu, dW_dn
   BwdWs(const moe4_ffn& f, int64_t T) {
     h = align_up((size_t)T * 2 * f.I * 2, 256);
     part_gu = h + align_up((size_t)T * f.I * 2, 256);
     part_dn = part_gu + align_up((size_t)((T + 127) / 128) * 2 * f.I * 4, 256);
     end = part_dn + align_up((size_t)kColParts * f.H * 4, 256);
+    const int64_t size[3][3] = {{f.H, T, 2 * (int64_t)f.I}, {f.H, 2 * (int64_t)f.I, T}, {f.I, f.H, T}};
+    int64_t tiles = 0, work = 0;   // k-tiles of 64
+    for (const auto& z : size) {
+      const int64_t n = tiles_of<Tile128>(z[0], z[1]);
+      tiles += n;
+      work += n * ((z[2] + 63) / 64);
+    }
+    const int64_t share = (work + 511) / 512 > 8 ? (work + 511) / 512 : 8;
+    for (int i = 0; i < 3; ++i) {
+      const int64_t s = tiles >= 384 ? 1 : ((size[i][2] + 63) / 64) / share;
+      splits[i] = s < 2 ? 1 : (int)(s < 32 ? s : 32);
+      part[i] = end;
+      if (splits[i] > 1) end += align_up((size_t)splits[i] * size[i][0] * size[i][1] * 4, 256);
+    }
   }
 };
 
@@ -233,7 +246,7 @@ hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, cons
     DhArgs a = {{f.w_dn, nullptr, I, I}, {dy, nullptr, H, T}, T, H, I,
                 {f.act, f.act_alpha, f.act_limit}, gu, dgu, dw_dn ? h : nullptr,
                 db_gu ? part_gu : nullptr};
-    const bool big = (int64_t)((I + 255) / 256) * ((T + 255) / 256) >= 192;
+    const bool big = large_tiles_for(I, T);
     e = with_kind(f.gu_layout, f.act, [&](auto l, auto c) {
       constexpr int L = decltype(l)::value, A = decltype(c)::value;
       return big ? launch_dh<Tile256, L, A>(a, s) : launch_dh<Tile128, L, A>(a, s);
@@ -247,7 +260,12 @@ hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, cons
   }
   GradArgs g = {};
   int n = 0;
-  auto put = [&](const FfnProduct& p, bool col_b) {
+  JoinArgs join = {};
+  int joins = 0;
+  auto put = [&](FfnProduct p, int which, bool col_b) {
+    p.splits = at.splits[which];
+    p.part = reinterpret_cast<float*>(w8 + at.part[which]);
+    if (p.splits > 1) join.p[joins++] = p;
     // longest reduction first
     int i = n++;
     for (; i > 0 && g.p[i - 1].K < p.K; --i) {
@@ -259,17 +277,22 @@ hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, cons
   };
   if (dx)
     put({{f.w_gu, nullptr, H, H}, {dgu, nullptr, 2 * I, T}, 0, 0, 2 * I, H, T, nullptr, add,
-         add_dtype, dx, dx_dtype}, false);
+         add_dtype, dx, dx_dtype}, 0, false);
   if (dw_gu)
     put({{x, nullptr, H, H}, {dgu, nullptr, 2 * I, 2 * I}, 0, 0, T, H, 2 * I, nullptr, nullptr, 0,
-         dw_gu, dw_dtype}, true);
+         dw_gu, dw_dtype}, 1, true);
   if (dw_dn)
     put({{h, nullptr, I, I}, {dy, nullptr, H, H}, 0, 0, T, I, H, nullptr, nullptr, 0, dw_dn,
-         dw_dtype}, true);
+         dw_dtype}, 2, true);
   if (n) {
-    int64_t big = 0;
-    for (int i = 0; i < n; ++i) big += tiles_of<Tile256>(g.p[i]);
-    e = big >= 192 ? launch_grads<Tile256>(g, n, s) : launch_grads<Tile128>(g, n, s);
+    int64_t n256 = 0, n128 = 0;
+    for (int i = 0; i < n; ++i) {
+      n256 += tiles_of<Tile256>(g.p[i].na, g.p[i].nb);
+      n128 += tiles_of<Tile128>(g.p[i].na, g.p[i].nb);
+    }
+    e = joins == 0 && large_tiles(n256, n128) ? launch_grads<Tile256>(g, n, s)
+                                              : launch_grads<Tile128>(g, n, s);
+    if (e == hipSuccess && joins) e = launch_join(join, joins, s);
     if (e != hipSuccess) return e;
   }
   return db_dn ? col_sums(dy, T, H, part_dn, db_dn, dw_dtype, s) : hipSuccess;

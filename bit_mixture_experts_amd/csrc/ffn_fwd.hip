@@ -17,6 +17,8 @@ struct GateUpArgs {
   float* save_gu;
   uint16_t* h;            // bf16 [T, I]
   uint8_t *hq, *hs;       // MXFP8 [T, I], [T, I / 32]
+  int splits;             // parts of k
+  float* part;            // [splits][T][2][I] sums of gates and ups to be joined
 };
 
 // element of row t of save_gu that pair j's gate (or, with `up`, up) value has
@@ -97,19 +99,35 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(GateUpArgs a) {
   constexpr int kPairs = S::BA / 2, es = FP8 ? 1 : 2;
   const int na = (a.I + kPairs - 1) / kPairs, nb = (a.T + S::BB - 1) / S::BB;
   int ia, ib;
-  tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
+  const int id = xcd_remap(blockIdx.x, gridDim.x), split = id / (na * nb);
+  tile_of(id % (na * nb), na, nb, ia, ib);
   const int j0 = ia * kPairs, t0 = ib * S::BB;
   const int nt = min(S::BB, a.T - t0);
   OpLoader<S, kOpRow, S::BA, FP8> la;
   OpLoader<S, kOpRow, S::BB, FP8> lb;
-  la.init_row(a.W, es, a.H, 0, 2 * a.I, [&](int r) { return pair_row(a.layout, a.I, j0, r); });
-  lb.init_row(a.X, es, a.H, t0, nt, [=](int r) { return r < nt ? r : -1; });
-  MxState<FP8> mx;
-  if constexpr (FP8) mx = {a.W.s, a.X.s, a.w_s, a.x_s};
+  const KPart k(a.H, es, split, S::kSplits ? a.splits : 1);
+  la.init_row(a.W.from_row(k.kt0), es, k.K, 0, 2 * a.I,
+              [&](int r) { return pair_row(a.layout, a.I, j0, r); });
+  lb.init_row(a.X.from_row(k.kt0), es, k.K, t0, nt, [=](int r) { return r < nt ? r : -1; });
+  const MxScales mx = {a.W.s, a.X.s, a.w_s, a.x_s, a.H / 32, k.kt0 * 4};
   f32x16 acc[S::TA][S::TB];
   gemm_loop<S, kOpRow, kOpRow, FP8>(
-      acc, stage_mem, la, lb, a.H, mx, [&](int r) { return pair_row(a.layout, a.I, j0, r); },
+      acc, stage_mem, la, lb, k.K, mx, [&](int r) { return pair_row(a.layout, a.I, j0, r); },
       [&](int r) { return r < nt ? t0 + r : -1; });
+  if constexpr (S::kSplits) {
+    if (a.splits > 1) {
+      float* part = a.part + (int64_t)split * a.T * 2 * a.I;
+      for_each8<S, true, 1>(acc, stage_mem, [](int, int) { return NoPre{}; },
+                            [&](int row, int jj, float* g, float* u) {
+        const int j = j0 + jj;
+        if (row >= nt || j >= a.I) return;
+        float* o = part + (int64_t)(t0 + row) * 2 * a.I + j;
+        store8_f32(o, g);
+        store8_f32(o + a.I, u);
+      });
+      return;
+    }
+  }
   float bias[16];   // the same pairs in every turn
   load_bias8(a, j0 + lane_a<S, true>(), bias);
   for_each8<S, true, 1>(acc, stage_mem, [](int, int) { return NoPre{}; },
@@ -121,31 +139,92 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(GateUpArgs a) {
   });
 }
 
+// The parts of a split gate/up product, joined: 8 pairs of a token to a thread (four
+// neighbours share a block of MXFP8).
+template <bool FP8>
+__global__ __launch_bounds__(256) void k_ffn_gate_up_join(const GateUpArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = a.I / 8;
+  const int64_t t = i / per;
+  const int j = (int)(i - t * per) * 8;
+  const bool on = t < a.T;
+  float g[8] = {}, u[8] = {};
+  if (on) {
+    float bias[16];
+    load_bias8(a, j, bias);
+    for (int s = 0; s < a.splits; ++s) {
+      const float* p = a.part + ((int64_t)s * a.T + t) * 2 * a.I + j;
+      float x[8], y[8];
+      load8_f32(p, x);
+      load8_f32(p + a.I, y);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        g[q] += x[q];
+        u[q] += y[q];
+      }
+    }
+    finish8(a, (int)t, j, bias, g, u);
+  }
+  store_h8<FP8>(a, (int)t, j, on, g);
+}
+
+__global__ __launch_bounds__(256) void k_ffn_join(const JoinArgs a) {
+  const int q = (int)blockIdx.x < a.first[1] ? 0 : (int)blockIdx.x < a.first[2] ? 1 : 2;
+  const FfnProduct& p = a.p[q];
+  const int64_t at = ((int64_t)(blockIdx.x - a.first[q]) * 256 + threadIdx.x) * 8;
+  if (at >= (int64_t)p.nb * p.na) return;
+  const int c = (int)(at % p.na);
+  float v[8] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    float x[8];
+    load8_f32(p.part + (int64_t)s * p.nb * p.na + at, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+  if (p.bias) {
+    float x[8];
+    load8_bf16(p.bias + c, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+  if (p.add) {
+    float x[8];
+    load8_dt(p.add, p.add_dtype, at, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+  store8_dt(p.out, p.out_dtype, at, v);
+}
+
 // ------------------------------------------------------------- few tokens
 
 // A decode step reads every weight for a handful of tokens, so the kernel is a stream of the
-// weights: one workgroup takes 16 RT weight rows, its KS groups of RT waves split K, and each
-// wave multiplies its 16 rows with NT tiles of 16 tokens on 16x16 MFMAs (weights as the first
+// weights: one workgroup takes 16 RT weight rows and its KS waves split K; each multiplies
+// the RT tiles of 16 rows with NT tiles of 16 tokens on 16x16 MFMAs (weights as the first
 // operand: a lane ends with 4 weight rows of one token). Loads of the next batch of steps
 // (128 bytes of a row each) are in flight while one is multiplied; the partial sums meet in
-// LDS, in the order of the K splits.
+// LDS, in the order of the K splits. What bounds it at these sizes is the number of load
+// instructions of a CU (each touches 16 rows), so a wave keeps its tokens' operands for all
+// its row tiles and asks for nothing past its range.
 template <int RT, int KS, int NT, bool FP8>
 struct Skinny {
-  static constexpr int kThreads = RT * KS * 64;
+  static constexpr int kThreads = KS * 64;
   static constexpr int kLds = KS * RT * NT * 256 * 4;
-  static constexpr int kU = 4 / NT;   // steps of a batch: the same registers for any NT
+  // steps of a batch: about the same registers for any shape
+  static constexpr int kU = RT + NT >= 5 ? 1 : 8 / (RT + NT);
 
   struct Batch {
-    u32x4 w[kU][2], x[kU][NT][2];
-    uint32_t ws[FP8 ? kU : 1], xs[FP8 ? kU : 1][NT];
+    u32x4 w[kU][RT][2], x[kU][NT][2];
+    uint32_t ws[FP8 ? kU : 1][RT], xs[FP8 ? kU : 1][NT];
   };
 
-  // row: the lane's weight row or -1; sums in red[ks][rt][nt][256]
-  static __device__ __forceinline__ void run(const Operand& W, int64_t wrows, int row,
+  // row_of(rt): the weight row of this lane in row tile rt, or -1; sums in red[ks][rt][nt][256]
+  template <typename RowOf>
+  static __device__ __forceinline__ void run(const Operand& W, int64_t wrows, RowOf row_of,
                                              const Operand& X, int t0, int nt, int K,
                                              float* red) {
-    const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-    const int rt = w % RT, ks = w / RT, n = l & 15, g = l >> 4;
+    const int ks = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+    const int n = l & 15, g = l >> 4;
     const int kb = FP8 ? K : 2 * K;    // bytes of a row
     const int nb = K / 32;
     const rsrc_t rw = make_rsrc_uniform(W.p, (uint32_t)(wrows * kb));
@@ -154,9 +233,13 @@ struct Skinny {
     const rsrc_t rws = make_rsrc_uniform(W.s, FP8 ? (uint32_t)(wrows * nb) : 0u);
     const rsrc_t rxs = make_rsrc_uniform(FP8 ? X.s + (int64_t)t0 * nb : X.s,
                                          FP8 ? (uint32_t)(nt * nb) : 0u);
-    const uint32_t wo = row >= 0 ? (uint32_t)row * kb : (uint32_t)kOob;
-    const uint32_t wso = row >= 0 ? (uint32_t)row * nb : (uint32_t)kOob;
-    uint32_t xo[NT], xso[NT];
+    uint32_t wo[RT], wso[RT], xo[NT], xso[NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = row_of(i);
+      wo[i] = r >= 0 ? (uint32_t)r * kb : (uint32_t)kOob;
+      wso[i] = r >= 0 ? (uint32_t)r * nb : (uint32_t)kOob;
+    }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int t = 16 * i + n;
@@ -173,8 +256,11 @@ struct Skinny {
       for (int i = 0; i < kU; ++i) {
         const int k = 128 * (s + i);
         const bool in0 = s + i < s1 && k + p0 < kb, in1 = s + i < s1 && k + p1 < kb;
-        b.w[i][0] = buf_load_b128(rw, in0 ? (int)(wo + k + p0) : kOob);
-        b.w[i][1] = buf_load_b128(rw, in1 ? (int)(wo + k + p1) : kOob);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          b.w[i][j][0] = buf_load_b128(rw, in0 ? (int)(wo[j] + k + p0) : kOob);
+          b.w[i][j][1] = buf_load_b128(rw, in1 ? (int)(wo[j] + k + p1) : kOob);
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           b.x[i][j][0] = buf_load_b128(rx, in0 ? (int)(xo[j] + k + p0) : kOob);
@@ -183,15 +269,18 @@ struct Skinny {
         if constexpr (FP8) {
           const int blk = 4 * (s + i) + g;
           const bool on = s + i < s1 && blk < nb;
-          b.ws[i] = buf_load_u8(rws, on ? (int)(wso + blk) : kOob);
+#pragma unroll
+          for (int j = 0; j < RT; ++j) b.ws[i][j] = buf_load_u8(rws, on ? (int)(wso[j] + blk) : kOob);
 #pragma unroll
           for (int j = 0; j < NT; ++j) b.xs[i][j] = buf_load_u8(rxs, on ? (int)(xso[j] + blk) : kOob);
         }
       }
     };
-    f32x4 acc[NT];
+    f32x4 acc[RT][NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto join = [](u32x4 lo, u32x4 hi) {
       const auto v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       return __builtin_bit_cast(i32x8, v);
@@ -200,32 +289,48 @@ struct Skinny {
 #pragma unroll
       for (int i = 0; i < kU; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if constexpr (FP8) {
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                join(b.w[i][0], b.w[i][1]), join(b.x[i][j][0], b.x[i][j][1]), acc[j], 0, 0, 0,
-                (int)b.ws[i], 0, (int)b.xs[i][j]);
-          } else {
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(bf16x8, b.w[i][c]), __builtin_bit_cast(bf16x8, b.x[i][j][c]),
-                  acc[j], 0, 0, 0);
+          for (int j = 0; j < NT; ++j) {
+            if constexpr (FP8) {
+              acc[r][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  join(b.w[i][r][0], b.w[i][r][1]), join(b.x[i][j][0], b.x[i][j][1]), acc[r][j], 0,
+                  0, 0, (int)b.ws[i][r], 0, (int)b.xs[i][j]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, b.w[i][r][c]),
+                    __builtin_bit_cast(bf16x8, b.x[i][j][c]), acc[r][j], 0, 0, 0);
+            }
           }
-        }
     };
-    // steps past s1 load zeros
+    // (a batch that follows is asked for in straight line with the one before it: behind a
+    // branch of its own the compiler would wait for all loads in flight)
     Batch b0, b1;
-    load(b0, s0);
-    for (int s = s0; s < s1; s += 2 * kU) {
+    int s = s0;
+    load(b0, s);
+    for (;;) {
+      if (s + kU >= s1) {
+        mul(b0);
+        break;
+      }
       load(b1, s + kU);
       mul(b0);
-      load(b0, s + 2 * kU);
+      s += kU;
+      if (s + kU >= s1) {
+        mul(b1);
+        break;
+      }
+      load(b0, s + kU);
       mul(b1);
+      s += kU;
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<f32x4*>(red + ((ks * RT + rt) * NT + j) * 256 + l * 4) = acc[j];
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        *reinterpret_cast<f32x4*>(red + ((ks * RT + i) * NT + j) * 256 + l * 4) = acc[i][j];
     __syncthreads();
   }
 
@@ -240,15 +345,18 @@ struct Skinny {
 };
 
 template <int RT, int KS, int NT, bool FP8>
-__global__ __launch_bounds__(RT * KS * 64) void k_ffn_gate_up_skinny(const GateUpArgs a) {
+__global__ __launch_bounds__(KS * 64) void k_ffn_gate_up_skinny(const GateUpArgs a) {
   using S = Skinny<RT, KS, NT, FP8>;
   extern __shared__ __attribute__((aligned(16))) float red[];
   constexpr int NJ = 8 * RT;   // pairs of the workgroup: gate rows first, then up rows
   const int j0 = blockIdx.x * NJ, t0 = blockIdx.y * 16 * NT, nt = min(16 * NT, a.T - t0);
-  const int r = 16 * (wave_id() % RT) + (lane_id() & 15);
-  const int jr = j0 + (r < NJ ? r : r - NJ);
-  S::run(a.W, 2 * (int64_t)a.I, jr < a.I ? gu_col(a.layout, a.I, jr, r >= NJ) : -1, a.X, t0, nt,
-         a.H, red);
+  S::run(
+      a.W, 2 * (int64_t)a.I,
+      [&](int rt) {
+        const int r = 16 * rt + (lane_id() & 15), j = j0 + (r < NJ ? r : r - NJ);
+        return j < a.I ? gu_col(a.layout, a.I, j, r >= NJ) : -1;
+      },
+      a.X, t0, nt, a.H, red);
   // 8 pairs of a token to a thread; NJ = 32 gives a block of MXFP8 to four neighbours
   for (int i = threadIdx.x; i < 16 * NT * RT; i += S::kThreads) {
     const int m = i / RT, jj = 8 * (i % RT);
@@ -266,12 +374,17 @@ __global__ __launch_bounds__(RT * KS * 64) void k_ffn_gate_up_skinny(const GateU
 }
 
 template <int RT, int KS, int NT, bool FP8>
-__global__ __launch_bounds__(RT * KS * 64) void k_ffn_down_skinny(const FfnProduct p) {
+__global__ __launch_bounds__(KS * 64) void k_ffn_down_skinny(const FfnProduct p) {
   using S = Skinny<RT, KS, NT, FP8>;
   extern __shared__ __attribute__((aligned(16))) float red[];
   const int a0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * 16 * NT, nt = min(16 * NT, p.nb - t0);
-  const int r = a0 + 16 * (wave_id() % RT) + (lane_id() & 15);
-  S::run(p.A, p.na, r < p.na ? r : -1, p.B, t0, nt, p.K, red);
+  S::run(
+      p.A, p.na,
+      [&](int rt) {
+        const int r = a0 + 16 * rt + (lane_id() & 15);
+        return r < p.na ? r : -1;
+      },
+      p.B, t0, nt, p.K, red);
   for (int i = threadIdx.x; i < 16 * NT * 16 * RT; i += S::kThreads) {
     const int m = i / (16 * RT), c = i % (16 * RT);
     if (m >= nt || a0 + c >= p.na) continue;
@@ -286,58 +399,134 @@ __global__ __launch_bounds__(RT * KS * 64) void k_ffn_down_skinny(const FfnProdu
   }
 }
 
+// Row tiles of a workgroup of the bf16 kernels and of the second product: a wave's loads are 2 RT
+// for weights and 2 NT for tokens a step, so more row tiles save token loads, as long as
+// there is a workgroup for most CUs. Us at 16, 64 tokens, H 4096, I 8192: one row tile 60,
+// 119; by this rule 51, 90.
+// (Four with 64 tokens would not fit the registers.)
+template <int NT, typename F>
+hipError_t with_row_tiles(int64_t rows, F f) {
+  if constexpr (NT < 4)
+    if (rows >= 64 * 192) return f(std::integral_constant<int, 4>{});
+  if (rows >= 32 * 192) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1>{});
+}
+
 template <int NT, bool FP8>
 hipError_t launch_skinny(const GateUpArgs& g, const FfnProduct& d, hipStream_t s) {
-  constexpr int kRt = FP8 ? 4 : 1, kKs = !FP8 ? 8 : NT == 1 ? 4 : 2;
-  using G = Skinny<kRt, kKs, NT, FP8>;
-  using D = Skinny<1, 8, NT, FP8>;
   const uint32_t nt = (g.T + 16 * NT - 1) / (16 * NT);
-  k_ffn_gate_up_skinny<kRt, kKs, NT, FP8>
-      <<<dim3((g.I + 8 * kRt - 1) / (8 * kRt), nt), G::kThreads, G::kLds, s>>>(g);
-  hipError_t e = hipGetLastError();
+  auto gate_up = [&](auto rc) {
+    // MXFP8: h is quantised in blocks of 32, so a workgroup takes 32 pairs
+    constexpr int kRt = FP8 ? 4 : decltype(rc)::value, kKs = FP8 && NT == 1 ? 12 : 8;
+    using G = Skinny<kRt, kKs, NT, FP8>;
+    auto* k = &k_ffn_gate_up_skinny<kRt, kKs, NT, FP8>;
+    hipError_t e = allow_lds(k, G::kLds);
+    if (e != hipSuccess) return e;
+    k<<<dim3((g.I + 8 * kRt - 1) / (8 * kRt), nt), G::kThreads, G::kLds, s>>>(g);
+    return hipGetLastError();
+  };
+  hipError_t e;
+  if constexpr (FP8) e = gate_up(std::integral_constant<int, 4>{});
+  else e = with_row_tiles<NT>(2 * (int64_t)g.I, gate_up);
   if (e != hipSuccess) return e;
-  k_ffn_down_skinny<1, 8, NT, FP8><<<dim3((d.na + 15) / 16, nt), D::kThreads, D::kLds, s>>>(d);
-  return hipGetLastError();
+  return with_row_tiles<NT>(d.na, [&](auto rc) {
+    constexpr int kRt = decltype(rc)::value;
+    using D = Skinny<kRt, 8, NT, FP8>;
+    auto* k = &k_ffn_down_skinny<kRt, 8, NT, FP8>;
+    hipError_t r = allow_lds(k, D::kLds);
+    if (r != hipSuccess) return r;
+    k<<<dim3((d.na + 16 * kRt - 1) / (16 * kRt), nt), D::kThreads, D::kLds, s>>>(d);
+    return hipGetLastError();
+  });
 }
 
 template <typename S, bool FP8>
-hipError_t launch_tiled(const GateUpArgs& g, const FfnProduct& d, hipStream_t s) {
-  const int64_t n = (int64_t)((g.I + S::BA / 2 - 1) / (S::BA / 2)) * ((g.T + S::BB - 1) / S::BB);
-  hipError_t e = with_kind(g.layout, g.act.act, [&](auto l, auto c) {
+hipError_t launch_gate_up(const GateUpArgs& g, hipStream_t s) {
+  return with_kind(g.layout, g.act.act, [&](auto l, auto c) {
     auto* k = &k_ffn_gate_up<S, FP8, decltype(l)::value, decltype(c)::value>;
     constexpr int kBytes = FP8 ? S::kLdsMx : S::kLds;
-    hipError_t r = allow_lds(k, kBytes);
-    if (r != hipSuccess) return r;
-    k<<<(uint32_t)n, S::kThreads, kBytes, s>>>(g);
+    hipError_t e = allow_lds(k, kBytes);
+    if (e != hipSuccess) return e;
+    k<<<(uint32_t)(tiles_of<S>(2 * (int64_t)g.I, g.T) * g.splits), S::kThreads, kBytes, s>>>(g);
     return hipGetLastError();
   });
-  if (e != hipSuccess) return e;
-  return launch_product<S, kOpRow, kOpRow, FP8>(d, s);
 }
 
 template <bool FP8>
 hipError_t launch_forward(const GateUpArgs& g, const FfnProduct& d, int variant, hipStream_t s) {
   if (variant == MOE4_VARIANT_SKINNY) {
     if (g.T <= 16) return launch_skinny<1, FP8>(g, d, s);
-    if (g.T <= 32) return launch_skinny<2, FP8>(g, d, s);
-    return launch_skinny<4, FP8>(g, d, s);
+    if constexpr (FP8) return launch_skinny<2, FP8>(g, d, s);
+    else return g.T <= 32 ? launch_skinny<2, FP8>(g, d, s) : launch_skinny<4, FP8>(g, d, s);
   }
-  const int64_t big = (int64_t)((g.I + 127) / 128) * ((g.T + 255) / 256);
-  if (big >= 192) return launch_tiled<Tile256, FP8>(g, d, s);
-  return launch_tiled<Tile128, FP8>(g, d, s);
+  hipError_t e;
+  if (g.splits > 1) {
+    e = launch_gate_up<Tile128, FP8>(g, s);
+    if (e != hipSuccess) return e;
+    k_ffn_gate_up_join<FP8><<<(uint32_t)(((int64_t)g.T * (g.I / 8) + 255) / 256), 256, 0, s>>>(g);
+    e = hipGetLastError();
+  } else {
+    e = large_tiles_for(2 * (int64_t)g.I, g.T) ? launch_gate_up<Tile256, FP8>(g, s)
+                                               : launch_gate_up<Tile128, FP8>(g, s);
+  }
+  if (e != hipSuccess) return e;
+  if (d.splits > 1) {
+    e = launch_product<Tile128, kOpRow, kOpRow, FP8>(d, s);
+    if (e != hipSuccess) return e;
+    JoinArgs j = {};
+    j.p[0] = d;
+    return launch_join(j, 1, s);
+  }
+  return large_tiles_for(d.na, d.nb) ? launch_product<Tile256, kOpRow, kOpRow, FP8>(d, s)
+                                     : launch_product<Tile128, kOpRow, kOpRow, FP8>(d, s);
 }
 
 }  // namespace
 
-size_t ffn_forward_ws_bytes(const moe4_ffn& f, int64_t T) {
-  if (f.format == MOE4_FFN_MXFP8)
-    return align_up((size_t)T * f.I, 256) + align_up((size_t)T * (f.I / 32), 256);
-  return align_up((size_t)T * f.I * 2, 256);
+hipError_t launch_join(JoinArgs a, int n, hipStream_t s) {
+  a.first[0] = 0;
+  for (int i = 0; i < 3; ++i)
+    a.first[i + 1] =
+        a.first[i] + (i < n ? (int)(((int64_t)a.p[i].nb * a.p[i].na / 8 + 255) / 256) : 0);
+  k_ffn_join<<<a.first[3], 256, 0, s>>>(a);
+  return hipGetLastError();
 }
+
+namespace {
+
+// workspace: h (and its scales), the partial sums of a product that is split along k (the two
+// products' follow each other in time and share the place)
+struct FwdWs {
+  int gate_splits, down_splits;
+  size_t scales, part, end;
+  FwdWs(const moe4_ffn& f, int64_t T) {
+    const bool mx = f.format == MOE4_FFN_MXFP8;
+    const int es = mx ? 1 : 2;
+    // (for either variant: the size does not change with the one that is pinned)
+    gate_splits = T > 0 ? k_splits(tiles_of<Tile128>(2 * (int64_t)f.I, T), f.H, es) : 1;
+    down_splits = T > 0 ? k_splits(tiles_of<Tile128>(f.H, T), f.I, es) : 1;
+    scales = align_up((size_t)T * f.I * es, 256);
+    part = scales + (mx ? align_up((size_t)T * (f.I / 32), 256) : 0);
+    const size_t g = gate_splits > 1 ? (size_t)gate_splits * T * 2 * f.I * 4 : 0;
+    const size_t d = down_splits > 1 ? (size_t)down_splits * T * f.H * 4 : 0;
+    end = part + align_up(g > d ? g : d, 256);
+  }
+};
+
+}  // namespace
+
+size_t ffn_forward_ws_bytes(const moe4_ffn& f, int64_t T) { return FwdWs(f, T).end; }
 
 int ffn_variant(const moe4_ffn& f, int64_t T) {
   if (f.variant != MOE4_VARIANT_AUTO) return f.variant;
-  return T <= 64 ? MOE4_VARIANT_SKINNY : MOE4_VARIANT_TILED;
+  // The skinny kernels read the weights once for every 64 tokens (MXFP8: 32), mostly from the
+  // caches, the tiled ones pay two or three launches of long tiles. Us, skinny and tiled: 128
+  // tokens at H 2048, I 768 (18.9 MB read) 19 and 26; 256 33 and 28; 256 at 512, 512 (6.3 MB) 11
+  // and 18, 1024 (25 MB) 24 and 19; 128 at 2880, 2880 (100 MB) 70 and 40.
+  const bool mx = f.format == MOE4_FFN_MXFP8;
+  const int64_t weights = 3 * (int64_t)f.H * f.I * (mx ? 1 : 2), at_once = mx ? 32 : 64;
+  return T <= 32 || (T + at_once - 1) / at_once * weights <= 20 << 20 ? MOE4_VARIANT_SKINNY
+                                                                      : MOE4_VARIANT_TILED;
 }
 
 hipError_t launch_ffn_forward(const moe4_ffn& f, const void* x, const uint8_t* x_s, int T,
@@ -346,7 +535,11 @@ hipError_t launch_ffn_forward(const moe4_ffn& f, const void* x, const uint8_t* x
                               hipStream_t s) {
   const bool mx = f.format == MOE4_FFN_MXFP8;
   uint8_t* w8 = static_cast<uint8_t*>(ws);
+  const FwdWs at(f, T);
+  float* part = reinterpret_cast<float*>(w8 + at.part);
   GateUpArgs g = {};
+  g.splits = at.gate_splits;
+  g.part = part;
   g.W = {f.w_gu, f.gu_s, f.H, 2 * f.I};
   g.X = {x, x_s, f.H, T};
   g.w_s = (int64_t)2 * f.I * (f.H / 32);
@@ -360,7 +553,7 @@ hipError_t launch_ffn_forward(const moe4_ffn& f, const void* x, const uint8_t* x
   g.save_gu = save_gu;
   if (mx) {
     g.hq = w8;
-    g.hs = w8 + align_up((size_t)T * f.I, 256);
+    g.hs = w8 + at.scales;
   } else {
     g.h = reinterpret_cast<uint16_t*>(w8);
   }
@@ -377,6 +570,8 @@ hipError_t launch_ffn_forward(const moe4_ffn& f, const void* x, const uint8_t* x
   d.add_dtype = residual_dtype;
   d.out = out;
   d.out_dtype = out_dtype;
+  d.splits = at.down_splits;
+  d.part = part;
   *variant = ffn_variant(f, T);
   return mx ? launch_forward<true>(g, d, *variant, s) : launch_forward<false>(g, d, *variant, s);
 }

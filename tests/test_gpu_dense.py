@@ -399,6 +399,16 @@ def test_ffn_forward_many_tiles(T, H, I, mx, clamped):
     ffn_check(blk, T, VARIANTS["auto"], BF, BF, not mx)
 
 
+@pytest.mark.parametrize("T,H,I,mx,clamped", [(70, 2056, 520, False, True), (130, 1032, 2072, False, False),
+                                              (97, 2080, 1056, True, True), (200, 1056, 2080, True, False),
+                                              (40, 4104, 136, False, True), (33, 8, 4104, False, False)])
+def test_ffn_forward_split_k(T, H, I, mx, clamped):
+    # few tiles and a long reduction: cut along k, ragged at the last part's end, and joined
+    blk = Block("split", H, I, mx, clamped, True)
+    ffn_check(blk, T, VARIANTS["tiled"], BF, BF, not mx)
+    ffn_check(blk, T, VARIANTS["tiled"], F32, None, False)
+
+
 def test_ffn_forward_in_place_residual():
     blk = Block("inplace", 264, 136)
     for T in (5, 200):
@@ -486,7 +496,8 @@ def test_ffn_backward(T, H, I, clamped, bias):
     ffn_backward_check(blk, T, F32, F32, add=T % 2 == 0)
 
 
-@pytest.mark.parametrize("T,H,I,clamped", [(4100, 1544, 264, True), (2050, 264, 2056, False), (9000, 520, 392, True)])
+@pytest.mark.parametrize("T,H,I,clamped", [(4100, 1544, 264, True), (2050, 264, 2056, False), (9000, 520, 392, True),
+                                         (4099, 136, 200, True), (2061, 392, 72, False)])
 def test_ffn_backward_many_tiles(T, H, I, clamped):
     blk = Block("bwd-big", H, I, False, clamped, True)
     ffn_backward_check(blk, T)
