@@ -11,7 +11,7 @@
 namespace moe4 {
 namespace {
 
-constexpr int kGradBatch = 128, kGradChunk = 8192, kGradParts = 1024;
+constexpr int kGradBatch = 128, kGradChunk = 8192, kGradParts = 2048;
 
 struct GradBatch {
   const void* in[kGradBatch];

@@ -378,7 +378,7 @@ int norm_blocks(int64_t T, int W) {
 // the backward's workgroups each leave a row of partial sums: fewer of them
 int norm_bwd_blocks(int64_t T, int W) {
   const int64_t rows = W == 1 ? (T + 3) / 4 : T;
-  const int64_t most = W == 16 ? 256 : 768;
+  const int64_t most = W == 16 ? 256 : 1024;
   return (int)(rows < most ? rows : most);
 }
 
