@@ -757,6 +757,71 @@ def test_graph_capture_of_the_dense_step():
             assert torch.equal(got[n], b[n]), (k, n)
 
 
+@pytest.mark.parametrize("T,H,I,mx", [(2600, 264, 2568, False), (2600, 288, 2592, True), (200, 2080, 544, True),
+                                      (20, 288, 160, True)])
+def test_graph_capture_of_every_kernel_family(T, H, I, mx):
+    # large tiles, split products, skinny kernels: captured without an eager call before
+    blk = Block("capture", H, I, mx, mx, True)
+    x, xs, _ = blk.tokens(T)
+    out, base = torch.zeros((T, H), dtype=BF, device=DEV), torch.zeros((T, H), dtype=BF, device=DEV)
+    ws = blk.ws(T)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe4.moe4_ffn_forward(blk.ffn, x, out, x_s=xs, ws=ws)
+    for k in range(3):
+        x2, xs2, _ = blk.tokens(T, k + 1)
+        x.copy_(x2)
+        if mx:
+            xs.copy_(xs2)
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        moe4.moe4_ffn_forward(blk.ffn, x, base, x_s=xs, ws=ws)
+        assert torch.equal(got, base)
+
+
+def test_offsets_past_32_bits():
+    # tensors of more than 2^32 bytes: the last rows are those of a call on them alone
+    H, T, tail = 2048, 1_060_000, 300
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((T, H), generator=gen, device=DEV, dtype=BF)
+    w = torch.ones(H, device=DEV)
+    out = torch.empty_like(x)
+    q, s = torch.empty((T, H), dtype=torch.uint8, device=DEV), torch.empty((T, H // 32), dtype=torch.uint8, device=DEV)
+    rstd = torch.empty(T, device=DEV)
+    moe4.moe4_add_rmsnorm(x, w, 1e-6, out=out, out_q=q, out_s=s, rstd=rstd)
+    xe = x[-tail:].clone()
+    o2, r2 = torch.empty_like(xe), torch.empty(tail, device=DEV)
+    q2, s2 = torch.empty((tail, H), dtype=torch.uint8, device=DEV), torch.empty((tail, H // 32), dtype=torch.uint8, device=DEV)
+    moe4.moe4_add_rmsnorm(xe, w, 1e-6, out=o2, out_q=q2, out_s=s2, rstd=r2)
+    # (another number of rows takes another split of the row's sum: bf16 steps apart at most)
+    assert torch.allclose(rstd[-tail:], r2, rtol=1e-5, atol=0)
+    assert torch.allclose(out[-tail:].float(), o2.float(), rtol=2.0 ** -7, atol=0)
+    moe4.moe4_quantize_mxfp8(x, q, s)
+    moe4.moe4_quantize_mxfp8(xe, q2, s2)
+    assert torch.equal(q[-tail:], q2) and torch.equal(s[-tail:], s2)
+    dx = torch.empty_like(x)
+    moe4.moe4_add_rmsnorm_backward(out, x, w, rstd, dx)
+    d2 = torch.empty_like(xe)
+    moe4.moe4_add_rmsnorm_backward(out[-tail:].clone(), xe, w, rstd[-tail:].clone(), d2)
+    # dy is the normalised row itself, so p and n mean(p n) all but cancel and what is left is no
+    # measure: as in the parity test, each call's fp32 error is at most e times the terms'
+    # magnitudes rstd (|p| + |n| mean|p n|), and a bf16 step lies between their roundings
+    p, n, rr = out[-tail:].double(), xe.double() * r2.double()[:, None], r2.double()[:, None]
+    mag = rr * (p.abs() + n.abs() * (p * n).abs().mean(1, keepdim=True))
+    tol = 2 * (512 + 24) * U32 * mag + 2.0 ** -7 * d2.double().abs()
+    assert bool(((dx[-tail:].double() - d2.double()).abs() <= tol).all())
+    del dx, q, s
+    blk = Block("huge", H, 16)
+    moe4.moe4_ffn_forward(blk.ffn, x, out, ws=blk.ws(T))
+    o2 = torch.empty_like(xe)
+    moe4.moe4_ffn_forward(blk.ffn.with_variant(VARIANTS["tiled"]), xe, o2, ws=blk.ws(tail))
+    # (few tokens are split along k: the fp32 sums' order, then one bf16 step of h and out)
+    d = (out[-tail:].float() - o2.float()).norm()
+    assert d <= 4 * RMS_BF * o2.float().norm()
+
+
 def test_other_streams():
     # a side stream, by argument and as the current one, ordered by events alone
     blk = Block("stream", 136, 72)
