@@ -3,6 +3,12 @@
 //   dW_dn = dY^T h;  dW_gu = dGU^T x;  db_dn = sum_t dY;  db_gu = sum_t dGU
 // The first product's epilogue applies the activation's derivative to its fp32 accumulators
 // and writes dGU and the recomputed h in bf16, the operand type of the products that follow.
+//
+// 8192 tokens at H = I = 2880 with biases: 820-845 us, 0.98 PFLOP/s. dH 214 us: its epilogue reads
+// 189 MB of pre-activations and writes 141 MB while the matrix cores stand (37% of a tile's
+// time; small tiles, two workgroups to a CU, overlap it but multiply more slowly: 202 to 218
+// us), and 384 tiles are one and a half rounds. The other products 607 us, 1.12 PFLOP/s. The
+// biases' column sums 12 + 10 us.
 #include "ffn.hpp"
 
 namespace moe4 {
@@ -16,11 +22,51 @@ struct DhArgs {
   uint16_t* dgu;        // [T, 2I]
   uint16_t* h;          // [T, I] or null (no gradient of W_dn wanted)
   float* part;          // [row tiles][2I] column sums of dGU, or null
+  int splits;           // parts of k (few tokens and a wide stream)
+  float* dh;            // [splits][T][I] sums to be joined
 };
 
 // the saved pre-activations of 8 pairs: gate and up (halves), or pairs in turn (interleaved)
 struct RawGu {
   u32x4 v[4];
+};
+
+// dGU (and h) of 8 pairs j .. j+7 of token t from dH and their pre-activations; d: dGU in the
+// order of memory, the runs that start at col0 and col1
+template <int LAYOUT, int ACT>
+struct Pairs8 {
+  static constexpr bool kHalves = LAYOUT == MOE4_GU_HALVES;
+  static __device__ __forceinline__ int col0(int j) { return kHalves ? j : 2 * j; }
+  static __device__ __forceinline__ int col1(const DhArgs& a, int j) {
+    return kHalves ? a.I + j : 2 * j + 8;
+  }
+  static __device__ __forceinline__ RawGu load(const DhArgs& a, int64_t t, int j) {
+    RawGu r;
+    const float* p = a.gu + t * 2 * a.I;
+    const u32x4* q = reinterpret_cast<const u32x4*>(p + col0(j));
+    const u32x4* s = reinterpret_cast<const u32x4*>(p + col1(a, j));
+    r.v[0] = q[0];
+    r.v[1] = q[1];
+    r.v[2] = s[0];
+    r.v[3] = s[1];
+    return r;
+  }
+  static __device__ __forceinline__ void finish(const DhArgs& a, int64_t t, int j, const float* dh,
+                                                const RawGu& r, float* d) {
+    const FfnAct act = {ACT, a.act.alpha, a.act.limit};
+    float x[16], h[8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r.v[i / 4][i % 4]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (kHalves) act.backward(x[i], x[8 + i], dh[i], h[i], d[i], d[8 + i]);
+      else act.backward(x[2 * i], x[2 * i + 1], dh[i], h[i], d[2 * i], d[2 * i + 1]);
+    }
+    uint16_t* o = a.dgu + t * 2 * a.I;
+    *reinterpret_cast<u32x4*>(o + col0(j)) = pack8_bf16(d);
+    *reinterpret_cast<u32x4*>(o + col1(a, j)) = pack8_bf16(d + 8);
+    if (a.h) *reinterpret_cast<u32x4*>(a.h + t * a.I + j) = pack8_bf16(h);
+  }
 };
 
 // LAYOUT, ACT: the block's (their branches would double the epilogue's code four times over)
@@ -29,56 +75,41 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
   const int na = (a.I + S::BA - 1) / S::BA, nb = (a.T + S::BB - 1) / S::BB;
   int ia, ib;
-  tile_of(xcd_remap(blockIdx.x, gridDim.x), na, nb, ia, ib);
+  const int id = xcd_remap(blockIdx.x, gridDim.x), split = id / (na * nb);
+  tile_of(id % (na * nb), na, nb, ia, ib);
   const int j0 = ia * S::BA, t0 = ib * S::BB, nt = min(S::BB, a.T - t0);
   OpLoader<S, kOpCol, S::BA, false> la;
   OpLoader<S, kOpRow, S::BB, false> lb;
-  la.init_col(a.W, a.H, j0);
-  lb.init_row(a.dY, 2, a.H, t0, nt, [=](int r) { return r < nt ? r : -1; });
+  const KPart k(a.H, 2, split, S::kSplits ? a.splits : 1);
+  la.init_col(a.W.from_col(k.kt0), k.K, j0);
+  lb.init_row(a.dY.from_row(k.kt0), 2, k.K, t0, nt, [=](int r) { return r < nt ? r : -1; });
   f32x16 acc[S::TA][S::TB];
   gemm_loop<S, kOpCol, kOpRow, false>(
-      acc, stage_mem, la, lb, a.H, MxScales{}, [](int) { return -1; }, [](int) { return -1; });
-  constexpr bool halves = LAYOUT == MOE4_GU_HALVES;
-  const FfnAct act = {ACT, a.act.alpha, a.act.limit};
-  // where the lane's two runs of 8 pre-activations start in a row
-  auto col0 = [&](int j) { return halves ? j : 2 * j; };
-  auto col1 = [&](int j) { return halves ? a.I + j : 2 * j + 8; };
+      acc, stage_mem, la, lb, k.K, MxScales{}, [](int) { return -1; }, [](int) { return -1; });
+  if constexpr (S::kSplits) {
+    if (a.splits > 1) {
+      float* part = a.dh + (int64_t)split * a.T * a.I;
+      for_each8<S, false, 1>(acc, stage_mem, [](int, int) { return NoPre{}; },
+                                    [&](int row, int jj, float* v, const NoPre&) {
+        const int j = j0 + jj;
+        if (row < nt && j < a.I) store8_f32(part + (int64_t)(t0 + row) * a.I + j, v);
+      });
+      return;
+    }
+  }
+  using P = Pairs8<LAYOUT, ACT>;
   float sums[16] = {};   // of dGU over the lane's rows, in fp32 before the rounding
   for_each8<S, false, 4>(
       acc, stage_mem,
       [&](int row, int jj) {
         RawGu r;
-        const int j = j0 + jj;
-        if (row < nt && j < a.I) {
-          const float* p = a.gu + (int64_t)(t0 + row) * 2 * a.I;
-          const u32x4* q = reinterpret_cast<const u32x4*>(p + col0(j));
-          const u32x4* s = reinterpret_cast<const u32x4*>(p + col1(j));
-          r.v[0] = q[0];
-          r.v[1] = q[1];
-          r.v[2] = s[0];
-          r.v[3] = s[1];
-        }
+        if (row < nt && j0 + jj < a.I) r = P::load(a, t0 + row, j0 + jj);
         return r;
       },
       [&](int row, int jj, float* dh, const RawGu& r) {
-        const int j = j0 + jj;
-        if (row >= nt || j >= a.I) return;
-        const int64_t t = t0 + row;
-        float x[16], h[8], d[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r.v[i / 4][i % 4]);
-        if (halves) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) act.backward(x[i], x[8 + i], dh[i], h[i], d[i], d[8 + i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            act.backward(x[2 * i], x[2 * i + 1], dh[i], h[i], d[2 * i], d[2 * i + 1]);
-        }
-        uint16_t* o = a.dgu + t * 2 * a.I;
-        *reinterpret_cast<u32x4*>(o + col0(j)) = pack8_bf16(d);
-        *reinterpret_cast<u32x4*>(o + col1(j)) = pack8_bf16(d + 8);
-        if (a.h) *reinterpret_cast<u32x4*>(a.h + t * a.I + j) = pack8_bf16(h);
+        if (row >= nt || j0 + jj >= a.I) return;
+        float d[16];
+        P::finish(a, t0 + row, j0 + jj, dh, r, d);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sums[i] += d[i];
       });
@@ -110,7 +141,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_dh(const DhArgs a) {
     f32x4 s = red[(wa * kPer + l) * 4 + i];
 #pragma unroll
     for (int v = 1; v < S::WB; ++v) s += red[((v * S::WA + wa) * kPer + l) * 4 + i];
-    *reinterpret_cast<f32x4*>(o + (i < 2 ? col0(j) + 4 * i : col1(j) + 4 * (i - 2))) = s;
+    *reinterpret_cast<f32x4*>(o + (i < 2 ? P::col0(j) + 4 * i : P::col1(a, j) + 4 * (i - 2))) = s;
   }
 }
 
@@ -150,6 +181,25 @@ hipError_t launch_grads(GradArgs a, int n, hipStream_t s) {
     a.first[i + 1] = a.first[i] + (i < n ? (int)((tiles_of<S>(a.p[i].na, a.p[i].nb) * a.p[i].splits + 7) / 8 * 8) : 0);
   k<<<a.first[3], S::kThreads, S::kLds, s>>>(a);
   return hipGetLastError();
+}
+
+// The parts of a split dH, joined: 8 pairs of a token to a thread.
+template <int LAYOUT, int ACT>
+__global__ __launch_bounds__(256) void k_ffn_dh_join(const DhArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = a.I / 8;
+  const int64_t t = i / per;
+  if (t >= a.T) return;
+  const int j = (int)(i - t * per) * 8;
+  const RawGu r = Pairs8<LAYOUT, ACT>::load(a, t, j);
+  float dh[8] = {}, d[16];
+  for (int s = 0; s < a.splits; ++s) {
+    float x[8];
+    load8_f32(a.dh + ((int64_t)s * a.T + t) * a.I + j, x);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dh[q] += x[q];
+  }
+  Pairs8<LAYOUT, ACT>::finish(a, t, j, dh, r, d);
 }
 
 // Column sums of a bf16 matrix [T, N]: workgroup (x, p) sums part p's rows of 512 columns in
@@ -194,33 +244,38 @@ hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
   auto* k = &k_ffn_dh<S, LAYOUT, ACT>;
   hipError_t e = allow_lds(k, S::kLds);
   if (e != hipSuccess) return e;
-  k<<<(uint32_t)tiles_of<S>(a.I, a.T), S::kThreads, S::kLds, s>>>(a);
+  k<<<(uint32_t)(tiles_of<S>(a.I, a.T) * a.splits), S::kThreads, S::kLds, s>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  k_ffn_dh_join<LAYOUT, ACT>
+      <<<(uint32_t)(((int64_t)a.T * (a.I / 8) + 255) / 256), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// workspace: dGU, h, the partial sums of the two biases' gradients and of products that are
-// split along k: those whose reduction is longer than the share of a workgroup, where all the
-// products' tiles leave most of a round empty
+// workspace: dGU, h, the partial sums of the two biases' gradients, of dH where it is split along
+// k, and of the products after it: one whose reduction is several times a workgroup's share of
+// all their k-tiles (few tokens: dX; a small block and many tokens: the weights' gradients)
+// would still run when the others have ended
 struct BwdWs {
-  size_t h, part_gu, part_dn, part[3], end;
-  int splits[3];   // dX, dW_gu, dW_dn
+  size_t h, part_gu, part_dn, dh, part[3], end;
+  int dh_splits, splits[3];   // dX, dW_gu, dW_dn
   BwdWs(const moe4_ffn& f, int64_t T) {
     h = align_up((size_t)T * 2 * f.I * 2, 256);
     part_gu = h + align_up((size_t)T * f.I * 2, 256);
     part_dn = part_gu + align_up((size_t)((T + 127) / 128) * 2 * f.I * 4, 256);
-    end = part_dn + align_up((size_t)kColParts * f.H * 4, 256);
+    // (where dH is split, the bias gradient of the first projection comes from dGU's columns too)
+    const int wide = 2 * f.I > f.H ? 2 * f.I : f.H;
+    dh = part_dn + align_up((size_t)kColParts * wide * 4, 256);
+    dh_splits = T > 0 ? k_splits(tiles_of<Tile128>(f.I, T), f.H, 2) : 1;
+    end = dh + (dh_splits > 1 ? align_up((size_t)dh_splits * T * f.I * 4, 256) : 0);
     const int64_t size[3][3] = {{f.H, T, 2 * (int64_t)f.I}, {f.H, 2 * (int64_t)f.I, T}, {f.I, f.H, T}};
-    int64_t tiles = 0, work = 0;   // k-tiles of 64
-    for (const auto& z : size) {
-      const int64_t n = tiles_of<Tile128>(z[0], z[1]);
-      tiles += n;
-      work += n * ((z[2] + 63) / 64);
-    }
+    int64_t work = 0;   // k-tiles of 64
+    for (const auto& z : size) work += tiles_of<Tile128>(z[0], z[1]) * ((z[2] + 63) / 64);
     const int64_t share = (work + 511) / 512 > 8 ? (work + 511) / 512 : 8;
     for (int i = 0; i < 3; ++i) {
-      const int64_t s = tiles >= 384 ? 1 : ((size[i][2] + 63) / 64) / share;
+      const int64_t s = (size[i][2] + 63) / 64 / share;
       splits[i] = s < 2 ? 1 : (int)(s < 32 ? s : 32);
       part[i] = end;
       if (splits[i] > 1) end += align_up((size_t)splits[i] * size[i][0] * size[i][1] * 4, 256);
@@ -245,14 +300,18 @@ hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, cons
   if (dx || dw_gu || dw_dn || db_gu) {
     DhArgs a = {{f.w_dn, nullptr, I, I}, {dy, nullptr, H, T}, T, H, I,
                 {f.act, f.act_alpha, f.act_limit}, gu, dgu, dw_dn ? h : nullptr,
-                db_gu ? part_gu : nullptr};
-    const bool big = large_tiles_for(I, T);
+                db_gu && at.dh_splits == 1 ? part_gu : nullptr, at.dh_splits,
+                reinterpret_cast<float*>(w8 + at.dh)};
+    const bool big = at.dh_splits == 1 && large_tiles_for(I, T);
     e = with_kind(f.gu_layout, f.act, [&](auto l, auto c) {
       constexpr int L = decltype(l)::value, A = decltype(c)::value;
       return big ? launch_dh<Tile256, L, A>(a, s) : launch_dh<Tile128, L, A>(a, s);
     });
     if (e != hipSuccess) return e;
-    if (db_gu) {
+    if (db_gu && at.dh_splits > 1) {
+      e = col_sums(dgu, T, 2 * I, part_dn, db_gu, dw_dtype, s);
+      if (e != hipSuccess) return e;
+    } else if (db_gu) {
       const int rows = big ? Tile256::BB : Tile128::BB;
       e = launch_sum_rows(part_gu, (T + rows - 1) / rows, 2 * I, db_gu, dw_dtype, s);
       if (e != hipSuccess) return e;

@@ -93,6 +93,10 @@ __device__ __forceinline__ float row_sum(float x, float (&red)[2][W], int slot) 
   return s;
 }
 
+// One pass: the row stays in registers between its sum of squares and its outputs. Bound by HBM:
+// 4096 x 2880, fp32 x and bf16 stream in, sum, bf16 and MXFP8 out (130 MB): 26.7 us, 4.9 TB/s,
+// the rate of a large copy on this card; one row of 2048: 2.2 us, a launch.
+//
 // Shapes: W waves of a row, each lane NV chunks of 8 columns (W * NV * 512 columns at most).
 // W == 1 puts four rows into a workgroup and needs no barrier: for many rows. More waves a
 // row shorten a row's own latency: for few rows, and for rows past one wave's registers.
@@ -210,7 +214,9 @@ struct NormBwdArgs {
 };
 
 // n = s * rstd;  p = w * dy;  dx = rstd * (p - n * mean(p * n)) (+ dres);  dw = sum_t dy * n.
-// The workgroup sums its rows' dw in registers, in row order, and its waves' sums through LDS.
+// The workgroup sums its rows' dw in registers, in row order, and its waves' sums through LDS;
+// k_sum_rows joins the workgroups' sums. Bound by HBM: 8191 x 2880 in bf16 with dres (189 MB):
+// 38.6 us, 4.9 TB/s, and 4.7 us for the join.
 template <int DY, int DS, int DX, int W, int NV>
 __global__ __launch_bounds__(kNormThreads<W>) void k_add_rmsnorm_bwd(const NormBwdArgs a) {
   constexpr int kRows = W == 1 ? 4 : 1;
@@ -320,7 +326,8 @@ __global__ __launch_bounds__(kNormThreads<W>) void k_add_rmsnorm_bwd(const NormB
 }
 
 // out[c] = sum over the P rows of part [P][N], in fp32 in a fixed order: thread (y, x) takes
-// rows y, y + 32, ... of column 32 blockIdx + x, and the 32 sums of a column meet in LDS.
+// rows y, y + 32, ... of column 32 blockIdx + x, and the 32 sums of a column meet in LDS. 1024 x
+// 2880: 4.7 us, mostly its launch and one round trip.
 __global__ __launch_bounds__(1024) void k_sum_rows(const float* part, int P, int N, void* out,
                                                    int dtype) {
   __shared__ float red[32][33];
@@ -342,7 +349,8 @@ __global__ __launch_bounds__(1024) void k_sum_rows(const float* part, int P, int
   }
 }
 
-// 8 values a lane, four lanes a block
+// 8 values a lane, four lanes a block (the maximum by two quad permutes). Bound by HBM: 16384 x
+// 4096 from bf16 (203 MB): 36.4 us, 5.6 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256) void k_quantize_mxfp8(const void* v, int64_t n8, uint8_t* q,
                                                         uint8_t* s) {
