@@ -459,6 +459,13 @@ class _Call:
         return _stream(stream)
 
 
+def _int32(fn, **sizes):
+    """Sizes that the C interface takes as int32 (ctypes would cut a larger one off silently)."""
+    for name, v in sizes.items():
+        if not -(1 << 31) <= v < 1 << 31:   # a negative one is for the C interface to refuse
+            raise ValueError(f"{fn}: {name} = {v} outside int32")
+
+
 def moe4_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, out_q=None, out_s=None,
                      rstd=None, stream=None):
     """s = x + residual (rounded to the residual's type; sum_out), y = s * rstd * weight, as bf16
@@ -466,6 +473,8 @@ def moe4_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, out_
     x, residual bf16 or f32 [T, H]; weight bf16 or f32 [H]; rstd f32 [T]."""
     c = _Call("add_rmsnorm")
     T, H = sh = x.shape
+    if T >> 31 or H >> 31:
+        _int32(c.fn, T=T, H=H)
     if sum_out is not None and residual is not None and sum_out.dtype != residual.dtype:
         raise TypeError("sum_out must have the residual's dtype")
     px = c.ptr(x, "x", sh, _FLOATS)
@@ -478,6 +487,7 @@ def moe4_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, out_
 
 
 def moe4_add_rmsnorm_workspace_size(T, H):
+    _int32("add_rmsnorm_workspace_size", T=T, H=H)
     n = _lib.moe4_add_rmsnorm_workspace_size(T, H)
     if n == 0:
         raise Moe4Error(MOE4_ESHAPE, moe4_last_error())
@@ -490,6 +500,8 @@ def moe4_add_rmsnorm_backward(dy, s, weight, rstd, dx, dres=None, dweight=None, 
     added) and dweight f32 [H]. s: the forward's sum_out (its x without a residual)."""
     c = _Call("add_rmsnorm_backward")
     T, H = sh = s.shape
+    if T >> 31 or H >> 31:
+        _int32(c.fn, T=T, H=H)
     if dres is not None and dres.dtype != dx.dtype:
         raise TypeError("dres must have dx's dtype")
     ps = c.ptr(s, "s", sh, _FLOATS)
@@ -522,6 +534,7 @@ class Ffn:
                  gu_bias=None, dn_bias=None, act_alpha=1.702, act_limit=7.0,
                  variant=MOE4_VARIANT_AUTO):
         c = _Call("Ffn")
+        _int32("Ffn", H=H, I=I)
         wdt = _CODES if fmt == MOE4_FFN_MXFP8 else _BF16
         self.tensors = (w_gu, w_dn, gu_s, dn_s, gu_bias, dn_bias)
         self.desc = Moe4Ffn(
@@ -554,6 +567,7 @@ def _ffn_call(fn, ffn):
 
 
 def moe4_ffn_workspace_size(ffn, T, backward=False):
+    _int32("ffn_workspace_size", T=T)
     n = _lib.moe4_ffn_workspace_size(ffn.ref, T, int(bool(backward)))
     if n == 0:
         raise Moe4Error(MOE4_EINVAL, moe4_last_error())
@@ -565,6 +579,8 @@ def moe4_ffn_forward(ffn, x, out, x_s=None, residual=None, save_gu=None, ws=None
     residual (bf16 or f32); save_gu f32 [T, 2I]: the pre-activations for the backward pass."""
     c = _ffn_call("ffn_forward", ffn)
     T, H = x.shape[0], ffn.H
+    if T >> 31:
+        _int32(c.fn, T=T)
     mx = ffn.desc.format == MOE4_FFN_MXFP8
     pw, nw = c.ws(ws)
     _check(_lib.moe4_ffn_forward(
@@ -581,6 +597,8 @@ def moe4_ffn_backward(ffn, x, save_gu, dy, dx=None, dx_add=None, dw_gu=None, dw_
     added), dw_gu, dw_dn, db_gu, db_dn (one dtype, bf16 or f32); each may be None."""
     c = _ffn_call("ffn_backward", ffn)
     T, H, I = dy.shape[0], ffn.H, ffn.I
+    if T >> 31:
+        _int32(c.fn, T=T)
     given = [t for t in (dw_gu, dw_dn, db_gu, db_dn) if t is not None]
     if any(t.dtype != given[0].dtype for t in given):
         raise TypeError("the weights' and biases' gradients must have one dtype")

@@ -247,3 +247,20 @@ def test_binding_refuses_what_the_kernels_cannot_read():
         moe4.GradList([x])
     with pytest.raises(ValueError, match="differ in length"):
         moe4.GradList([], [x])
+
+
+def test_binding_refuses_sizes_past_int32():
+    # cut off to 32 bits, 2^32 + 3 rows would be 3
+    big = torch.empty(((1 << 32) + 3, 64), dtype=torch.bfloat16, device="meta")
+    wide = torch.empty((1, (1 << 32) + 64), dtype=torch.bfloat16, device="meta")
+    for x in (big, wide):
+        with pytest.raises(ValueError, match="outside"):
+            moe4.moe4_add_rmsnorm(x, x[0], 1e-6, out=x)
+        with pytest.raises(ValueError, match="outside"):
+            moe4.moe4_add_rmsnorm_backward(x, x, x[0], x[:, 0], x)
+    with pytest.raises(ValueError, match="outside"):
+        moe4.moe4_add_rmsnorm_workspace_size((1 << 32) + 3, 64)
+    with pytest.raises(ValueError, match="I = 4294967360 outside"):
+        moe4.Ffn(moe4.MOE4_FFN_BF16, wide, wide, gu_layout=1, act=1, H=64, I=(1 << 32) + 64)
+    with pytest.raises(ValueError, match="T = 4294967299 outside"):
+        moe4.moe4_ffn_workspace_size(None, (1 << 32) + 3)
