@@ -518,6 +518,8 @@ def moe4_quantize_mxfp8(x, q, s, stream=None):
     [..., K/32]."""
     c = _Call("quantize_mxfp8")
     sh = tuple(x.shape)
+    if not sh:
+        raise ValueError("quantize_mxfp8: x has no dimension")
     K = sh[-1]
     R = x.numel() // K if K else 0
     _check(_lib.moe4_quantize_mxfp8(c.ptr(x, "x", sh, _FLOATS), _dt(x), R, K,
@@ -615,7 +617,9 @@ def moe4_ffn_backward(ffn, x, save_gu, dy, dx=None, dx_add=None, dw_gu=None, dw_
 class GradList:
     """Owns references to a list of gradients (bf16 or f32, any shapes) and the host arrays that
     moe4_grad_norm and moe4_clip_grads read. outs: where moe4_clip_grads writes (same shapes and
-    dtypes), None for in place. Build it anew when a gradient is another tensor."""
+    dtypes), None for in place. Build it anew when a gradient is another tensor. What
+    moe4_clip_grads writes may overlap nothing else of the list (a gradient that is in it twice
+    would be scaled by two workgroups at once): it refuses such a list."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -632,6 +636,27 @@ class GradList:
             self._numel[i], self._dtype[i] = g.numel(), _dt(g)
             if self.outs is not None:
                 self._out[i] = c.ptr(self.outs[i], f"outs[{i}]", tuple(g.shape), (g.dtype,))
+        self.clash = self._overlap()
+
+    def _overlap(self):
+        """Where an output overlaps another output, or another entry's gradient: a message."""
+        spans = []   # (first byte, end, entry, whether it is written)
+        for i, g in enumerate(self.grads):
+            size = g.numel() * g.element_size()
+            if size == 0:
+                continue
+            out = self._in[i] if self._out is None else self._out[i]
+            spans.append((out, out + size, i, True))
+            if out != self._in[i]:
+                spans.append((self._in[i], self._in[i] + size, i, False))
+        spans.sort()
+        end = {True: (0, 0), False: (0, 0)}   # the furthest byte written, read so far
+        for a, b, i, written in spans:
+            for w in (True, False) if written else (True,):
+                if a < end[w][0]:
+                    return f"outs[{i if written else end[w][1]}] overlaps entry {end[w][1] if written else i}"
+            end[written] = max(end[written], (b, i))
+        return None
 
 
 def moe4_grad_workspace_size(grads):
@@ -660,6 +685,8 @@ def moe4_clip_grads(grads, max_norm, norm_out=None, ws=None, norm_in=None, strea
     """Scales a GradList by min(1, max_norm / (norm + 1e-6)); the norm is norm_in where given,
     else the list's own; norm_out f32 [1] takes the norm used."""
     c = _grad_call("clip_grads", grads)
+    if grads.clash:
+        raise ValueError(f"clip_grads: {grads.clash}")
     pw, nw = c.ws(ws)
     _check(_lib.moe4_clip_grads(grads._in, grads._out, grads._numel, grads._dtype, grads.n,
                                 max_norm, c.ptr(norm_in, "norm_in", (1,), _F32),

@@ -571,7 +571,8 @@ int moe4_grad_norm(const void* const* grads, const int64_t* numel, const int32_t
  * the step.
  *   grads, numel, dtype, n, ws as moe4_grad_norm
  *   outs: host array of n device pointers (16-byte aligned; outs[i] may be
- *   grads[i]), or NULL for all in place
+ *   grads[i], and overlaps nothing else of the list), or NULL for all in place
+ *   (no gradient is then in the list twice)
  *   max_norm: positive
  *   norm_in f32 [1] (device) or NULL: the norm to clip by, where it spans more
  *   than this list (other ranks' shards); NULL computes it here

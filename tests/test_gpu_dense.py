@@ -52,7 +52,7 @@ class Guarded:
         n = int(np.prod(shape))
         self.n, self.dtype = n, dtype
         self.raw = torch.full((n * torch.empty(0, dtype=dtype).element_size() + 1024,), 0xA5,
-                              dtype=torch.uint8, device=DEV)
+                              dtype=torch.uint8, device="cuda")
         self.t = self.raw[512:512 + n * torch.empty(0, dtype=dtype).element_size()].view(dtype).view(shape)
 
     def check(self, what):
@@ -105,8 +105,8 @@ def test_quantize_mxfp8_every_rounding():
     flat = np.zeros(x.shape[0] * 31, np.float32)
     flat[:len(v)] = v
     x[:, 1:] = flat.reshape(-1, 31)
-    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=DEV)
-    s = torch.empty((x.shape[0], 1), dtype=torch.float8_e8m0fnu, device=DEV)
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty((x.shape[0], 1), dtype=torch.float8_e8m0fnu, device="cuda")
     moe4.moe4_quantize_mxfp8(to_dev(x), q, s)
     wq, ws = dense.quantize_mxfp8(x)
     assert np.array_equal(q.view(torch.uint8).cpu().numpy(), wq)
@@ -190,7 +190,7 @@ def test_add_rmsnorm_in_place_and_alone():
     for so, out in outs[1:]:
         assert torch.equal(so, outs[0][0]) and torch.equal(out, outs[0][1])
     # MXFP8 alone, and the bf16 output alone without a sum, match the call that writes all
-    q, qs = torch.empty((9, 512), dtype=torch.uint8, device=DEV), torch.empty((9, 16), dtype=torch.uint8, device=DEV)
+    q, qs = torch.empty((9, 512), dtype=torch.uint8, device="cuda"), torch.empty((9, 16), dtype=torch.uint8, device="cuda")
     q2, qs2 = torch.empty_like(q), torch.empty_like(qs)
     out = torch.empty_like(x)
     moe4.moe4_add_rmsnorm(x, w, 1e-5, residual=res, out_q=q, out_s=qs)
@@ -204,7 +204,7 @@ def test_add_rmsnorm_non_finite_rows_stay_apart():
     w, wv = draw(r, (96,))
     x[1, 7], x[2, 95] = float("nan"), float("inf")
     out = torch.empty_like(x)
-    q, qs = torch.empty((4, 96), dtype=torch.uint8, device=DEV), torch.empty((4, 3), dtype=torch.uint8, device=DEV)
+    q, qs = torch.empty((4, 96), dtype=torch.uint8, device="cuda"), torch.empty((4, 3), dtype=torch.uint8, device="cuda")
     moe4.moe4_add_rmsnorm(x, w, 1e-6, out=out, out_q=q, out_s=qs)
     o = val(out)
     assert np.isnan(o[1]).all() and np.isnan(o[2, 95]) and np.isfinite(o[[0, 3]]).all()
@@ -224,7 +224,7 @@ def test_add_rmsnorm_backward(T, H, yd, sd, dd, wd):
     rstd = 1 / np.sqrt(np.mean(sv * sv, 1) + 1e-6)
     rt = to_dev(rstd.astype(np.float32))
     rstd = rt.double().cpu().numpy()
-    ws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
     for with_res in (True, False):
         dx, dw = out_t((T, H), dd), out_t((H,), F32)
         moe4.moe4_add_rmsnorm_backward(dy, s, w, rt, dx.t, dres=dres if with_res else None,
@@ -256,7 +256,7 @@ def test_add_rmsnorm_backward_against_differences():
     dy, yv = draw(r, (T, H), F32)
     _, rstd, _ = dense.add_rmsnorm(sv, wv, 1e-5)
     dx, dw = torch.empty_like(s), torch.empty_like(w)
-    ws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
     moe4.moe4_add_rmsnorm_backward(dy, s, w, to_dev(rstd.astype(np.float32)), dx, dweight=dw, ws=ws)
     vs, vw, h = r.standard_normal((T, H)), r.standard_normal(H), 1e-5
 
@@ -309,7 +309,7 @@ class Block:
 
     def ws(self, T, backward=False):
         n = moe4.moe4_ffn_workspace_size(self.ffn, T, backward)
-        return torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)   # NaNs wherever it is read first
+        return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")   # NaNs wherever it is read first
 
 
 def row_norm(got, want, rel, what, floor=1e-30):
@@ -428,7 +428,7 @@ def test_ffn_non_finite_tokens_stay_apart(mx, variant):
     blk = Block("nan", 96, 64, mx, mx, True)
     T = 20
     x, xs, xv = blk.tokens(T)
-    clean = torch.empty((T, 96), dtype=BF, device=DEV)
+    clean = torch.empty((T, 96), dtype=BF, device="cuda")
     moe4.moe4_ffn_forward(blk.ffn.with_variant(VARIANTS[variant]), x, clean, x_s=xs, ws=blk.ws(T))
     if mx:
         xs[7, 0] = 255
@@ -513,7 +513,7 @@ def test_ffn_backward_outputs_one_by_one():
     shapes = dict(dx=(T, 136), dw_gu=(144, 136), dw_dn=(136, 72), db_gu=(144,), db_dn=(136,))
 
     def run(names):
-        o = {k: torch.full(shapes[k], 7.0, dtype=BF, device=DEV) for k in names}
+        o = {k: torch.full(shapes[k], 7.0, dtype=BF, device="cuda") for k in names}
         moe4.moe4_ffn_backward(blk.ffn, x, gu, dy, ws=blk.ws(T, True), **o)
         return o
     full = run(shapes)
@@ -534,8 +534,8 @@ def test_ffn_backward_against_differences():
     x, _, xv = blk.tokens(T)
     dy, dyv = draw(rng("dyd"), (T, 72))
     fw = dense.ffn_forward(xv, blk.wg, blk.wd, blk.layout, blk.act, blk.bg, blk.bd)
-    o = dict(dx=torch.empty((T, 72), device=DEV), dw_gu=torch.empty((96, 72), device=DEV),
-             dw_dn=torch.empty((72, 48), device=DEV))
+    o = dict(dx=torch.empty((T, 72), device="cuda"), dw_gu=torch.empty((96, 72), device="cuda"),
+             dw_dn=torch.empty((72, 48), device="cuda"))
     moe4.moe4_ffn_backward(blk.ffn, x, to_dev(fw["gu"].astype(np.float32)), dy, ws=blk.ws(T, True), **o)
 
     def loss(x=xv, wg=blk.wg, wd=blk.wd):
@@ -551,16 +551,16 @@ def test_ffn_backward_against_differences():
 
 def test_ffn_no_tokens():
     blk = Block("empty", 72, 40, False, False, True)
-    e = torch.empty((0, 72), dtype=BF, device=DEV)
+    e = torch.empty((0, 72), dtype=BF, device="cuda")
     moe4.moe4_ffn_forward(blk.ffn, e, e)
     for dt in (BF, F32):
-        o = dict(dw_gu=torch.full((80, 72), 3.0, dtype=dt, device=DEV), dw_dn=torch.full((72, 40), 3.0, dtype=dt, device=DEV),
-                 db_gu=torch.full((80,), 3.0, dtype=dt, device=DEV), db_dn=torch.full((72,), 3.0, dtype=dt, device=DEV))
-        moe4.moe4_ffn_backward(blk.ffn, e, torch.empty((0, 80), device=DEV), e, dx=e, **o)
+        o = dict(dw_gu=torch.full((80, 72), 3.0, dtype=dt, device="cuda"), dw_dn=torch.full((72, 40), 3.0, dtype=dt, device="cuda"),
+                 db_gu=torch.full((80,), 3.0, dtype=dt, device="cuda"), db_dn=torch.full((72,), 3.0, dtype=dt, device="cuda"))
+        moe4.moe4_ffn_backward(blk.ffn, e, torch.empty((0, 80), device="cuda"), e, dx=e, **o)
         assert all(bool((v == 0).all()) for v in o.values())
-    moe4.moe4_add_rmsnorm(e, torch.ones(72, device=DEV), 1e-6, out=e)
-    dw = torch.full((72,), 3.0, device=DEV)
-    moe4.moe4_add_rmsnorm_backward(e, e, torch.ones(72, device=DEV), torch.empty(0, device=DEV), e, dweight=dw)
+    moe4.moe4_add_rmsnorm(e, torch.ones(72, device="cuda"), 1e-6, out=e)
+    dw = torch.full((72,), 3.0, device="cuda")
+    moe4.moe4_add_rmsnorm_backward(e, e, torch.ones(72, device="cuda"), torch.empty(0, device="cuda"), e, dweight=dw)
     assert bool((dw == 0).all())
 
 
@@ -586,14 +586,14 @@ def test_clip_grads(sizes, dtypes, in_place):
     want = dense.grad_norm(vs)
     outs = None if in_place else [Guarded(tuple(t.shape), t.dtype) for t in ts]
     gl = moe4.GradList(ts, None if in_place else [o.t for o in outs])
-    ws = torch.full((moe4.moe4_grad_workspace_size(gl),), 0xFF, dtype=torch.uint8, device=DEV)
-    norm = torch.full((1,), -1.0, device=DEV)
+    ws = torch.full((moe4.moe4_grad_workspace_size(gl),), 0xFF, dtype=torch.uint8, device="cuda")
+    norm = torch.full((1,), -1.0, device="cuda")
     moe4.moe4_grad_norm(gl, norm, ws)
     # fp64 sums: the fp32 rounding of the root, and of the root's own step
     assert abs(norm.item() - want) <= 2 * U32 * want
     for max_norm in (max(want, 1.0) * 4, max(want, 1e-3) / 3):
         before = [t.clone() for t in ts]
-        n2 = torch.full((1,), -1.0, device=DEV)
+        n2 = torch.full((1,), -1.0, device="cuda")
         moe4.moe4_clip_grads(gl, max_norm, n2, ws)
         cur = dense.grad_norm([val(t) for t in before])
         k = dense.clip_factor(cur, max_norm)
@@ -608,9 +608,9 @@ def test_clip_grads(sizes, dtypes, in_place):
                 outs[i].check("clipped gradient")
                 assert torch.equal(ts[i], t)
     # a norm from elsewhere
-    total = torch.tensor([10.0 * max(want, 1.0)], device=DEV)
+    total = torch.tensor([10.0 * max(want, 1.0)], device="cuda")
     before = [t.clone() for t in ts]
-    n3 = torch.zeros(1, device=DEV)
+    n3 = torch.zeros(1, device="cuda")
     moe4.moe4_clip_grads(gl, 1.0, n3, norm_in=total)
     assert n3.item() == total.item()
     k = 1.0 / (total.item() + 1e-6)
@@ -622,10 +622,10 @@ def test_clip_grads(sizes, dtypes, in_place):
 def test_grad_norm_of_extreme_values():
     # squares that overflow, or vanish, in fp32; infinities and NaNs leave the gradients alone
     for v in (1e30, 1e-30, 3e38):
-        t = torch.full((1000,), v, device=DEV)
+        t = torch.full((1000,), v, device="cuda")
         gl = moe4.GradList([t])
-        ws = torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device=DEV)
-        n = torch.empty(1, device=DEV)
+        ws = torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device="cuda")
+        n = torch.empty(1, device="cuda")
         moe4.moe4_grad_norm(gl, n, ws)
         want = math.sqrt(1000) * float(np.float32(v))
         if want < 3.4028234e38:
@@ -633,7 +633,7 @@ def test_grad_norm_of_extreme_values():
         else:
             assert math.isinf(n.item())
     for bad in (float("inf"), float("nan")):
-        t = torch.ones(5000, device=DEV)
+        t = torch.ones(5000, device="cuda")
         t[4321] = bad
         o = torch.zeros_like(t)
         gl = moe4.GradList([t], [o])
@@ -650,18 +650,18 @@ def test_sums_do_not_depend_on_the_run():
     dy, _ = draw(rng("dyx"), (T, 520))
     gu = to_dev(dense.ffn_forward(xv, blk.wg, blk.wd, blk.layout, blk.act, blk.bg, blk.bd)["gu"].astype(np.float32))
     w, _ = draw(rng("w"), (520,))
-    rstd = torch.ones(T, device=DEV)
-    nws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, 520), dtype=torch.uint8, device=DEV)
+    rstd = torch.ones(T, device="cuda")
+    nws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, 520), dtype=torch.uint8, device="cuda")
     first = None
     for _ in range(3):
-        o = [torch.empty((528, 520), dtype=F32, device=DEV), torch.empty((520, 264), dtype=F32, device=DEV),
-             torch.empty((528,), dtype=F32, device=DEV), torch.empty((520,), dtype=F32, device=DEV)]
+        o = [torch.empty((528, 520), dtype=F32, device="cuda"), torch.empty((520, 264), dtype=F32, device="cuda"),
+             torch.empty((528,), dtype=F32, device="cuda"), torch.empty((520,), dtype=F32, device="cuda")]
         moe4.moe4_ffn_backward(blk.ffn, x, gu, dy, dw_gu=o[0], dw_dn=o[1], db_gu=o[2], db_dn=o[3], ws=blk.ws(T, True))
-        dx, dw = torch.empty((T, 520), dtype=BF, device=DEV), torch.empty(520, device=DEV)
+        dx, dw = torch.empty((T, 520), dtype=BF, device="cuda"), torch.empty(520, device="cuda")
         moe4.moe4_add_rmsnorm_backward(dy, x, w, rstd, dx, dweight=dw, ws=nws)
-        n = torch.empty(1, device=DEV)
+        n = torch.empty(1, device="cuda")
         gl = moe4.GradList(o)
-        moe4.moe4_grad_norm(gl, n, torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device=DEV))
+        moe4.moe4_grad_norm(gl, n, torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device="cuda"))
         got = o + [dw, n]
         if first is None:
             first = got
@@ -671,8 +671,8 @@ def test_sums_do_not_depend_on_the_run():
 # ----------------------------------------------------- refusals of the binding
 
 def test_binding_refusals():
-    x = torch.zeros((4, 64), dtype=BF, device=DEV)
-    w = torch.ones(64, device=DEV)
+    x = torch.zeros((4, 64), dtype=BF, device="cuda")
+    w = torch.ones(64, device="cuda")
     with pytest.raises(ValueError, match="weight has shape"):
         moe4.moe4_add_rmsnorm(x, w[:32], 1e-6, out=x)
     with pytest.raises(TypeError, match="contiguous"):
@@ -682,7 +682,7 @@ def test_binding_refusals():
     with pytest.raises(TypeError, match="residual's dtype"):
         moe4.moe4_add_rmsnorm(x, w, 1e-6, residual=x, sum_out=x.float(), out=x)
     with pytest.raises(ValueError, match="out_s has shape"):
-        moe4.moe4_add_rmsnorm(x, w, 1e-6, out_q=x.to(torch.uint8), out_s=torch.zeros((4, 3), dtype=torch.uint8, device=DEV))
+        moe4.moe4_add_rmsnorm(x, w, 1e-6, out_q=x.to(torch.uint8), out_s=torch.zeros((4, 3), dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError, match="GPU"):
         moe4.moe4_add_rmsnorm(x, w.cpu(), 1e-6, out=x)
     blk = Block("refuse", 64, 32)
@@ -691,14 +691,14 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="x has shape"):
         moe4.moe4_ffn_forward(blk.ffn, x[:, :32].contiguous(), x.clone(), ws=blk.ws(4))
     with pytest.raises(TypeError, match="one dtype"):
-        moe4.moe4_ffn_backward(blk.ffn, x, torch.zeros((4, 64), device=DEV), x, dw_gu=torch.empty((64, 64), dtype=BF, device=DEV),
-                               dw_dn=torch.empty((64, 32), device=DEV), ws=blk.ws(4, True))
+        moe4.moe4_ffn_backward(blk.ffn, x, torch.zeros((4, 64), device="cuda"), x, dw_gu=torch.empty((64, 64), dtype=BF, device="cuda"),
+                               dw_dn=torch.empty((64, 32), device="cuda"), ws=blk.ws(4, True))
     with pytest.raises(ValueError, match="w_dn has shape"):
-        moe4.Ffn(moe4.MOE4_FFN_BF16, torch.empty((64, 64), dtype=BF, device=DEV), torch.empty((64, 64), dtype=BF, device=DEV),
+        moe4.Ffn(moe4.MOE4_FFN_BF16, torch.empty((64, 64), dtype=BF, device="cuda"), torch.empty((64, 64), dtype=BF, device="cuda"),
                  gu_layout=1, act=1, H=64, I=32)
     with pytest.raises(moe4.Moe4Error, match="16-byte"):
-        moe4.moe4_quantize_mxfp8(torch.zeros(40, dtype=BF, device=DEV)[4:36], torch.empty(32, dtype=torch.uint8, device=DEV),
-                                 torch.empty(1, dtype=torch.uint8, device=DEV))
+        moe4.moe4_quantize_mxfp8(torch.zeros(40, dtype=BF, device="cuda")[4:36], torch.empty(32, dtype=torch.uint8, device="cuda"),
+                                 torch.empty(1, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError, match="outs\\[0\\] has dtype"):
         moe4.GradList([x], [w])
     with pytest.raises(ValueError, match="outs\\[0\\] has shape"):
@@ -713,13 +713,13 @@ def test_graph_capture_of_the_dense_step():
     blk = Block("graph", 264, 136, False, True, True)
     T, H, I = 130, 264, 136
     w, _ = draw(rng("gw"), (H,))
-    z = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype, device=DEV)   # noqa: E731
+    z = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype, device="cuda")   # noqa: E731
     b = dict(x=z(T, H), res=z(T, H), dy=z(T, H), s=z(T, H), n=z(T, H), r=z(T, dtype=F32), gu=z(T, 2 * I, dtype=F32), o=z(T, H),
              dn=z(T, H), dx=z(T, H), dw=z(H, dtype=F32), wg=z(2 * I, H), wd=z(H, I), bg=z(2 * I), bd=z(H), norm=z(1, dtype=F32))
     gl = moe4.GradList([b["wg"], b["wd"], b["bg"], b["bd"], b["dw"]])
     ws = blk.ws(T, True)
-    nws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device=DEV)
-    gws = torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device=DEV)
+    nws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    gws = torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device="cuda")
 
     def step():
         moe4.moe4_add_rmsnorm(b["x"], w, 1e-6, residual=b["res"], sum_out=b["s"], out=b["n"], rstd=b["r"])
@@ -763,7 +763,7 @@ def test_graph_capture_of_every_kernel_family(T, H, I, mx):
     # large tiles, split products, skinny kernels: captured without an eager call before
     blk = Block("capture", H, I, mx, mx, True)
     x, xs, _ = blk.tokens(T)
-    out, base = torch.zeros((T, H), dtype=BF, device=DEV), torch.zeros((T, H), dtype=BF, device=DEV)
+    out, base = torch.zeros((T, H), dtype=BF, device="cuda"), torch.zeros((T, H), dtype=BF, device="cuda")
     ws = blk.ws(T)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
@@ -784,16 +784,16 @@ def test_graph_capture_of_every_kernel_family(T, H, I, mx):
 def test_offsets_past_32_bits():
     # tensors of more than 2^32 bytes: the last rows are those of a call on them alone
     H, T, tail = 2048, 1_060_000, 300
-    gen = torch.Generator(device=DEV).manual_seed(3)
-    x = torch.randn((T, H), generator=gen, device=DEV, dtype=BF)
-    w = torch.ones(H, device=DEV)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((T, H), generator=gen, device="cuda", dtype=BF)
+    w = torch.ones(H, device="cuda")
     out = torch.empty_like(x)
-    q, s = torch.empty((T, H), dtype=torch.uint8, device=DEV), torch.empty((T, H // 32), dtype=torch.uint8, device=DEV)
-    rstd = torch.empty(T, device=DEV)
+    q, s = torch.empty((T, H), dtype=torch.uint8, device="cuda"), torch.empty((T, H // 32), dtype=torch.uint8, device="cuda")
+    rstd = torch.empty(T, device="cuda")
     moe4.moe4_add_rmsnorm(x, w, 1e-6, out=out, out_q=q, out_s=s, rstd=rstd)
     xe = x[-tail:].clone()
-    o2, r2 = torch.empty_like(xe), torch.empty(tail, device=DEV)
-    q2, s2 = torch.empty((tail, H), dtype=torch.uint8, device=DEV), torch.empty((tail, H // 32), dtype=torch.uint8, device=DEV)
+    o2, r2 = torch.empty_like(xe), torch.empty(tail, device="cuda")
+    q2, s2 = torch.empty((tail, H), dtype=torch.uint8, device="cuda"), torch.empty((tail, H // 32), dtype=torch.uint8, device="cuda")
     moe4.moe4_add_rmsnorm(xe, w, 1e-6, out=o2, out_q=q2, out_s=s2, rstd=r2)
     # (another number of rows takes another split of the row's sum: bf16 steps apart at most)
     assert torch.allclose(rstd[-tail:], r2, rtol=1e-5, atol=0)
@@ -827,7 +827,7 @@ def test_other_streams():
     blk = Block("stream", 136, 72)
     T = 100
     x, _, _ = blk.tokens(T)
-    base = torch.empty((T, 136), dtype=BF, device=DEV)
+    base = torch.empty((T, 136), dtype=BF, device="cuda")
     moe4.moe4_ffn_forward(blk.ffn, x, base, ws=blk.ws(T))
     st = torch.cuda.Stream()
     a, c = torch.empty_like(base), torch.empty_like(base)
@@ -859,14 +859,14 @@ def test_block_with_routed_experts():
     w1, w1v = draw(r, (H,))
     w2, w2v = draw(r, (H,))
     wr, wrv = draw(r, (spec.E, H), std=1 / math.sqrt(H))
-    h = torch.empty((T, H), dtype=BF, device=DEV)
+    h = torch.empty((T, H), dtype=BF, device="cuda")
     n = torch.empty_like(h)
-    rstd = torch.empty(T, device=DEV)
+    rstd = torch.empty(T, device="cuda")
     moe4.moe4_add_rmsnorm(x, w1, 1e-6, residual=res, sum_out=h, out=n, rstd=rstd)
-    lg = torch.empty((T, spec.E), device=DEV)
+    lg = torch.empty((T, spec.E), device="cuda")
     moe4.moe4_router_logits(n, wr, lg)
     routed = run_layer(ex, n, lg, k)
-    gu = torch.empty((T, 2 * I), device=DEV)
+    gu = torch.empty((T, 2 * I), device="cuda")
     stream = torch.empty_like(h)
     moe4.moe4_ffn_forward(blk.ffn, n, stream, residual=h, save_gu=gu, ws=blk.ws(T))
     h2, n2 = torch.empty_like(h), torch.empty_like(h)
@@ -887,11 +887,11 @@ def test_block_with_routed_experts():
     # backward: the stream's gradient through the dense block (a routed part added), the norm
     dy, dyv = draw(r, (T, H), std=0.1)
     droute, drv = draw(r, (T, H), F32, 0.1)
-    dn = torch.empty((T, H), device=DEV)
-    dwg, dwd = torch.empty((2 * I, H), device=DEV), torch.empty((H, I), device=DEV)
+    dn = torch.empty((T, H), device="cuda")
+    dwg, dwd = torch.empty((2 * I, H), device="cuda"), torch.empty((H, I), device="cuda")
     moe4.moe4_ffn_backward(blk.ffn, n, gu, dy, dx=dn, dx_add=droute, dw_gu=dwg, dw_dn=dwd, ws=blk.ws(T, True))
-    dx, dw = torch.empty_like(h), torch.empty(H, device=DEV)
-    nws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device=DEV)
+    dx, dw = torch.empty_like(h), torch.empty(H, device="cuda")
+    nws = torch.empty(moe4.moe4_add_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
     moe4.moe4_add_rmsnorm_backward(dn, h, w1, rstd, dx, dres=dy, dweight=dw, ws=nws)
     b = dense.ffn_backward(nv, fo["gu"], dyv, blk.wg, blk.wd, blk.layout, blk.act)
     wx, ww = dense.add_rmsnorm_backward(b["dx"] + drv, sv, w1v, rs, dyv)
@@ -900,7 +900,42 @@ def test_block_with_routed_experts():
     grads = [dwg, dwd, dw]
     gl = moe4.GradList(grads)
     total = dense.grad_norm([val(g) for g in grads])
-    norm = torch.empty(1, device=DEV)
-    moe4.moe4_clip_grads(gl, total / 2, norm, torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device=DEV))
+    norm = torch.empty(1, device="cuda")
+    moe4.moe4_clip_grads(gl, total / 2, norm, torch.empty(moe4.moe4_grad_workspace_size(gl), dtype=torch.uint8, device="cuda"))
     assert abs(norm.item() - total) <= 2 * U32 * total
     assert abs(dense.grad_norm([val(g) for g in grads]) - total / 2) <= 1e-5 * total
+
+
+def test_clip_refuses_outputs_that_overlap():
+    a = torch.arange(64, dtype=F32, device="cuda")
+    norm, ws = torch.empty(1, dtype=F32, device="cuda"), None
+    before = a.clone()
+    twice = moe4.GradList([a, torch.ones(4, device="cuda"), a])
+    ws = torch.empty(moe4.moe4_grad_workspace_size(twice), dtype=torch.uint8, device="cuda")
+    # read only, a gradient counts as often as it is in the list: sum i^2 for i < 64 is 85344
+    moe4.moe4_grad_norm(twice, norm, ws)
+    assert abs(norm.item() - (2 * 85344 + 4) ** 0.5) <= 2.0 ** -23 * norm.item()
+    b = torch.empty(64, dtype=F32, device="cuda")
+    refused = [(twice, "outs\\[2\\] overlaps entry 0"),
+               (moe4.GradList([a[:32], a[16:48]]), "outs\\[1\\] overlaps entry 0"),
+               (moe4.GradList([a, b], [b, a]), "overlaps entry"),
+               (moe4.GradList([a[:32], a[32:]], [b[:32], b[16:48]]), "outs\\[1\\] overlaps entry 0"),
+               (moe4.GradList([a[16:48]], [a[:32]]), "overlaps entry 0")]
+    for g, what in refused:
+        with pytest.raises(ValueError, match=what):
+            moe4.moe4_clip_grads(g, 1.0, norm, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, before)
+    # neighbours, a gradient read by two entries, and in place beside out of place
+    ok = moe4.GradList([a[:32], a[32:], a[:32]], [a[:32], b[:32], b[32:]])
+    assert ok.clash is not None   # entry 2 reads what entry 0 writes
+    ok = moe4.GradList([a[:32], a[32:], a[32:]], [a[:32], b[:32], b[32:]])
+    moe4.moe4_clip_grads(ok, 1e9, norm, ws)
+    assert torch.equal(b[:32], a[32:]) and torch.equal(b[32:], a[32:]) and torch.equal(a, before)
+    moe4.moe4_clip_grads(moe4.GradList([a[:32], a[32:]]), 1e9, norm, ws)
+
+
+def test_quantize_refuses_a_scalar():
+    x = torch.ones((), dtype=F32, device="cuda")
+    with pytest.raises(ValueError, match="no dimension"):
+        moe4.moe4_quantize_mxfp8(x, x, x)
