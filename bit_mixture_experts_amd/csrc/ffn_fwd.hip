@@ -8,8 +8,8 @@
 // 1.29 PFLOP/s (a large library product reaches 1.24 to 1.55 on this card; of the k loop's
 // cycles 85% multiply, at a clock that the load pulls to 1.9 GHz); 2048 in MXFP8 at H = I = 2880
 // 82 us, 1.24 PFLOP/s (the second product's 96 large or 368 small tiles do not fill the chip).
-// Few tokens are bound by launches and by load instructions: one token at H 2048, I 768 5.5 + 3.9
-// us, 16 in MXFP8 at 2880, 2880 11.5 + 4.9 us; one token at H 4096, I 8192 43 us, 4.7 TB/s.
+// Few tokens are bound by launches and by load instructions: one token at H 2048, I 768 5.5 + 3.8
+// us, 16 in MXFP8 at 2880, 2880 12.5 + 5.1 us; one token at H 4096, I 8192 43 us, 4.7 TB/s.
 #include "ffn.hpp"
 
 namespace moe4 {
@@ -33,22 +33,30 @@ __device__ __forceinline__ int gu_col(int layout, int I, int j, bool up) {
   return layout == MOE4_GU_HALVES ? (up ? I + j : j) : 2 * j + (up ? 1 : 0);
 }
 
-// the biases of 8 pairs j .. j+7: gates, then ups; zeros without
-__device__ __forceinline__ void load_bias8(const GateUpArgs& a, int j, float* b) {
+// the biases of 8 pairs j .. j+7 as they lie in memory (bf16); zeros without
+struct RawBias {
+  u32x4 v[2];
+};
+__device__ __forceinline__ RawBias load_bias8(const GateUpArgs& a, int j) {
+  RawBias r = {};
+  if (!a.bias || j >= a.I) return r;
+  const bool halves = a.layout == MOE4_GU_HALVES;
+  r.v[0] = *reinterpret_cast<const u32x4*>(a.bias + (halves ? j : 2 * j));
+  r.v[1] = *reinterpret_cast<const u32x4*>(a.bias + (halves ? a.I + j : 2 * j + 8));
+  return r;
+}
+// gates, then ups
+__device__ __forceinline__ void unpack_bias8(const GateUpArgs& a, const RawBias& r, float* b) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) b[i] = 0.0f;
-  if (!a.bias || j >= a.I) return;
-  if (a.layout == MOE4_GU_HALVES) {
-    load8_bf16(a.bias + j, b);
-    load8_bf16(a.bias + a.I + j, b + 8);
-  } else {
-    float x[16];
-    load8_bf16(a.bias + 2 * j, x);
-    load8_bf16(a.bias + 2 * j + 8, x + 8);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      b[i] = x[2 * i];
-      b[8 + i] = x[2 * i + 1];
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t h = r.v[0][i / 2], f = r.v[i / 4][i % 4];
+    const uint32_t u = r.v[1][i / 2];
+    if (a.layout == MOE4_GU_HALVES) {
+      b[i] = i & 1 ? bf16hi(h) : bf16lo(h);
+      b[8 + i] = i & 1 ? bf16hi(u) : bf16lo(u);
+    } else {
+      b[i] = bf16lo(f);
+      b[8 + i] = bf16hi(f);
     }
   }
 }
@@ -136,7 +144,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_gate_up(GateUpArgs a) {
     }
   }
   float bias[16];   // the same pairs in every turn
-  load_bias8(a, j0 + lane_a<S, true>(), bias);
+  unpack_bias8(a, load_bias8(a, j0 + lane_a<S, true>()), bias);
   for_each8<S, true, 1>(acc, stage_mem, [](int, int) { return NoPre{}; },
                         [&](int row, int jj, float* g, float* u) {
     const int t = t0 + row, j = j0 + jj;
@@ -158,7 +166,7 @@ __global__ __launch_bounds__(256) void k_ffn_gate_up_join(const GateUpArgs a) {
   float g[8] = {}, u[8] = {};
   if (on) {
     float bias[16];
-    load_bias8(a, j, bias);
+    unpack_bias8(a, load_bias8(a, j), bias);
     for (int s = 0; s < a.splits; ++s) {
       const float* p = a.part + ((int64_t)s * a.T + t) * 2 * a.I + j;
       float x[8], y[8];
@@ -213,6 +221,11 @@ __global__ __launch_bounds__(256) void k_ffn_join(const JoinArgs a) {
 // LDS, in the order of the K splits. What bounds it at these sizes is the number of load
 // instructions of a CU (each touches 16 rows), so a wave keeps its tokens' operands for all
 // its row tiles and asks for nothing past its range.
+//
+// MXFP8 operands are taken to bf16 on the way (exact) and multiplied as such: the e4m3 matrix
+// instruction keeps a product only to 2^-16 of its block's largest, which sends a few more values
+// of h to a neighbouring code. The loads hide most of it: 16 tokens at 2880, 2880 17.0 us with that
+// instruction and 17.6 so, 2.6e-3 and 1.7e-3 off in relative 2-norm, 1.7e-3 being bf16's rounding.
 template <int RT, int KS, int NT, bool FP8>
 struct Skinny {
   static constexpr int kThreads = KS * 64;
@@ -253,9 +266,9 @@ struct Skinny {
       xo[i] = t < nt ? (uint32_t)t * kb : (uint32_t)kOob;
       xso[i] = t < nt ? (uint32_t)t * nb : (uint32_t)kOob;
     }
-    // the lane's two 16-byte pieces of a 128-byte step: neighbours for bf16 (any split of k
-    // that both operands share will do), k = 64 c + 16 g for e4m3, where the scales fix it
-    const int p0 = FP8 ? 16 * g : 32 * g, p1 = p0 + (FP8 ? 64 : 16);
+    // a lane's two 16-byte pieces of a 128-byte step are neighbours (any split of k that both
+    // operands share will do): for e4m3 they are a block with one scale
+    const int p0 = 32 * g, p1 = p0 + 16;
     const int steps = (kb + 127) / 128;
     const int s0 = steps * ks / KS, s1 = steps * (ks + 1) / KS;
     auto load = [&](Batch& b, int s) {
@@ -288,29 +301,28 @@ struct Skinny {
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto join = [](u32x4 lo, u32x4 hi) {
-      const auto v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      return __builtin_bit_cast(i32x8, v);
+    // chunk c of 8 k of a step in a lane, as bf16
+    constexpr int kC = FP8 ? 4 : 2;
+    auto operand = [](const u32x4* v, int c, uint32_t scale) {
+      if constexpr (FP8) return mx_bf16x8(v[c / 2][2 * (c % 2)], v[c / 2][2 * (c % 2) + 1], scale);
+      else return __builtin_bit_cast(bf16x8, v[c]);
     };
     auto mul = [&](const Batch& b) {
 #pragma unroll
       for (int i = 0; i < kU; ++i)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int c = 0; c < kC; ++c) {
+          bf16x8 x[NT];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if constexpr (FP8) {
-              acc[r][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  join(b.w[i][r][0], b.w[i][r][1]), join(b.x[i][j][0], b.x[i][j][1]), acc[r][j], 0,
-                  0, 0, (int)b.ws[i][r], 0, (int)b.xs[i][j]);
-            } else {
+          for (int j = 0; j < NT; ++j) x[j] = operand(b.x[i][j], c, b.xs[FP8 ? i : 0][j]);
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, b.w[i][r][c]),
-                    __builtin_bit_cast(bf16x8, b.x[i][j][c]), acc[r][j], 0, 0, 0);
-            }
+          for (int r = 0; r < RT; ++r) {
+            const bf16x8 w = operand(b.w[i][r], c, b.ws[FP8 ? i : 0][r]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[j], acc[r][j], 0, 0, 0);
           }
+        }
     };
     // (a batch that follows is asked for in straight line with the one before it: behind a
     // branch of its own the compiler would wait for all loads in flight)
@@ -357,6 +369,11 @@ __global__ __launch_bounds__(KS * 64) void k_ffn_gate_up_skinny(const GateUpArgs
   extern __shared__ __attribute__((aligned(16))) float red[];
   constexpr int NJ = 8 * RT;   // pairs of the workgroup: gate rows first, then up rows
   const int j0 = blockIdx.x * NJ, t0 = blockIdx.y * 16 * NT, nt = min(16 * NT, a.T - t0);
+  // 8 pairs of a token to a thread; NJ = 32 gives a block of MXFP8 to four neighbours
+  static_assert(16 * NT * RT <= S::kThreads, "a thread for every 8 pairs");
+  const int m = threadIdx.x / RT, jj = 8 * (threadIdx.x % RT);
+  // what the end needs from memory is asked for first
+  const RawBias raw = load_bias8(a, j0 + jj);
   S::run(
       a.W, 2 * (int64_t)a.I,
       [&](int rt) {
@@ -364,20 +381,17 @@ __global__ __launch_bounds__(KS * 64) void k_ffn_gate_up_skinny(const GateUpArgs
         return j < a.I ? gu_col(a.layout, a.I, j, r >= NJ) : -1;
       },
       a.X, t0, nt, a.H, red);
-  // 8 pairs of a token to a thread; NJ = 32 gives a block of MXFP8 to four neighbours
-  for (int i = threadIdx.x; i < 16 * NT * RT; i += S::kThreads) {
-    const int m = i / RT, jj = 8 * (i % RT);
-    const bool on = m < nt && j0 + jj < a.I;
-    float g[8], u[8], bias[16];
-    load_bias8(a, j0 + jj, bias);
+  if (m >= 16 * NT) return;
+  const bool on = m < nt && j0 + jj < a.I;
+  float g[8], u[8], bias[16];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      g[q] = S::sum(red, jj + q, m);
-      u[q] = S::sum(red, NJ + jj + q, m);
-    }
-    if (on) finish8(a, t0 + m, j0 + jj, bias, g, u);
-    store_h8<FP8>(a, t0 + m, j0 + jj, on, g);
+  for (int q = 0; q < 8; ++q) {
+    g[q] = S::sum(red, jj + q, m);
+    u[q] = S::sum(red, NJ + jj + q, m);
   }
+  unpack_bias8(a, raw, bias);
+  if (on) finish8(a, t0 + m, j0 + jj, bias, g, u);
+  store_h8<FP8>(a, t0 + m, j0 + jj, on, g);
 }
 
 template <int RT, int KS, int NT, bool FP8>
@@ -385,6 +399,24 @@ __global__ __launch_bounds__(KS * 64) void k_ffn_down_skinny(const FfnProduct p)
   using S = Skinny<RT, KS, NT, FP8>;
   extern __shared__ __attribute__((aligned(16))) float red[];
   const int a0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * 16 * NT, nt = min(16 * NT, p.nb - t0);
+  // what the end needs from memory is asked for first: bias and addend of the thread's values
+  constexpr int kAll = 16 * NT * 16 * RT, kTurns = (kAll + S::kThreads - 1) / S::kThreads;
+  uint32_t bias[kTurns], add[kTurns];
+  const bool add32 = p.add_dtype == MOE4_DTYPE_F32;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int n = 0; n < kTurns; ++n) {
+      const int i = n * S::kThreads + threadIdx.x, m = i / (16 * RT), c = i % (16 * RT);
+      if (m < nt && a0 + c < p.na) f(n, m, c, (int64_t)(t0 + m) * p.na + a0 + c);
+    }
+  };
+#pragma unroll
+  for (int n = 0; n < kTurns; ++n) bias[n] = add[n] = 0;
+  each([&](int n, int, int c, int64_t at) {
+    if (p.bias) bias[n] = p.bias[a0 + c];
+    if (p.add)
+      add[n] = add32 ? static_cast<const uint32_t*>(p.add)[at] : static_cast<const uint16_t*>(p.add)[at];
+  });
   S::run(
       p.A, p.na,
       [&](int rt) {
@@ -392,18 +424,13 @@ __global__ __launch_bounds__(KS * 64) void k_ffn_down_skinny(const FfnProduct p)
         return r < p.na ? r : -1;
       },
       p.B, t0, nt, p.K, red);
-  for (int i = threadIdx.x; i < 16 * NT * 16 * RT; i += S::kThreads) {
-    const int m = i / (16 * RT), c = i % (16 * RT);
-    if (m >= nt || a0 + c >= p.na) continue;
-    const int64_t at = (int64_t)(t0 + m) * p.na + a0 + c;
+  each([&](int n, int m, int c, int64_t at) {
     float v = S::sum(red, c, m);
-    if (p.bias) v += bf16_to_f32(p.bias[a0 + c]);
-    if (p.add)
-      v += p.add_dtype == MOE4_DTYPE_F32 ? static_cast<const float*>(p.add)[at]
-                                         : bf16_to_f32(static_cast<const uint16_t*>(p.add)[at]);
+    v += __uint_as_float(bias[n] << 16);
+    v += __uint_as_float(add32 ? add[n] : add[n] << 16);
     if (p.out_dtype == MOE4_DTYPE_F32) static_cast<float*>(p.out)[at] = v;
     else static_cast<uint16_t*>(p.out)[at] = f32_to_bf16(v);
-  }
+  });
 }
 
 // Row tiles of a workgroup of the bf16 kernels and of the second product: a wave's loads are 2 RT

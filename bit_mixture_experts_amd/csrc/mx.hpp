@@ -47,4 +47,16 @@ __device__ __forceinline__ u32x2 mx_quantize8(const float* v, uint32_t& byte) {
   return q;
 }
 
+// 8 codes (two dwords) of a block with scale `byte` as bf16: exact from 2^-133 on, e4m3's four
+// significant bits and the scale's power of two fit; a NaN scale gives NaNs
+__device__ __forceinline__ bf16x8 mx_bf16x8(uint32_t lo, uint32_t hi, uint32_t byte) {
+  const float f = __uint_as_float(byte << 23);
+  u32x4 r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true));
+  return __builtin_bit_cast(bf16x8, r);
+}
+
 }  // namespace moe4

@@ -409,6 +409,44 @@ def test_ffn_forward_split_k(T, H, I, mx, clamped):
     ffn_check(blk, T, VARIANTS["tiled"], F32, None, False)
 
 
+@pytest.mark.parametrize("T,H,I", [(1, 96, 6176), (16, 64, 3104), (19, 32, 3136), (32, 96, 6144), (7, 6176, 32),
+                                   (30, 6144, 96), (12, 12320, 32), (25, 12288, 64), (33, 64, 3104)])
+def test_ffn_mx_few_tokens_wide(T, H, I):
+    # every count of weight rows to a workgroup, in both products
+    blk = Block("wide", H, I, True, T % 2 == 1, True)
+    ffn_check(blk, T, VARIANTS["skinny"], BF, BF, True)
+    ffn_check(blk, T, VARIANTS["skinny"], F32, None, False)
+
+
+def test_ffn_mx_every_code_and_scale():
+    # few tokens: each pre-activation is one code of one block times 1, which has to be exact
+    H, I = 32, 1024
+    codes = np.empty((2 * I, H), np.uint8)
+    codes[:] = (32 * (np.arange(2 * I) // 256))[:, None] + np.arange(32)
+    scales = (np.arange(2 * I) % 256).astype(np.uint8)[:, None]
+    w = dense.mxfp8_values(codes, scales)   # NaN for code 0x7F, 0xFF and scale 255
+    ffn = moe4.Ffn(moe4.MOE4_FFN_MXFP8, to_dev(codes), to_dev(np.zeros((H, I), np.uint8)), H=H, I=I,
+                   gu_s=to_dev(scales), dn_s=to_dev(np.full((H, I // 32), 127, np.uint8)),
+                   gu_layout=moe4.MOE4_GU_HALVES, act=moe4.MOE4_ACT_SWIGLU, variant=moe4.MOE4_VARIANT_SKINNY)
+    x = np.zeros((H, H), np.uint8)
+    x[np.arange(H), np.arange(H)] = 0x38   # 1.0
+    gu = out_t((H, 2 * I), F32)
+    out = torch.empty((H, H), dtype=F32, device="cuda")
+    ws = torch.empty(moe4.moe4_ffn_workspace_size(ffn, H), dtype=torch.uint8, device="cuda")
+    moe4.moe4_ffn_forward(ffn, to_dev(x), out, x_s=to_dev(np.full((H, 1), 127, np.uint8)), save_gu=gu.t, ws=ws)
+    got, want = gu.t.double().cpu().numpy(), w.T
+    bad = np.isnan(w).any(1)   # a NaN anywhere in a weight's row reaches every token
+    assert bad.sum() == 256 * 2 + 6 and np.isnan(got[:, bad]).all()
+    # a row with a value past fp32's range holds an infinity, which times 0 is a NaN: left out
+    bad |= (np.abs(w) > 3.38e38).any(1)
+    got, want = got[:, ~bad], want[:, ~bad]
+    assert want.shape[1] >= 2048 - 518 - 8 * 8
+    # below 2^-126 (fp32's and bf16's normal range) a value may be rounded or become zero
+    small = np.abs(want) < 2.0 ** -126
+    assert np.array_equal(got[~small], want[~small])
+    assert np.all(np.abs(got[small] - want[small]) <= 2.0 ** -126)
+
+
 def test_ffn_forward_in_place_residual():
     blk = Block("inplace", 264, 136)
     for T in (5, 200):
