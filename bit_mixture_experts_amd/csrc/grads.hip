@@ -6,8 +6,8 @@
 // for any finite gradients (an fp32 square overflows from 1.9e19 on and vanishes below
 // 1e-23), and the fp64 adds hide behind the loads.
 //
-// Bound by HBM. 88 million fp32 values in 48 tensors (352 MB): squares 81 us, 4.3 TB/s; scaling
-// to another place 108 us, 6.5 TB/s, part of its reads from the caches. Fp64 partial sums, at most
+// Bound by HBM. 88 million fp32 values in 48 tensors (352 MB): squares 81-92 us, 4.1 TB/s; scaling
+// to another place 108-115 us, 6.3 TB/s, part of its reads from the caches. Fp64 partial sums, at most
 // 2048 a launch (1024 left CUs idle between chunks: 88 us; chunks of half the size 86), are added
 // up by every scaling workgroup for itself, which saves a launch.
 #include "internal.hpp"

@@ -406,8 +406,11 @@ _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
+_DT = {torch.bfloat16: MOE4_DTYPE_BF16, torch.float32: MOE4_DTYPE_F32}
+
+
 def _dt(t):
-    return 0 if t is None else MOE4_DTYPE_F32 if t.dtype == torch.float32 else MOE4_DTYPE_BF16
+    return 0 if t is None else _DT.get(t.dtype, 0)   # what is neither is refused as a pointer
 
 
 class _Call:
@@ -422,9 +425,11 @@ class _Call:
     def ptr(self, t, name, shape, dtypes):
         if t is None:
             return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.get_device() != self.dev:
+        try:
+            dev = t.get_device()
+        except AttributeError:
+            raise TypeError(f"{name} must be a torch.Tensor") from None
+        if dev != self.dev:
             self.place(t, name)
         if t.dtype not in dtypes or not t.is_contiguous():
             _ptr(t, dtypes, name)
@@ -448,7 +453,9 @@ class _Call:
             return None, 0
         if ws.get_device() != self.dev:
             self.place(ws, "ws")
-        return _ptr(ws, None, "ws"), ws.numel() * ws.element_size()
+        if not ws.is_contiguous():
+            _ptr(ws, None, "ws")
+        return ws.data_ptr(), ws.nbytes
 
     def stream(self, stream):
         if stream is None:
@@ -477,13 +484,18 @@ def moe4_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, out_
         _int32(c.fn, T=T, H=H)
     if sum_out is not None and residual is not None and sum_out.dtype != residual.dtype:
         raise TypeError("sum_out must have the residual's dtype")
-    px = c.ptr(x, "x", sh, _FLOATS)
-    _check(_lib.moe4_add_rmsnorm(
-        px, _dt(x), c.ptr(residual, "residual", sh, _FLOATS), _dt(residual),
-        c.ptr(sum_out, "sum_out", sh, _FLOATS), c.ptr(weight, "weight", (H,), _FLOATS), _dt(weight),
-        T, H, eps, c.ptr(out, "out", sh, _BF16), c.ptr(out_q, "out_q", sh, _CODES),
-        c.ptr(out_s, "out_s", (T, H // 32), _SCALES), c.ptr(rstd, "rstd", (T,), _F32),
-        c.stream(stream)))
+    ptr = c.ptr
+    rc = _lib.moe4_add_rmsnorm(
+        ptr(x, "x", sh, _FLOATS), _dt(x),
+        None if residual is None else ptr(residual, "residual", sh, _FLOATS), _dt(residual),
+        None if sum_out is None else ptr(sum_out, "sum_out", sh, _FLOATS),
+        ptr(weight, "weight", (H,), _FLOATS), _dt(weight), T, H, eps,
+        None if out is None else ptr(out, "out", sh, _BF16),
+        None if out_q is None else ptr(out_q, "out_q", sh, _CODES),
+        None if out_s is None else ptr(out_s, "out_s", (T, H // 32), _SCALES),
+        None if rstd is None else ptr(rstd, "rstd", (T,), _F32), c.stream(stream))
+    if rc:
+        _check(rc)
 
 
 def moe4_add_rmsnorm_workspace_size(T, H):
@@ -522,9 +534,11 @@ def moe4_quantize_mxfp8(x, q, s, stream=None):
         raise ValueError("quantize_mxfp8: x has no dimension")
     K = sh[-1]
     R = x.numel() // K if K else 0
-    _check(_lib.moe4_quantize_mxfp8(c.ptr(x, "x", sh, _FLOATS), _dt(x), R, K,
-                                    c.ptr(q, "q", sh, _CODES),
-                                    c.ptr(s, "s", sh[:-1] + (K // 32,), _SCALES), c.stream(stream)))
+    rc = _lib.moe4_quantize_mxfp8(c.ptr(x, "x", sh, _FLOATS), _dt(x), R, K,
+                                  c.ptr(q, "q", sh, _CODES),
+                                  c.ptr(s, "s", sh[:-1] + (K // 32,), _SCALES), c.stream(stream))
+    if rc:
+        _check(rc)
 
 
 class Ffn:
@@ -585,12 +599,16 @@ def moe4_ffn_forward(ffn, x, out, x_s=None, residual=None, save_gu=None, ws=None
         _int32(c.fn, T=T)
     mx = ffn.desc.format == MOE4_FFN_MXFP8
     pw, nw = c.ws(ws)
-    _check(_lib.moe4_ffn_forward(
-        ffn.ref, c.ptr(x, "x", (T, H), _CODES if mx else _BF16),
-        c.ptr(x_s, "x_s", (T, H // 32), _SCALES), T,
-        c.ptr(residual, "residual", (T, H), _FLOATS), _dt(residual),
-        c.ptr(out, "out", (T, H), _FLOATS), _dt(out),
-        c.ptr(save_gu, "save_gu", (T, 2 * ffn.I), _F32), pw, nw, c.stream(stream)))
+    ptr, sh = c.ptr, (T, H)
+    rc = _lib.moe4_ffn_forward(
+        ffn.ref, ptr(x, "x", sh, _CODES if mx else _BF16),
+        None if x_s is None else ptr(x_s, "x_s", (T, H // 32), _SCALES), T,
+        None if residual is None else ptr(residual, "residual", sh, _FLOATS), _dt(residual),
+        ptr(out, "out", sh, _FLOATS), _dt(out),
+        None if save_gu is None else ptr(save_gu, "save_gu", (T, 2 * ffn.I), _F32), pw, nw,
+        c.stream(stream))
+    if rc:
+        _check(rc)
 
 
 def moe4_ffn_backward(ffn, x, save_gu, dy, dx=None, dx_add=None, dw_gu=None, dw_dn=None,
