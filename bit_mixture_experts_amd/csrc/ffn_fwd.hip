@@ -433,6 +433,9 @@ __global__ __launch_bounds__(KS * 64) void k_ffn_down_skinny(const FfnProduct p)
   });
 }
 
+// Eight waves split K. (In MXFP8, one and 16 tokens at 2880, 2880 to 4096, 8192, twelve took 1%
+// longer, sixteen, with 128 registers a lane, 25 to 45%.)
+//
 // Row tiles of a workgroup of the bf16 kernels and of the second product: a wave's loads are 2 RT
 // for weights and 2 NT for tokens a step, so more row tiles save token loads, as long as
 // there is a workgroup for most CUs. Us at 16, 64 tokens, H 4096, I 8192: one row tile 60,
@@ -451,9 +454,9 @@ hipError_t launch_skinny(const GateUpArgs& g, const FfnProduct& d, hipStream_t s
   const uint32_t nt = (g.T + 16 * NT - 1) / (16 * NT);
   auto gate_up = [&](auto rc) {
     // MXFP8: h is quantised in blocks of 32, so a workgroup takes 32 pairs
-    constexpr int kRt = FP8 ? 4 : decltype(rc)::value, kKs = FP8 && NT == 1 ? 12 : 8;
-    using G = Skinny<kRt, kKs, NT, FP8>;
-    auto* k = &k_ffn_gate_up_skinny<kRt, kKs, NT, FP8>;
+    constexpr int kRt = FP8 ? 4 : decltype(rc)::value;
+    using G = Skinny<kRt, 8, NT, FP8>;
+    auto* k = &k_ffn_gate_up_skinny<kRt, 8, NT, FP8>;
     hipError_t e = allow_lds(k, G::kLds);
     if (e != hipSuccess) return e;
     k<<<dim3((g.I + 8 * kRt - 1) / (8 * kRt), nt), G::kThreads, G::kLds, s>>>(g);
