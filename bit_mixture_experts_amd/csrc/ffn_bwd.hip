@@ -21,7 +21,7 @@ struct DhArgs {
   const float* gu;      // [T, 2I]
   uint16_t* dgu;        // [T, 2I]
   uint16_t* h;          // [T, I] or null (no gradient of W_dn wanted)
-  float* part;          // [row tiles][2I] column sums of dGU, or null
+  float* part;          // [row tiles, or the join's rows of workgroups][2I] column sums of dGU, or null
   int splits;           // parts of k (few tokens and a wide stream)
   float* dh;            // [splits][T][I] sums to be joined
 };
@@ -183,23 +183,49 @@ hipError_t launch_grads(GradArgs a, int n, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The parts of a split dH, joined: 8 pairs of a token to a thread.
+// The parts of a split dH, joined: 8 pairs of a token to a thread, 128 pairs of kJoinRows tokens
+// to a workgroup, which leaves its column sums of dGU in part, in fp32 before the rounding as
+// the whole dH's epilogue does. (Summed from dGU in memory they cost a pass of their own and
+// hold each term's rounding to bf16. Us of the whole backward with biases: 100 tokens at 2880,
+// 2880 62.5 that way and 59.3 this, 1024 175 and 171.5, 128 at H 4096, I 8192 166.3 and 160.7.)
+constexpr int kJoinRows = 16;
 template <int LAYOUT, int ACT>
 __global__ __launch_bounds__(256) void k_ffn_dh_join(const DhArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per = a.I / 8;
-  const int64_t t = i / per;
-  if (t >= a.T) return;
-  const int j = (int)(i - t * per) * 8;
-  const RawGu r = Pairs8<LAYOUT, ACT>::load(a, t, j);
-  float dh[8] = {}, d[16];
-  for (int s = 0; s < a.splits; ++s) {
-    float x[8];
-    load8_f32(a.dh + ((int64_t)s * a.T + t) * a.I + j, x);
+  __shared__ __attribute__((aligned(16))) f32x4 red[4][16][4];   // [wave][8 pairs][16 values]
+  using P = Pairs8<LAYOUT, ACT>;
+  const int x = threadIdx.x & 15, w = wave_id();
+  const int t = blockIdx.y * kJoinRows + (threadIdx.x >> 4), j = (blockIdx.x * 16 + x) * 8;
+  float d[16] = {};
+  if (t < a.T && j < a.I) {
+    const RawGu r = P::load(a, t, j);
+    float dh[8] = {};
+    for (int s = 0; s < a.splits; ++s) {
+      float v[8];
+      load8_f32(a.dh + ((int64_t)s * a.T + t) * a.I + j, v);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dh[q] += x[q];
+      for (int q = 0; q < 8; ++q) dh[q] += v[q];
+    }
+    P::finish(a, t, j, dh, r, d);
   }
-  Pairs8<LAYOUT, ACT>::finish(a, t, j, dh, r, d);
+  if (!a.part) return;
+  // the wave's four tokens, then the four waves in order
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    d[i] += __shfl_xor(d[i], 16, kWave);
+    d[i] += __shfl_xor(d[i], 32, kWave);
+  }
+  if (lane_id() < 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      red[w][x][i] = f32x4{d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
+  }
+  __syncthreads();
+  // four values of 8 pairs to a thread of the first wave
+  const int c = threadIdx.x >> 2, i = threadIdx.x & 3, jc = (blockIdx.x * 16 + c) * 8;
+  if (w != 0 || jc >= a.I) return;
+  const f32x4 s = red[0][c][i] + red[1][c][i] + red[2][c][i] + red[3][c][i];
+  float* o = a.part + (int64_t)blockIdx.y * 2 * a.I;
+  *reinterpret_cast<f32x4*>(o + (i < 2 ? P::col0(jc) + 4 * i : P::col1(a, jc) + 4 * (i - 2))) = s;
 }
 
 // Column sums of a bf16 matrix [T, N]: workgroup (x, p) sums part p's rows of 512 columns in
@@ -247,8 +273,7 @@ hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
   k<<<(uint32_t)(tiles_of<S>(a.I, a.T) * a.splits), S::kThreads, S::kLds, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  k_ffn_dh_join<LAYOUT, ACT>
-      <<<(uint32_t)(((int64_t)a.T * (a.I / 8) + 255) / 256), 256, 0, s>>>(a);
+  k_ffn_dh_join<LAYOUT, ACT><<<dim3((a.I + 127) / 128, (a.T + kJoinRows - 1) / kJoinRows), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -264,11 +289,10 @@ struct BwdWs {
   BwdWs(const moe4_ffn& f, int64_t T) {
     h = align_up((size_t)T * 2 * f.I * 2, 256);
     part_gu = h + align_up((size_t)T * f.I * 2, 256);
-    part_dn = part_gu + align_up((size_t)((T + 127) / 128) * 2 * f.I * 4, 256);
-    // (where dH is split, the bias gradient of the first projection comes from dGU's columns too)
-    const int wide = 2 * f.I > f.H ? 2 * f.I : f.H;
-    dh = part_dn + align_up((size_t)kColParts * wide * 4, 256);
     dh_splits = T > 0 ? k_splits(tiles_of<Tile128>(f.I, T), f.H, 2) : 1;
+    const int64_t rows = dh_splits > 1 ? kJoinRows : Tile128::BB;
+    part_dn = part_gu + align_up((size_t)((T + rows - 1) / rows) * 2 * f.I * 4, 256);
+    dh = part_dn + align_up((size_t)kColParts * f.H * 4, 256);
     end = dh + (dh_splits > 1 ? align_up((size_t)dh_splits * T * f.I * 4, 256) : 0);
     const int64_t size[3][3] = {{f.H, T, 2 * (int64_t)f.I}, {f.H, 2 * (int64_t)f.I, T}, {f.I, f.H, T}};
     int64_t work = 0;   // k-tiles of 64
@@ -300,19 +324,15 @@ hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, cons
   if (dx || dw_gu || dw_dn || db_gu) {
     DhArgs a = {{f.w_dn, nullptr, I, I}, {dy, nullptr, H, T}, T, H, I,
                 {f.act, f.act_alpha, f.act_limit}, gu, dgu, dw_dn ? h : nullptr,
-                db_gu && at.dh_splits == 1 ? part_gu : nullptr, at.dh_splits,
-                reinterpret_cast<float*>(w8 + at.dh)};
+                db_gu ? part_gu : nullptr, at.dh_splits, reinterpret_cast<float*>(w8 + at.dh)};
     const bool big = at.dh_splits == 1 && large_tiles_for(I, T);
     e = with_kind(f.gu_layout, f.act, [&](auto l, auto c) {
       constexpr int L = decltype(l)::value, A = decltype(c)::value;
       return big ? launch_dh<Tile256, L, A>(a, s) : launch_dh<Tile128, L, A>(a, s);
     });
     if (e != hipSuccess) return e;
-    if (db_gu && at.dh_splits > 1) {
-      e = col_sums(dgu, T, 2 * I, part_dn, db_gu, dw_dtype, s);
-      if (e != hipSuccess) return e;
-    } else if (db_gu) {
-      const int rows = big ? Tile256::BB : Tile128::BB;
+    if (db_gu) {
+      const int rows = at.dh_splits > 1 ? kJoinRows : big ? Tile256::BB : Tile128::BB;
       e = launch_sum_rows(part_gu, (T + rows - 1) / rows, 2 * I, db_gu, dw_dtype, s);
       if (e != hipSuccess) return e;
     }

@@ -532,8 +532,9 @@ int moe4_ffn_forward(const moe4_ffn* f, const void* x, const uint8_t* x_s, int32
  *   dH = dY W_dn;  dGU = act'(gu) * dH;  dx = dGU W_gu (+ dx_add)
  *   dw_dn = dY^T h;  dw_gu = dGU^T x;  db_dn = sum_t dY;  db_gu = sum_t dGU
  * with h recomputed from save_gu. dGU and h are rounded once to bf16, the
- * operand type of the products that read them; every sum is fp32, in a fixed
- * order. Any output may be NULL and is then not computed.
+ * operand type of the products that read them; db_gu sums dGU before that
+ * rounding. Every sum is fp32, in a fixed order. Any output may be NULL and is
+ * then not computed.
  *   x bf16 [T, H] (needed for dw_gu); save_gu f32 [T, 2I]; dy bf16 [T, H]
  *   dx [T, H] of dx_dtype; dx_add [T, H] of add_dtype or NULL: a gradient of x
  *   from elsewhere (the routed experts'), added in fp32 (may be dx where the

@@ -1,13 +1,16 @@
 """The dense feed-forward block in every pairing of gate/up layout and activation, and the
-precision of its MXFP8 products for few tokens, against the float64 definitions in
-oracle/dense.py."""
+precision of its bias gradient and of the MXFP8 products for few tokens, against the float64
+definitions in oracle/dense.py."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from oracle import dense
-from gpu_helpers import to_dev
-from test_gpu_dense import BF, F32, U32, VARIANTS, Block, ffn_backward_check, ffn_check, out_t, rng, within
+from oracle import bf16_bits_from_f32, bf16_bits_to_f64, dense
+from gpu_helpers import say, to_dev
+from test_gpu_dense import (ALPHA, BF, F32, LIMIT, U32, UBF, VARIANTS, Block, draw, ffn_backward_check, ffn_check,
+                            out_t, rng, val, within)
 
 pytestmark = pytest.mark.gpu
 moe4 = pytest.importorskip("bit_mixture_experts_amd.moe4")
@@ -79,3 +82,67 @@ BWD = [(65, 264, 136), (300, 392, 200), (1, 1544, 72), (70, 1032, 136), (333, 20
 @pytest.mark.parametrize("T,H,I", BWD + [(4100, 1032, 2056)])
 def test_ffn_backward_forms(T, H, I, layout, act):
     ffn_backward_check(Form("form-bwd", H, I, layout, act, bias=True), T)
+
+
+def grad_terms(gv, dh, layout, act):
+    """(dGU, the size of its terms, what the activation's evaluation in fp32 may cost in units
+    of 2^-24 of that): each [T, 2I] in memory's order."""
+    g, u = dense._split(gv, layout)
+    if act == "swiglu":
+        a, lin, sat_g, sat_u = 1.0, u, np.zeros(g.shape, bool), np.zeros(g.shape, bool)
+    else:
+        a, lin = ALPHA, np.clip(u, -LIMIT, LIMIT) + 1
+        sat_g, sat_u = g > LIMIT, np.abs(u) > LIMIT
+        g = np.where(sat_g, LIMIT, g)
+    s = 1 / (1 + np.exp(-a * g))
+    dg, du = np.where(sat_g, 0.0, dh * lin * (s + a * g * s * (1 - s))), np.where(sat_u, 0.0, dh * g * s)
+    mg = np.where(sat_g, 0.0, np.abs(dh) * np.abs(lin) * (s + np.abs(a * g) * s * (1 - s)))
+    # the exponential's argument is off by three roundings of |a g|, which is its relative error;
+    # about eight more operations, and 1 - s, off by 3 * 2^-24 of s times |a g|
+    cost = 16 + 8 * np.abs(a * g)
+    return (dense._join(dg, du, layout), dense._join(mg, np.abs(du), layout), dense._join(cost, cost, layout))
+
+
+@pytest.mark.parametrize("layout,act", FORMS)
+@pytest.mark.parametrize("T,H,I", BWD)
+def test_ffn_bias_gradient_is_summed_in_fp32(T, H, I, layout, act):
+    """db_gu sums dGU before its rounding to bf16, whatever the number of tokens. One entry of dY
+    a token, so that dH is one exact product; then only the activation's own fp32 operations
+    and the T fp32 additions are left."""
+    blk = Form("form-db", H, I, layout, act, bias=True)
+    r = rng("onehot", T, H)
+    dyv = np.zeros((T, H))
+    dyv[np.arange(T), r.integers(0, H, T)] = bf16_bits_to_f64(bf16_bits_from_f32(r.standard_normal(T).astype(np.float32)))
+    x, _, xv = blk.tokens(T)
+    gv = dense.ffn_forward(xv, blk.wg, blk.wd, blk.layout, blk.act, blk.bg, blk.bd)["gu"].astype(np.float32)
+    dy = to_dev(bf16_bits_from_f32(dyv.astype(np.float32)))
+    alone, full = out_t((2 * I,), F32), out_t((2 * I,), F32)
+    moe4.moe4_ffn_backward(blk.ffn, x, to_dev(gv), dy, db_gu=alone.t, ws=blk.ws(T, True))
+    dx, dwg = torch.empty((T, H), dtype=BF, device="cuda"), torch.empty((2 * I, H), dtype=F32, device="cuda")
+    dwd = torch.empty((H, I), dtype=F32, device="cuda")
+    moe4.moe4_ffn_backward(blk.ffn, x, to_dev(gv), dy, dx=dx, dw_gu=dwg, dw_dn=dwd, db_gu=full.t, ws=blk.ws(T, True))
+    alone.check("db_gu"), full.check("db_gu")
+    assert torch.equal(alone.t, full.t)
+    dgu, mag, cost = grad_terms(gv.astype(np.float64), dyv @ blk.wd, layout, act)
+    tol = U32 * ((cost + T + 4) * mag).sum(0) + 1e-37
+    within(full.t.double().cpu().numpy(), dgu.sum(0), tol, "db_gu")
+
+
+@pytest.mark.parametrize("layout,act", FORMS)
+@pytest.mark.parametrize("T,H,I", BWD[:4])
+def test_ffn_bias_gradient_of_ordinary_gradients(T, H, I, layout, act):
+    # the 2-norm over the output: 1e-5 for the fp32 sums of dH, T more fp32 additions
+    blk = Form("form-db2", H, I, layout, act, bias=True)
+    x, _, xv = blk.tokens(T)
+    dy, dyv = draw(rng("dy-db", T, H), (T, H), std=0.1)
+    gv = dense.ffn_forward(xv, blk.wg, blk.wd, blk.layout, blk.act, blk.bg, blk.bd)["gu"].astype(np.float32)
+    w = dense.ffn_backward(xv, gv.astype(np.float64), dyv, blk.wg, blk.wd, layout, act, ALPHA, LIMIT)
+    for dt in (F32, BF):
+        db = out_t((2 * I,), dt)
+        moe4.moe4_ffn_backward(blk.ffn, x, to_dev(gv), dy, db_gu=db.t, ws=blk.ws(T, True))
+        db.check("db_gu")
+        d = np.linalg.norm(val(db.t) - w["db_gu"])
+        tol = ((UBF if dt == BF else U32) + 1e-5) * np.linalg.norm(w["db_gu"]) + \
+            np.linalg.norm(T * U32 * np.abs(w["dgu"]).sum(0))
+        say(f"  db_gu: {d:.3e} of {tol:.3e}")
+        assert d <= tol and math.isfinite(d)
