@@ -225,11 +225,28 @@ inline hipError_t allow_lds(K* kernel, int bytes) {
 // and its reads cost about as much as eight: 1024 tokens at H = I = 512 19 us whole and 25 in
 // parts of four). Us whole and in parts: 128 tokens at H 4096, I 8192 174 and 81, at 2880,
 // 2880 65 and 40; 512 tokens at 4096, 8192 184 and 142.
+constexpr int kMostSplits = 16;
 inline int k_splits(int64_t n128, int K, int es) {
   const int nk = (int)(((int64_t)K * es + 127) / 128);
   const int64_t most = 512 / n128, long_enough = nk / 8;
   const int64_t s = most < long_enough ? most : long_enough;
-  return s < 2 ? 1 : (int)(s < 16 ? s : 16);
+  return s < 2 ? 1 : (int)(s < kMostSplits ? s : kMostSplits);
+}
+
+// Bytes that the parts of a product [nb, na] cut into at most `splits` take, for this nb or any
+// smaller one: parts x tiles are at most 512, and a tile holds 64 KiB. Workspaces are sized by
+// this, not by the call's own parts, which become fewer as nb grows: a buffer made for the most
+// tokens serves any fewer.
+constexpr int64_t kMostPartBytes = 512 * 128 * 128 * 4;
+inline int64_t part_bytes(int64_t na, int64_t nb, int64_t splits) {
+  const int64_t b = splits < 2 ? 0 : splits * na * nb * 4;
+  return b < kMostPartBytes ? b : kMostPartBytes;
+}
+// the most parts that k_splits makes of a product with na columns and a reduction of K
+inline int64_t most_k_splits(int64_t na, int K, int es) {
+  if ((na + 127) / 128 > 256) return 1;
+  const int64_t s = ((int64_t)K * es + 127) / 128 / 8;
+  return s < kMostSplits ? s : kMostSplits;
 }
 
 // The sums of split products (those of up to three, one after another), with what their tiles'

@@ -254,6 +254,7 @@ __global__ __launch_bounds__(256) void k_col_sums(const uint16_t* m, int T, int 
   }
 }
 
+constexpr int kMostGradSplits = 32;
 constexpr int kColParts = 128;
 int col_parts(int T) { return T < kColParts ? (T > 0 ? T : 1) : kColParts; }
 
@@ -282,7 +283,8 @@ hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
 // workspace: dGU, h, the partial sums of the two biases' gradients, of dH where it is split along
 // k, and of the products after it: one whose reduction is several times a workgroup's share of
 // all their k-tiles (few tokens: dX; a small block and many tokens: the weights' gradients)
-// would still run when the others have ended
+// would still run when the others have ended. Every region's size is one that does not fall as T
+// grows (part_bytes), whatever this T is split into.
 struct BwdWs {
   size_t h, part_gu, part_dn, dh, part[3], end;
   int dh_splits, splits[3];   // dX, dW_gu, dW_dn
@@ -290,20 +292,29 @@ struct BwdWs {
     h = align_up((size_t)T * 2 * f.I * 2, 256);
     part_gu = h + align_up((size_t)T * f.I * 2, 256);
     dh_splits = T > 0 ? k_splits(tiles_of<Tile128>(f.I, T), f.H, 2) : 1;
-    const int64_t rows = dh_splits > 1 ? kJoinRows : Tile128::BB;
-    part_dn = part_gu + align_up((size_t)((T + rows - 1) / rows) * 2 * f.I * 4, 256);
+    // dH whole leaves a row of bias sums per row tile, the join one per kJoinRows tokens of the
+    // at most 256 tiles that are split
+    const int64_t most_dh = most_k_splits(f.I, f.H, 2), whole = (T + Tile128::BB - 1) / Tile128::BB;
+    int64_t joined = most_dh > 1 ? 256 / ((f.I + 127) / 128) * (Tile128::BB / kJoinRows) : 0;
+    if (joined > (T + kJoinRows - 1) / kJoinRows) joined = (T + kJoinRows - 1) / kJoinRows;
+    part_dn = part_gu + align_up((size_t)(joined > whole ? joined : whole) * 2 * f.I * 4, 256);
     dh = part_dn + align_up((size_t)kColParts * f.H * 4, 256);
-    end = dh + (dh_splits > 1 ? align_up((size_t)dh_splits * T * f.I * 4, 256) : 0);
+    end = dh + align_up((size_t)part_bytes(f.I, T, most_dh), 256);
     const int64_t size[3][3] = {{f.H, T, 2 * (int64_t)f.I}, {f.H, 2 * (int64_t)f.I, T}, {f.I, f.H, T}};
     int64_t work = 0;   // k-tiles of 64
     for (const auto& z : size) work += tiles_of<Tile128>(z[0], z[1]) * ((z[2] + 63) / 64);
     const int64_t share = (work + 511) / 512 > 8 ? (work + 511) / 512 : 8;
+    // parts x tiles of the three together: at most work / share, so at most 512
+    size_t at = end, most = 0;
     for (int i = 0; i < 3; ++i) {
-      const int64_t s = (size[i][2] + 63) / 64 / share;
-      splits[i] = s < 2 ? 1 : (int)(s < 32 ? s : 32);
-      part[i] = end;
-      if (splits[i] > 1) end += align_up((size_t)splits[i] * size[i][0] * size[i][1] * 4, 256);
+      const int64_t nk = (size[i][2] + 63) / 64, s = nk / share, ms = nk / 8;
+      splits[i] = s < 2 ? 1 : (int)(s < kMostGradSplits ? s : kMostGradSplits);
+      part[i] = at;
+      if (splits[i] > 1) at += align_up((size_t)splits[i] * size[i][0] * size[i][1] * 4, 256);
+      most += align_up((size_t)part_bytes(size[i][0], size[i][1], ms < kMostGradSplits ? ms : kMostGradSplits), 256);
     }
+    const size_t all = (size_t)kMostPartBytes + 3 * 256;
+    end += most < all ? most : all;
   }
 };
 

@@ -532,7 +532,7 @@ hipError_t launch_join(JoinArgs a, int n, hipStream_t s) {
 namespace {
 
 // workspace: h (and its scales), the partial sums of a product that is split along k (the two
-// products' follow each other in time and share the place)
+// products' follow each other in time and share the place). It does not fall as T grows.
 struct FwdWs {
   int gate_splits, down_splits;
   size_t scales, part, end;
@@ -544,9 +544,9 @@ struct FwdWs {
     down_splits = T > 0 ? k_splits(tiles_of<Tile128>(f.H, T), f.I, es) : 1;
     scales = align_up((size_t)T * f.I * es, 256);
     part = scales + (mx ? align_up((size_t)T * (f.I / 32), 256) : 0);
-    const size_t g = gate_splits > 1 ? (size_t)gate_splits * T * 2 * f.I * 4 : 0;
-    const size_t d = down_splits > 1 ? (size_t)down_splits * T * f.H * 4 : 0;
-    end = part + align_up(g > d ? g : d, 256);
+    const int64_t g = part_bytes(2 * (int64_t)f.I, T, most_k_splits(2 * (int64_t)f.I, f.H, es));
+    const int64_t d = part_bytes(f.H, T, most_k_splits(f.H, f.I, es));
+    end = part + align_up((size_t)(g > d ? g : d), 256);
   }
 };
 

@@ -550,7 +550,8 @@ int moe4_ffn_backward(const moe4_ffn* f, const uint16_t* x, int32_t T, const flo
                       int32_t dw_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of moe4_ffn_forward (backward == 0) or moe4_ffn_backward at T
- * tokens; 0 if the descriptor or T is invalid. */
+ * tokens; 0 if the descriptor or T is invalid. Never less than for fewer
+ * tokens, so a buffer for the largest batch serves every smaller one. */
 size_t moe4_ffn_workspace_size(const moe4_ffn* f, int32_t T, int32_t backward);
 
 /*
