@@ -372,9 +372,10 @@ __global__ __launch_bounds__(256) void k_quantize_mxfp8(const void* v, int64_t n
 
 // Waves of a row: each lane holds at most 32 columns (the registers of the operands of one
 // row, at four waves a SIMD), and a row of few goes over four waves.
+constexpr int64_t kManyRows = 2048;
 int norm_waves(int64_t T, int H) {
   if (H > 8192) return 16;
-  if (H > 4096 || (T < 2048 && H > 512)) return 4;
+  if (H > 4096 || (T < kManyRows && H > 512)) return 4;
   return H > 2048 ? 2 : 1;
 }
 // workgroups: enough waves for every CU's latency to be covered, each with several rows
@@ -446,8 +447,13 @@ hipError_t launch_add_rmsnorm(const void* x, int x_dtype, const void* res, int r
   });
 }
 
+// For this T or any smaller one: from kManyRows on a row of 512 < H <= 2048 goes to one wave,
+// and four rows to a workgroup, so fewer workgroups leave sums than just below it.
 size_t add_rmsnorm_ws_bytes(int64_t T, int H) {
-  return (size_t)norm_bwd_blocks(T, norm_waves(T, H)) * H * 4;
+  const int own = norm_bwd_blocks(T, norm_waves(T, H));
+  const int64_t few = T < kManyRows ? T : kManyRows - 1;
+  const int below = norm_bwd_blocks(few, norm_waves(few, H));
+  return (size_t)(own > below ? own : below) * H * 4;
 }
 
 hipError_t launch_add_rmsnorm_backward(const void* dy, int dy_dtype, const void* sv, int s_dtype,

@@ -459,7 +459,7 @@ int moe4_add_rmsnorm_backward(const void* dy, int32_t dy_dtype, const void* s, i
                               const void* weight, int32_t w_dtype, const float* rstd,
                               const void* dres, int32_t T, int32_t H, void* dx, int32_t dx_dtype,
                               float* dweight, void* ws, size_t ws_bytes, void* stream);
-/* 0 if T or H is invalid */
+/* 0 if T or H is invalid; never less than for fewer rows */
 size_t moe4_add_rmsnorm_workspace_size(int32_t T, int32_t H);
 
 /*

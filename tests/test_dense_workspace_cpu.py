@@ -48,6 +48,15 @@ def test_block_sizes_are_not_extravagant(H, I):
         assert bwd <= T * I * 6 + sums + (64 << 20) + 8192
 
 
+@pytest.mark.parametrize("H", [8, 512, 520, 1024, 2048, 2056, 2880, 4096, 4104, 8192, 16384])
+def test_norm_sizes_never_fall(H):
+    last = 0
+    for T in _sizes_of_t() + [1 << 17, 1 << 20, 1 << 30]:
+        n = lib.moe4_add_rmsnorm_workspace_size(T, H)
+        assert n >= last and n > 0, (T, n, last)
+        last = n
+
+
 def test_grad_sizes_never_fall():
     last = 0
     for n in list(range(0, 1000)) + [1 << k for k in range(10, 21)]:

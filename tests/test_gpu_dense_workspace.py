@@ -55,3 +55,23 @@ def test_block_with_the_largest_batchs_workspace(H, I, mx):
         for k in grads[0]:
             assert torch.equal(grads[0][k], grads[1][k]), (T, k)
             assert bool(torch.isfinite(grads[0][k]).all()), (T, k)
+
+
+@pytest.mark.parametrize("H", [520, 2048, 2056])
+def test_norm_backward_with_the_largest_batchs_workspace(H):
+    big = 4100
+    shared = Scratch(moe4.moe4_add_rmsnorm_workspace_size(big, H))
+    r = rng("ws-norm", H)
+    dy, _ = draw(r, (big, H), std=0.1)
+    s, sv = draw(r, (big, H))
+    w, _ = draw(r, (H,))
+    rstd = torch.from_numpy((1 / np.sqrt(np.mean(sv * sv, 1))).astype(np.float32)).cuda()
+    for T in (big, 2048, 2047, 1025, 3, 1):
+        outs = []
+        for sc in (shared, Scratch(moe4.moe4_add_rmsnorm_workspace_size(T, H))):
+            dx, dw = torch.empty((T, H), dtype=BF, device="cuda"), torch.full((H,), float("nan"), device="cuda")
+            moe4.moe4_add_rmsnorm_backward(dy[:T], s[:T], w, rstd[:T], dx, dweight=dw, ws=sc.ws)
+            sc.check()
+            outs.append((dx, dw))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        assert bool(torch.isfinite(outs[0][1]).all())
