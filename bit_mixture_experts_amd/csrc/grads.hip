@@ -9,7 +9,7 @@
 // Bound by HBM. 88 million fp32 values in 48 tensors (352 MB): squares 81-92 us, 4.1 TB/s; scaling
 // to another place 108-115 us, 6.3 TB/s, part of its reads from the caches. Fp64 partial sums, at most
 // 2048 a launch (1024 left CUs idle between chunks: 88 us; chunks of half the size 86), are added
-// up by every scaling workgroup for itself, which saves a launch.
+// up by every scaling workgroup for itself, which saves a launch while they are few.
 #include "internal.hpp"
 #include "common.hpp"
 
@@ -17,6 +17,12 @@ namespace moe4 {
 namespace {
 
 constexpr int kGradBatch = 128, kGradChunk = 8192, kGradParts = 2048;
+// The most partial sums that every scaling workgroup adds up for itself; more of them are joined by
+// a launch first, since their number grows with the list and so does that of the workgroups. Us
+// by themselves and joined: 2 tensors, 10 sums 6.5 and 8.1; 64, 1024 sums 21.9 and 23.7; 257, 4112
+// sums 83.4 and 83.3; 512, 8192 sums 190 and 182; 6144, 12288 sums 700 and 640; 32768 tensors of
+// 20 elements 2954 and 2068.
+constexpr int kScaleParts = kGradParts;
 
 struct GradBatch {
   const void* in[kGradBatch];
@@ -92,17 +98,24 @@ __global__ __launch_bounds__(256) void k_grad_squares(const GradBatch b, double*
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// the norm from the partial sums, in the same order in every workgroup
-__device__ __forceinline__ float total_norm(const double* part, int nparts, double* red) {
+// the sum of the squares from the partial sums, in the same order wherever it is taken
+__device__ __forceinline__ double total_squares(const double* part, int nparts, double* red) {
   double s = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < nparts; i += 256) s += part[i];
-  return (float)sqrt(block_sum(s, red));
+  return block_sum(s, red);
 }
 
 __global__ __launch_bounds__(256) void k_grad_norm(const double* part, int nparts, float* norm) {
   __shared__ double red[4];
-  const float v = total_norm(part, nparts, red);
-  if (threadIdx.x == 0) norm[0] = v;
+  const double s = total_squares(part, nparts, red);
+  if (threadIdx.x == 0) norm[0] = (float)sqrt(s);
+}
+
+__global__ __launch_bounds__(256) void k_grad_join(const double* part, int nparts, double* total) {
+  __shared__ double red[4];
+  const double s = total_squares(part, nparts, red);
+  if (threadIdx.x == 0) total[0] = s;
 }
 
 // out = g * min(1, max_norm / (norm + 1e-6)), rounded once to the gradient's type. A norm that
@@ -111,7 +124,7 @@ __global__ __launch_bounds__(256) void k_grad_scale(const GradBatch b, const dou
                                                     int nparts, const float* norm_in,
                                                     float max_norm, float* norm_out) {
   __shared__ double red[4];
-  const float norm = norm_in ? norm_in[0] : total_norm(part, nparts, red);
+  const float norm = norm_in ? norm_in[0] : (float)sqrt(total_squares(part, nparts, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) norm_out[0] = norm;
   const double k = (double)max_norm / ((double)norm + 1e-6);
   const float coef = k < 1.0 && __builtin_isfinite(norm) ? (float)k : 1.0f;
@@ -202,10 +215,16 @@ hipError_t launch_clip_grads(const void* const* in, void* const* out, const int6
   if (!norm_in) {
     e = squares(in, numel, dtype, n, part, &parts, s);
     if (e != hipSuccess) return e;
+    if (parts > kScaleParts) {
+      k_grad_join<<<1, 256, 0, s>>>(part, parts, part + parts);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      part += parts;
+      parts = 1;
+    }
   }
   bool first = true;
   e = each_batch(in, out, numel, dtype, n, [&](const GradBatch& b, int blocks) {
-    // the scaling workgroups start with the partial sums: fewer, longer ones
     k_grad_scale<<<blocks, 256, 0, s>>>(b, part, parts, norm_in, max_norm,
                                         first ? norm_out : nullptr);
     first = false;
