@@ -127,28 +127,32 @@ __global__ __launch_bounds__(256) void k_grad_scale(const GradBatch b, const dou
   const float norm = norm_in ? norm_in[0] : (float)sqrt(total_squares(part, nparts, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) norm_out[0] = norm;
   const double k = (double)max_norm / ((double)norm + 1e-6);
-  const float coef = k < 1.0 && __builtin_isfinite(norm) ? (float)k : 1.0f;
+  const bool clip = k < 1.0 && __builtin_isfinite(norm);
+  // a factor below fp32's normal range would hold few bits: it goes in two, the second exact
+  const bool tiny = clip && k < 0x1p-126;
+  const float coef = clip ? (float)(tiny ? k * 0x1p126 : k) : 1.0f, down = tiny ? 0x1p-126f : 1.0f;
+  auto scaled = [&](float g) { return g * coef * down; };
   // back to front: what the norm's pass read last is still in the caches
   for (int c = b.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int t = __builtin_amdgcn_readfirstlane(tensor_of(b, c));
-    if (coef == 1.0f && b.in[t] == b.out[t]) continue;
+    if (!clip && b.in[t] == b.out[t]) continue;
     const int64_t at = (int64_t)(c - b.first[t]) * kGradChunk, n = b.numel[t] - at;
     if (b.f32[t]) {
       const float* p = static_cast<const float*>(b.in[t]) + at;
       float* o = static_cast<float*>(b.out[t]) + at;
       walk<float, 4>(p, n, [&](int i, u32x4 v) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * coef);
+        for (int q = 0; q < 4; ++q) v[q] = __float_as_uint(scaled(__uint_as_float(v[q])));
         reinterpret_cast<u32x4*>(o)[i] = v;
-      }, [&](int i) { o[i] = p[i] * coef; });
+      }, [&](int i) { o[i] = scaled(p[i]); });
     } else {
       const uint16_t* p = static_cast<const uint16_t*>(b.in[t]) + at;
       uint16_t* o = static_cast<uint16_t*>(b.out[t]) + at;
       walk<uint16_t, 8>(p, n, [&](int i, u32x4 v) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(bf16lo(v[q]) * coef, bf16hi(v[q]) * coef);
+        for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(scaled(bf16lo(v[q])), scaled(bf16hi(v[q])));
         reinterpret_cast<u32x4*>(o)[i] = v;
-      }, [&](int i) { o[i] = f32_to_bf16(bf16_to_f32(p[i]) * coef); });
+      }, [&](int i) { o[i] = f32_to_bf16(scaled(bf16_to_f32(p[i]))); });
     }
   }
 }

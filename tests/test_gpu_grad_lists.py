@@ -75,3 +75,19 @@ def test_clip_costs_as_much_as_its_norm_and_its_scaling():
     w, p = best(whole), best(parts)
     say(f"  {n} tensors: {w:.2f} ms in one call, {p:.2f} ms in two")
     assert w <= 2 * p
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("max_norm", [1e-3, 1e-6, 3.0])
+def test_clip_factors_below_fp32s_normal_range(dtype, max_norm):
+    # max_norm / norm is a subnormal in fp32, with few bits of it left; the product is none
+    r = rng("factor")
+    t = torch.from_numpy((r.uniform(0.5, 1.0, 999) * 1e36).astype(np.float32)).cuda().to(dtype)
+    v = val(t)
+    o = Guarded((999,), dtype)
+    gl = moe4.GradList([t], [o.t])
+    norm = torch.empty(1, device="cuda")
+    moe4.moe4_clip_grads(gl, max_norm, norm, workspace(gl))
+    k = dense.clip_factor(dense.grad_norm([v]), float(np.float32(max_norm)))
+    within(val(o.t), v * k, (ueps(dtype) + 4 * U32) * np.abs(v) * k, "clipped")
+    o.check("clipped")
