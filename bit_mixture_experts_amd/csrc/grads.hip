@@ -2,9 +2,9 @@
 //
 // The list travels in the kernels' arguments, kGradBatch tensors to a launch, so nothing is
 // copied to the device and a captured graph holds the list by value. Work is dealt in chunks
-// of kGradChunk elements of one tensor. Squares are summed in fp64: the norm is right to fp32
-// for any finite gradients (an fp32 square overflows from 1.9e19 on and vanishes below
-// 1e-23), and the fp64 adds hide behind the loads.
+// of kGradChunk elements of one tensor. Squares are summed in fp64 (an fp32 square overflows from
+// 1.9e19 on and vanishes below 1e-23): the norm is right to fp32 for any finite gradients, an
+// infinity where it passes fp32's range, and the fp64 adds hide behind the loads.
 //
 // Bound by HBM. 88 million fp32 values in 48 tensors (352 MB): squares 81-92 us, 4.1 TB/s; scaling
 // to another place 108-115 us, 6.3 TB/s, part of its reads from the caches. Fp64 partial sums, at most
@@ -118,15 +118,17 @@ __global__ __launch_bounds__(256) void k_grad_join(const double* part, int npart
   if (threadIdx.x == 0) total[0] = s;
 }
 
-// out = g * min(1, max_norm / (norm + 1e-6)), rounded once to the gradient's type. A norm that
+// out = g * min(1, max_norm / (norm + 1e-6)), rounded once to the gradient's type. The norm is the
+// fp32 one that is written, or, where finite gradients pass fp32's range, the fp64 one. A norm that
 // is no finite number leaves the gradients as they are: the caller reads it and drops the step.
 __global__ __launch_bounds__(256) void k_grad_scale(const GradBatch b, const double* part,
                                                     int nparts, const float* norm_in,
                                                     float max_norm, float* norm_out) {
   __shared__ double red[4];
-  const float norm = norm_in ? norm_in[0] : (float)sqrt(total_squares(part, nparts, red));
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) norm_out[0] = norm;
-  const double k = (double)max_norm / ((double)norm + 1e-6);
+  const double exact = norm_in ? (double)norm_in[0] : sqrt(total_squares(part, nparts, red));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) norm_out[0] = (float)exact;
+  const double norm = __builtin_isfinite((float)exact) ? (double)(float)exact : exact;
+  const double k = (double)max_norm / (norm + 1e-6);
   const bool clip = k < 1.0 && __builtin_isfinite(norm);
   // a factor below fp32's normal range would hold few bits: it goes in two, the second exact
   const bool tiny = clip && k < 0x1p-126;

@@ -557,7 +557,8 @@ size_t moe4_ffn_workspace_size(const moe4_ffn* f, int32_t T, int32_t backward);
 /*
  * Global norm of a list of gradients: norm[0] = sqrt(sum_i sum_e g_i[e]^2) as
  * fp32, the squares summed in fp64 in a fixed order (right for any finite
- * gradients, however large or small).
+ * gradients, however small or large; an infinity where the norm itself passes
+ * fp32's range).
  *   grads, numel, dtype: host arrays of n entries, read during the call:
  *   device pointers (16-byte aligned; NULL where numel is 0), elements (0 <=
  *   numel <= 2^36), MOE4_DTYPE_*; 0 <= n <= 2^20
@@ -569,9 +570,10 @@ int moe4_grad_norm(const void* const* grads, const int64_t* numel, const int32_t
 
 /*
  * Clipping by the global norm: outs[i] = grads[i] * min(1, max_norm / (norm +
- * 1e-6)), rounded once to the gradient's type. Where the norm is an infinity
- * or a NaN the gradients pass unchanged: the caller reads the norm and drops
- * the step.
+ * 1e-6)), rounded once to the gradient's type. Where a gradient holds an
+ * infinity or a NaN, or norm_in is one, the gradients pass unchanged: the caller
+ * reads the norm and drops the step. Finite gradients whose norm passes fp32's
+ * range are clipped by the fp64 norm (norm_out is then an infinity).
  *   grads, numel, dtype, n, ws as moe4_grad_norm
  *   outs: host array of n device pointers (16-byte aligned; outs[i] may be
  *   grads[i], and overlaps nothing else of the list), or NULL for all in place

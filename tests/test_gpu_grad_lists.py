@@ -77,6 +77,27 @@ def test_clip_costs_as_much_as_its_norm_and_its_scaling():
     assert w <= 2 * p
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_clip_finite_gradients_past_fp32s_norm(dtype, in_place):
+    # the norm of these is 1000^1/2 * 3e38: no fp32 value, but the gradients are finite
+    t = torch.full((1000,), 3e38, device="cuda").to(dtype)
+    t[::2] *= -1
+    v = val(t)
+    o = None if in_place else Guarded((1000,), dtype)
+    gl = moe4.GradList([t], None if in_place else [o.t])
+    norm = torch.empty(1, device="cuda")
+    moe4.moe4_clip_grads(gl, 2.0, norm, workspace(gl))
+    assert math.isinf(norm.item())
+    k = dense.clip_factor(dense.grad_norm([v]), 2.0)
+    assert 0 < k < 1e-38
+    within(val(t if in_place else o.t), v * k, (ueps(dtype) + 4 * U32) * np.abs(v) * k, "clipped")
+    # an infinite norm from elsewhere says nothing of the gradients' size: unchanged
+    t2 = torch.ones(100, device="cuda")
+    moe4.moe4_clip_grads(moe4.GradList([t2]), 0.5, norm_in=norm)
+    assert bool((t2 == 1).all())
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("max_norm", [1e-3, 1e-6, 3.0])
 def test_clip_factors_below_fp32s_normal_range(dtype, max_norm):
