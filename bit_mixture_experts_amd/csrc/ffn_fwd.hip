@@ -557,13 +557,18 @@ size_t ffn_forward_ws_bytes(const moe4_ffn& f, int64_t T) { return FwdWs(f, T).e
 int ffn_variant(const moe4_ffn& f, int64_t T) {
   if (f.variant != MOE4_VARIANT_AUTO) return f.variant;
   // The skinny kernels read the weights once for every 64 tokens (MXFP8: 32), mostly from the
-  // caches, the tiled ones pay two or three launches of long tiles. Us, skinny and tiled: 128
-  // tokens at H 2048, I 768 (18.9 MB read) 19 and 26; 256 33 and 28; 256 at 512, 512 (6.3 MB) 11
-  // and 18, 1024 (25 MB) 24 and 19; 128 at 2880, 2880 (100 MB) 70 and 40.
+  // caches, the tiled ones pay two or three launches of long tiles. Us, skinny and tiled, in
+  // bf16: 128 tokens at H 2048, I 768 (18.9 MB read) 18 and 24, 256 32 and 26; 256 at 512, 512 (6.3
+  // MB) 10 and 17, 1024 (25 MB) 24 and 18; 128 at 2880, 2880 (100 MB) 70 and 36. MXFP8: 32 at 2880,
+  // 2880 18 and 25, 64 (50 MB) 27 and 28, 128 44 and 34; 128 at 1024, 1024 (12.6 MB) 13 and 18,
+  // 512 (50 MB) 31 and 19; 32 at H 4096, I 8192 40 and 36. Small weights and many tokens are
+  // bound by the workgroups' number instead: at 64, 64 4096 tokens 9.0 and 10.2 (MXFP8 11.3 and
+  // 11.5), 16384 25 and 11 (37 and 12).
   const bool mx = f.format == MOE4_FFN_MXFP8;
   const int64_t weights = 3 * (int64_t)f.H * f.I * (mx ? 1 : 2), at_once = mx ? 32 : 64;
-  return T <= 32 || (T + at_once - 1) / at_once * weights <= 20 << 20 ? MOE4_VARIANT_SKINNY
-                                                                      : MOE4_VARIANT_TILED;
+  return T <= 32 || (T <= 4096 && (T + at_once - 1) / at_once * weights <= 20 << 20)
+             ? MOE4_VARIANT_SKINNY
+             : MOE4_VARIANT_TILED;
 }
 
 hipError_t launch_ffn_forward(const moe4_ffn& f, const void* x, const uint8_t* x_s, int T,

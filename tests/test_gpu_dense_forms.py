@@ -72,6 +72,15 @@ def test_ffn_mx_few_tokens_multiply_exactly():
     within(gu.t.double().cpu().numpy(), xv @ wv.T, (H + 2) * U32 * (np.abs(xv) @ np.abs(wv).T), "gu")
 
 
+@pytest.mark.parametrize("mx", [False, True])
+def test_ffn_small_block_many_tokens_runs_tiled(mx):
+    # a small block's weights are read again for every few tokens: with many tokens the tiles win
+    blk = Form("small", 64, 64, "halves", "swiglu", mx, True)
+    for T, family in ((64, moe4.MOE4_VARIANT_SKINNY), (16384, moe4.MOE4_VARIANT_TILED)):
+        ffn_check(blk, T, VARIANTS["auto"], BF, BF, True)
+        assert moe4.moe4_last_variant() == family
+
+
 # ----------------------------------------------------------------- backward
 
 # dH whole in small tiles; cut along k and joined; dH and the other products in the largest tiles
