@@ -198,9 +198,12 @@ inline hipError_t with_kind(int layout, int act, F f) {
 // Which tiles, by rounds of the chip: a round is 256 tiles of 256 x 256 or 512 of 128 x 128,
 // and one of the small tiles takes two thirds of one of the large (half the work, at three
 // quarters of the rate: each LDS operand feeds half as many MFMAs). Few tokens or a ragged last
-// round go to the small ones. Both sides, large and small tiles, in us: 512 tokens at H 4096, I
-// 8192 271 and 184; 2048 at 2880, 2880 136 and 129; 4096 at 2048, 768 73 and 55; 8192 in
-// MXFP8 at 2880, 2880 283 and 350.
+// round go to the small ones. Us of a forward, large and small tiles throughout (few tokens cut
+// along k): bf16 1024 tokens at 2880, 2880 92 and 74, 2048 121 and 118 (each product by the rule
+// 109), 8192 363 and 402; 4096 at 2048, 768 67 and 53, 8192 81 and 96; 1024 at 4096, 8192 194 and
+// 221, 4096 640 and 808. MXFP8 1024 at 2880, 2880 72 and 65, 2048 87 and 91 (by the rule 80),
+// 4096 135 and 165; 4096 at 2048, 768 44 and 39, 8192 56 and 65; 1024 at 4096, 8192 134 and 166,
+// 2048 230 and 303 (by the rule 248: the one size tried where it loses).
 template <typename S>
 inline int64_t tiles_of(int64_t na, int64_t nb) {
   return ((na + S::BA - 1) / S::BA) * ((nb + S::BB - 1) / S::BB);
