@@ -417,6 +417,9 @@ int moe4_expert_backward(const moe4_experts* ex, const uint16_t* x_perm, const i
  * passes (a shared expert), the 8-bit form of both, and the clipping of the
  * adapters' gradients. Activations are bf16; a tensor whose type is an
  * argument is bf16 or fp32 (MOE4_DTYPE_*, no default). Sizes are in elements.
+ * An output shares memory with an input only where this says it may, and with
+ * no other output or workspace; calls that run at once have workspaces of their
+ * own.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -428,7 +431,7 @@ int moe4_expert_backward(const moe4_experts* ex, const uint16_t* x_perm, const i
  * next layer and for the backward pass. y is written as bf16 (out), as MXFP8
  * (out_q and out_s, see moe4_quantize_mxfp8, each value rounded once from
  * fp32), or both. Squares are summed in fp32: a row whose sum of squares
- * passes fp32's range gives rstd 0.
+ * passes fp32's range gives rstd 0, and values below 1e-23 count as zeros.
  *   x [T, H] of x_dtype; residual [T, H] of res_dtype or NULL; weight [H] of
  *   w_dtype; eps >= 0; 8 <= H <= 16384, a multiple of 8 (32 with out_q)
  *   sum_out [T, H] of res_dtype or NULL (needs residual; may be the residual
