@@ -224,10 +224,13 @@ inline hipError_t allow_lds(K* kernel, int bytes) {
 }
 
 // Parts of k for n tiles of 128 x 128 that leave most of a round (512) empty: as many as fill it,
-// each with at least eight k-tiles of 128 bytes (a part's own first loads, the launch that joins
-// and its reads cost about as much as eight: 1024 tokens at H = I = 512 19 us whole and 25 in
-// parts of four). Us whole and in parts: 128 tokens at H 4096, I 8192 174 and 81, at 2880,
-// 2880 65 and 40; 512 tokens at 4096, 8192 184 and 142.
+// each with at least eight k-tiles of 128 bytes (in bf16 a part's own first loads, the launch that
+// joins and its reads cost about as much as eight). Us of a forward, whole and in parts, bf16: 64
+// tokens at H 4096, I 8192 126 and 55, at 2880, 2880 60 and 32; 128 at 2880, 2880 65 and 36, at 2048,
+// 768 29 and 25; 512 147 and 115, 66 and 58, 37 and 33; 1024 at 2048, 768 38 and 36, 2048 39 and 42.
+// MXFP8, whose k-tiles multiply in half the time while the join costs the same: 64 61 and 40, 35 and
+// 29; 128 at 2880, 2880 41 and 34; but 512 95 and 92, 44 and 50, 21 and 24, and 2048 at 2048, 768
+// 25 and 34: parts are too short there.
 constexpr int kMostSplits = 16;
 inline int k_splits(int64_t n128, int K, int es) {
   const int nk = (int)(((int64_t)K * es + 127) / 128);

@@ -4,7 +4,7 @@
 // The first product's epilogue applies the activation's derivative to its fp32 accumulators
 // and writes dGU and the recomputed h in bf16, the operand type of the products that follow.
 //
-// 8192 tokens at H = I = 2880 with biases: 820-845 us, 0.98 PFLOP/s. dH 214 us: its epilogue reads
+// 8192 tokens at H = I = 2880 with biases: 820-855 us, 0.97 PFLOP/s. dH 214 us: its epilogue reads
 // 189 MB of pre-activations and writes 141 MB while the matrix cores stand (37% of a tile's
 // time; small tiles, two workgroups to a CU, overlap it but multiply more slowly: 202 to 218
 // us), and 384 tiles are one and a half rounds. The other products 607 us, 1.12 PFLOP/s. The
