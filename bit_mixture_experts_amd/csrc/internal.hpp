@@ -111,6 +111,12 @@ hipError_t launch_expert_backward(const moe4_experts& ex, const uint16_t* x_perm
 // ---- the dense half of the block
 // out[c] (of dtype) = sum over the P rows of part [P, N]
 hipError_t launch_sum_rows(const float* part, int P, int N, void* out, int dtype, hipStream_t s);
+// the same with rows ld apart
+hipError_t launch_sum_rows_of(const float* part, int P, int ld, int N, void* out, int dtype,
+                              hipStream_t s);
+// the same with the columns from `cut` on in another output
+hipError_t launch_sum_rows2(const float* part, int P, int N, void* out, int dtype, int cut,
+                            void* out2, hipStream_t s);
 hipError_t launch_add_rmsnorm(const void* x, int x_dtype, const void* res, int res_dtype, void* sum,
                               const void* w, int w_dtype, int T, int H, float eps, uint16_t* out,
                               uint8_t* q, uint8_t* qs, float* rstd, hipStream_t s);
@@ -139,6 +145,24 @@ hipError_t launch_grad_norm(const void* const* in, const int64_t* numel, const i
 hipError_t launch_clip_grads(const void* const* in, void* const* out, const int64_t* numel,
                              const int32_t* dtype, int n, float max_norm, const float* norm_in,
                              float* norm_out, void* ws, hipStream_t s);
+
+
+// ---- a block held in 4 bits
+hipError_t launch_quantize_mxfp4(const void* x, int x_dtype, int64_t n, uint8_t* q, uint8_t* qs,
+                                 uint16_t* values, hipStream_t s);
+hipError_t launch_join_norm(const void* b, int b_dtype, const void* res, int s_dtype,
+                            float res_scale, float block_scale, const float* gate,
+                            const void* w_post, int post_dtype, const void* w_pre, int pre_dtype,
+                            int T, int H, float eps, void* sum, float* ro, float* ri,
+                            uint16_t* out, uint8_t* q, uint8_t* qs, bool q4, hipStream_t s);
+size_t join_norm_ws_bytes(int64_t T, int H);
+hipError_t launch_join_norm_backward(const void* dy, int dy_dtype, const void* sv, int s_dtype,
+                                     const void* b, int b_dtype, const void* ds, float res_scale,
+                                     float block_scale, const float* gate, const void* w_post,
+                                     int post_dtype, const void* w_pre, int pre_dtype,
+                                     const float* ro, const float* ri, int T, int H, void* db,
+                                     void* dres, float* dgate, float* dw_post, float* dw_pre,
+                                     void* ws, hipStream_t st);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

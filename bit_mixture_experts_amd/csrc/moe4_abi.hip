@@ -939,6 +939,139 @@ int moe4_clip_grads(const void* const* grads, void* const* outs, const int64_t* 
                   "moe4_clip_grads");
 }
 
+int moe4_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t R, int64_t K, uint8_t* blocks,
+                        uint8_t* scales, uint16_t* values, void* stream) {
+  REQUIRE_DTYPE(x_dtype, "x_dtype");
+  if (R < 0) return fail(MOE4_ESHAPE, "R = %lld is negative", (long long)R);
+  if (K < 0 || K % 32)
+    return fail(MOE4_ESHAPE, "K = %lld is not a non-negative multiple of 32", (long long)K);
+  if (K && R > ((int64_t)1 << 40) / K)
+    return fail(MOE4_ESHAPE, "R * K is beyond the supported 2^40");
+  if (R == 0 || K == 0) return ok();
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(blocks, "blocks");
+  REQUIRE_PTR(scales, "scales");
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(blocks, 16, "blocks");
+  REQUIRE_ALIGN(values, 16, "values");
+  return launched(moe4::launch_quantize_mxfp4(x, x_dtype, R * K, blocks, scales, values,
+                                              (hipStream_t)stream),
+                  "moe4_quantize_mxfp4");
+}
+
+int moe4_join_norm(const void* b, int32_t b_dtype, const void* residual, int32_t s_dtype,
+                   float res_scale, float block_scale, const float* gate, const void* w_post,
+                   int32_t post_dtype, const void* w_pre, int32_t pre_dtype, int32_t T,
+                   int32_t H, float eps, void* sum_out, float* rstd_post, float* rstd_pre,
+                   uint16_t* out, uint8_t* out_q, uint8_t* out_s, int32_t q_format,
+                   void* stream) {
+  int rc = check_norm_shape(T, H);
+  if (rc) return rc;
+  REQUIRE_DTYPE(b_dtype, "b_dtype");
+  REQUIRE_DTYPE(s_dtype, "s_dtype");
+  if (w_post) REQUIRE_DTYPE(post_dtype, "post_dtype");
+  if (w_pre) REQUIRE_DTYPE(pre_dtype, "pre_dtype");
+  if (!(eps >= 0.0f)) return fail(MOE4_EINVAL, "eps = %g must not be negative", (double)eps);
+  if ((out_q == nullptr) != (out_s == nullptr))
+    return fail(MOE4_EINVAL, "out_q and out_s must be given together");
+  if (out_q && q_format != MOE4_X_MXFP8 && q_format != MOE4_X_MXFP4)
+    return fail(MOE4_EINVAL, "q_format %s (%d)", q_format ? "is neither MXFP8 nor MXFP4" : "unset",
+                q_format);
+  if (out_q && H % 32)
+    return fail(MOE4_ESHAPE, "H = %d must be a multiple of 32 for an 8- or 4-bit output", H);
+  if (T == 0) return ok();
+  REQUIRE_PTR(b, "b");
+  if (!w_pre && (out || out_q || rstd_pre))
+    return fail(MOE4_EINVAL, "%s given without w_pre", out ? "out" : out_q ? "out_q" : "rstd_pre");
+  if (!w_post && rstd_post) return fail(MOE4_EINVAL, "rstd_post given without w_post");
+  if (!out && !out_q && !sum_out)
+    return fail(MOE4_EINVAL, "sum_out, out and out_q are all NULL");
+  if (w_pre && !out && !out_q) return fail(MOE4_EINVAL, "w_pre given, out and out_q both NULL");
+  REQUIRE_ALIGN(b, 16, "b");
+  REQUIRE_ALIGN(residual, 16, "residual");
+  REQUIRE_ALIGN(gate, 4, "gate");
+  REQUIRE_ALIGN(w_post, 16, "w_post");
+  REQUIRE_ALIGN(w_pre, 16, "w_pre");
+  REQUIRE_ALIGN(sum_out, 16, "sum_out");
+  REQUIRE_ALIGN(rstd_post, 4, "rstd_post");
+  REQUIRE_ALIGN(rstd_pre, 4, "rstd_pre");
+  REQUIRE_ALIGN(out, 16, "out");
+  REQUIRE_ALIGN(out_q, 16, "out_q");
+  return launched(moe4::launch_join_norm(b, b_dtype, residual, s_dtype, res_scale, block_scale,
+                                         gate, w_post, post_dtype, w_pre, pre_dtype, T, H, eps,
+                                         sum_out, rstd_post, rstd_pre, out, out_q, out_s,
+                                         q_format == MOE4_X_MXFP4, (hipStream_t)stream),
+                  "moe4_join_norm");
+}
+
+size_t moe4_join_norm_workspace_size(int32_t T, int32_t H) {
+  if (check_norm_shape(T, H) != MOE4_OK) return 0;
+  ok();
+  const size_t need = moe4::join_norm_ws_bytes(T, H);
+  return need < 256 ? 256 : need;
+}
+
+int moe4_join_norm_backward(const void* dy, int32_t dy_dtype, const void* s, int32_t s_dtype,
+                            const void* b, int32_t b_dtype, const void* ds, float res_scale,
+                            float block_scale, const float* gate, const void* w_post,
+                            int32_t post_dtype, const void* w_pre, int32_t pre_dtype,
+                            const float* rstd_post, const float* rstd_pre, int32_t T, int32_t H,
+                            void* db, void* dres, float* dgate, float* dw_post, float* dw_pre,
+                            void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_norm_shape(T, H);
+  if (rc) return rc;
+  REQUIRE_DTYPE(s_dtype, "s_dtype");
+  REQUIRE_DTYPE(b_dtype, "b_dtype");
+  if (w_post) REQUIRE_DTYPE(post_dtype, "post_dtype");
+  if (w_pre) {
+    REQUIRE_DTYPE(pre_dtype, "pre_dtype");
+    REQUIRE_DTYPE(dy_dtype, "dy_dtype");
+  } else if (dy || s || rstd_pre || dw_pre) {
+    return fail(MOE4_EINVAL, "%s given without w_pre",
+                dy ? "dy" : s ? "s" : rstd_pre ? "rstd_pre" : "dw_pre");
+  }
+  if (!w_post && (rstd_post || dw_post))
+    return fail(MOE4_EINVAL, "%s given without w_post", rstd_post ? "rstd_post" : "dw_post");
+  if (T > 0) {
+    if (w_pre) {
+      REQUIRE_PTR(dy, "dy");
+      REQUIRE_PTR(s, "s");
+      REQUIRE_PTR(rstd_pre, "rstd_pre");
+    } else {
+      REQUIRE_PTR(ds, "ds");
+    }
+    if (w_post) REQUIRE_PTR(rstd_post, "rstd_post");
+    REQUIRE_PTR(b, "b");
+    REQUIRE_PTR(db, "db");
+    if (db == dres) return fail(MOE4_EINVAL, "db and dres are the same memory");
+  }
+  REQUIRE_ALIGN(dy, 16, "dy");
+  REQUIRE_ALIGN(s, 16, "s");
+  REQUIRE_ALIGN(b, 16, "b");
+  REQUIRE_ALIGN(ds, 16, "ds");
+  REQUIRE_ALIGN(gate, 4, "gate");
+  REQUIRE_ALIGN(w_post, 16, "w_post");
+  REQUIRE_ALIGN(w_pre, 16, "w_pre");
+  REQUIRE_ALIGN(rstd_post, 4, "rstd_post");
+  REQUIRE_ALIGN(rstd_pre, 4, "rstd_pre");
+  REQUIRE_ALIGN(db, 16, "db");
+  REQUIRE_ALIGN(dres, 16, "dres");
+  REQUIRE_ALIGN(dgate, 4, "dgate");
+  REQUIRE_ALIGN(dw_post, 16, "dw_post");
+  REQUIRE_ALIGN(dw_pre, 16, "dw_pre");
+  if ((dw_post || dw_pre) && T > 0) {
+    rc = check_ws(ws, ws_bytes, moe4::join_norm_ws_bytes(T, H), "moe4_join_norm_backward");
+    if (rc) return rc;
+  }
+  if (T == 0 && !dw_post && !dw_pre) return ok();
+  return launched(
+      moe4::launch_join_norm_backward(dy, dy_dtype, s, s_dtype, b, b_dtype, ds, res_scale,
+                                      block_scale, gate, w_post, post_dtype, w_pre, pre_dtype,
+                                      rstd_post, rstd_pre, T, H, db, dres, dgate, dw_post, dw_pre,
+                                      ws, (hipStream_t)stream),
+      "moe4_join_norm_backward");
+}
+
 size_t moe4_workspace_size(const moe4_experts* ex, int32_t T, int32_t k) {
   if (check_experts(ex) != MOE4_OK) return 0;
   if (T < 0 || k < 1 || k > ex->E || (int64_t)T * k >= ((int64_t)1 << 31)) {

@@ -32,6 +32,7 @@ MOE4_VARIANT_AUTO, MOE4_VARIANT_SKINNY, MOE4_VARIANT_TILED = 0, 1, 2
 MOE4_DTYPE_BF16, MOE4_DTYPE_F32 = 1, 2
 MOE4_NOALLOC_SCRATCH_BYTES = 16 << 20
 MOE4_FFN_BF16, MOE4_FFN_MXFP8 = 1, 2
+MOE4_X_BF16, MOE4_X_MXFP8, MOE4_X_MXFP4 = 1, 2, 3
 
 # every symbol declared in include/moe4.h
 EXPORTS = ("moe4_quantize_nf4", "moe4_compress_absmax", "moe4_expand_absmax",
@@ -42,7 +43,8 @@ EXPORTS = ("moe4_quantize_nf4", "moe4_compress_absmax", "moe4_expand_absmax",
            "moe4_add_rmsnorm", "moe4_add_rmsnorm_backward", "moe4_add_rmsnorm_workspace_size",
            "moe4_quantize_mxfp8", "moe4_ffn_forward", "moe4_ffn_backward",
            "moe4_ffn_workspace_size", "moe4_grad_norm", "moe4_clip_grads",
-           "moe4_grad_workspace_size",
+           "moe4_grad_workspace_size", "moe4_quantize_mxfp4", "moe4_join_norm",
+           "moe4_join_norm_backward", "moe4_join_norm_workspace_size",
            "moe4_workspace_size", "moe4_set_timing_events", "moe4_last_error",
            "moe4_last_variant")
 
@@ -117,6 +119,13 @@ _SIGS = {
     "moe4_grad_norm": ([_vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp], ctypes.c_int),
     "moe4_clip_grads": ([_vp, _vp, _vp, _vp, _i32, _f32c, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "moe4_grad_workspace_size": ([_i32], ctypes.c_size_t),
+    "moe4_quantize_mxfp4": ([_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "moe4_join_norm": ([_vp, _i32, _vp, _i32, _f32c, _f32c, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                        _f32c, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp], ctypes.c_int),
+    "moe4_join_norm_backward": ([_vp, _i32, _vp, _i32, _vp, _i32, _vp, _f32c, _f32c, _vp, _vp,
+                                 _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, _sz, _vp], ctypes.c_int),
+    "moe4_join_norm_workspace_size": ([_i32, _i32], ctypes.c_size_t),
     "moe4_workspace_size": ([_P, _i32, _i32], ctypes.c_size_t),
     "moe4_set_timing_events": ([_vp, _i32], ctypes.c_int),
     "moe4_last_error": ([], ctypes.c_char_p),
@@ -710,3 +719,91 @@ def moe4_clip_grads(grads, max_norm, norm_out=None, ws=None, norm_in=None, strea
                                 max_norm, c.ptr(norm_in, "norm_in", (1,), _F32),
                                 c.ptr(norm_out, "norm_out", (1,), _F32), pw, nw,
                                 c.stream(stream)))
+
+
+# ---- a block held in 4 bits: MXFP4 quantiser, what stands between two blocks
+
+def moe4_quantize_mxfp4(x, blocks, scales, values=None, stream=None):
+    """x bf16 or f32 [..., K] -> blocks u8 [..., K/32, 16], scales (u8 or float8_e8m0fnu)
+    [..., K/32]; values bf16 [..., K]: what the codes stand for (may be x)."""
+    c = _Call("quantize_mxfp4")
+    sh = tuple(x.shape)
+    if not sh:
+        raise ValueError("quantize_mxfp4: x has no dimension")
+    K = sh[-1]
+    R = x.numel() // K if K else 0
+    nb = sh[:-1] + (K // 32,)
+    rc = _lib.moe4_quantize_mxfp4(
+        c.ptr(x, "x", sh, _FLOATS), _dt(x), R, K, c.ptr(blocks, "blocks", nb + (16,), _U8),
+        c.ptr(scales, "scales", nb, _SCALES),
+        None if values is None else c.ptr(values, "values", sh, _BF16), c.stream(stream))
+    if rc:
+        _check(rc)
+
+
+def moe4_join_norm(b, w_pre, eps, residual=None, res_scale=1.0, block_scale=1.0, gate=None,
+                   w_post=None, sum_out=None, out=None, out_q=None, out_s=None, rstd_post=None,
+                   rstd_pre=None, stream=None):
+    """s = res_scale * residual + block_scale * gate * (b, normed with w_post) -> sum_out;
+    y = s, normed with w_pre, as bf16 (out) and, or, in 8 or 4 bits (out_q u8 or float8_e4m3fn
+    [T, H], or u8 [T, H/32, 16]; out_s [T, H/32]). b, and residual and sum_out (one type), bf16 or
+    f32 [T, H]; gate f32 [T]; w_post, w_pre bf16 or f32 [H]; rstd_post, rstd_pre f32 [T]. Without
+    w_pre: the sum alone."""
+    c = _Call("join_norm")
+    T, H = sh = b.shape
+    if T >> 31 or H >> 31:
+        _int32(c.fn, T=T, H=H)
+    if residual is not None and sum_out is not None and sum_out.dtype != residual.dtype:
+        raise TypeError("sum_out must have the residual's dtype")
+    stream_t = sum_out if residual is None else residual
+    q4 = out_q is not None and out_q.dim() == 3
+    ptr = c.ptr
+    rc = _lib.moe4_join_norm(
+        ptr(b, "b", sh, _FLOATS), _dt(b), ptr(residual, "residual", sh, _FLOATS),
+        MOE4_DTYPE_BF16 if stream_t is None else _dt(stream_t), res_scale, block_scale,
+        ptr(gate, "gate", (T,), _F32), ptr(w_post, "w_post", (H,), _FLOATS), _dt(w_post),
+        ptr(w_pre, "w_pre", (H,), _FLOATS), _dt(w_pre), T, H, eps,
+        ptr(sum_out, "sum_out", sh, _FLOATS), ptr(rstd_post, "rstd_post", (T,), _F32),
+        ptr(rstd_pre, "rstd_pre", (T,), _F32), ptr(out, "out", sh, _BF16),
+        ptr(out_q, "out_q", (T, H // 32, 16) if q4 else sh, _U8 if q4 else _CODES),
+        ptr(out_s, "out_s", (T, H // 32), _SCALES), MOE4_X_MXFP4 if q4 else MOE4_X_MXFP8,
+        c.stream(stream))
+    if rc:
+        _check(rc)
+
+
+def moe4_join_norm_workspace_size(T, H):
+    _int32("join_norm_workspace_size", T=T, H=H)
+    n = _lib.moe4_join_norm_workspace_size(T, H)
+    if n == 0:
+        raise Moe4Error(MOE4_ESHAPE, moe4_last_error())
+    return n
+
+
+def moe4_join_norm_backward(dy, s, b, w_pre, rstd_pre, db, dres=None, ds=None, res_scale=1.0,
+                            block_scale=1.0, gate=None, w_post=None, rstd_post=None, dgate=None,
+                            dw_post=None, dw_pre=None, ws=None, stream=None):
+    """Gradients of moe4_join_norm: db (of b's dtype), dres (of the stream's; res_scale applied),
+    dgate f32 [T], dw_post and dw_pre f32 [H]. ds: the gradient that reaches s past the second norm.
+    Without w_pre: dy, s, rstd_pre None, and ds needed."""
+    c = _Call("join_norm_backward")
+    T, H = sh = b.shape
+    if T >> 31 or H >> 31:
+        _int32(c.fn, T=T, H=H)
+    of_stream = [t for t in (s, ds, dres) if t is not None]
+    if any(t.dtype != of_stream[0].dtype for t in of_stream):
+        raise TypeError("s, ds and dres must have one dtype")
+    if db.dtype != b.dtype:
+        raise TypeError("db must have b's dtype")
+    pb = c.ptr(b, "b", sh, _FLOATS)
+    pw, nw = c.ws(ws)
+    ptr = c.ptr
+    _check(_lib.moe4_join_norm_backward(
+        ptr(dy, "dy", sh, _FLOATS), _dt(dy), ptr(s, "s", sh, _FLOATS),
+        _dt(of_stream[0]) if of_stream else 0, pb, _dt(b), ptr(ds, "ds", sh, _FLOATS), res_scale,
+        block_scale, ptr(gate, "gate", (T,), _F32), ptr(w_post, "w_post", (H,), _FLOATS),
+        _dt(w_post), ptr(w_pre, "w_pre", (H,), _FLOATS), _dt(w_pre),
+        ptr(rstd_post, "rstd_post", (T,), _F32), ptr(rstd_pre, "rstd_pre", (T,), _F32), T, H,
+        ptr(db, "db", sh, _FLOATS), ptr(dres, "dres", sh, _FLOATS), ptr(dgate, "dgate", (T,), _F32),
+        ptr(dw_post, "dw_post", (H,), _F32), ptr(dw_pre, "dw_pre", (H,), _F32), pw, nw,
+        c.stream(stream)))

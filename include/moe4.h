@@ -595,6 +595,94 @@ int moe4_clip_grads(const void* const* grads, void* const* outs, const int64_t* 
  * gradients; 0 if n is invalid. */
 size_t moe4_grad_workspace_size(int32_t n);
 
+/* ------------------------------------------------------------------------
+ * A block whose weights are held in 4 bits: the MXFP4 quantiser, the dense
+ * product with an MXFP4 weight, the whole routed layer of a decode step, and
+ * what stands between two blocks. The rules of the dense half hold here too: an
+ * output shares memory with an input only where this says it may, and with no
+ * other output or workspace; calls that run at once have workspaces of their
+ * own.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * MXFP4 quantisation of rows of bf16 or fp32: e2m1 codes in blocks of 32 along
+ * the row, one e8m0 scale (the power of two 2^(byte - 127)) per block, laid out
+ * as moe4_experts and moe4_decode_mxfp4 read them. The scale is the smallest
+ * power of two, from 2^-127 on, that brings the block's largest magnitude to at
+ * most 7, which is half a step past the largest code 6; codes are value / scale
+ * rounded to nearest even, 7 and what lies between it and 6 to 6, so no value
+ * is off by more than half a step. A block that holds an infinity or a NaN takes
+ * scale byte 255 (NaN) and codes 0.
+ *   x [R, K] of x_dtype (16-byte aligned); K % 32 == 0
+ *   blocks u8 [R, K/32, 16] out (16-byte aligned), scales u8 [R, K/32] out
+ *   values bf16 [R, K] out (16-byte aligned) or NULL: what the codes stand for
+ *   (exact; NaN in a block of scale 255, an infinity where code 4 meets scale
+ *   2^126, from magnitudes above 3.5 * 2^126), for a forward pass that sees the
+ *   rounded weights; may be x where x is bf16
+ */
+int moe4_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t R, int64_t K, uint8_t* blocks,
+                        uint8_t* scales, uint16_t* values, void* stream);
+
+/* 8- and 4-bit formats of activations (no default) */
+enum { MOE4_X_BF16 = 1, MOE4_X_MXFP8 = 2, MOE4_X_MXFP4 = 3 };
+
+/*
+ * Between two blocks: a block's output is normed, gated and scaled, joins the
+ * residual stream, and the stream is normed for the next block:
+ *   n = b * rstd_post * w_post, rstd_post[t] = 1 / sqrt(mean_h b^2 + eps)
+ *       (n = b without w_post)
+ *   s = res_scale * residual + block_scale * gate[t] * n, rounded to s_dtype
+ *   y = s * rstd_pre * w_pre,   rstd_pre[t] = 1 / sqrt(mean_h s^2 + eps)
+ * s goes to sum_out; y is written as bf16 (out), as MXFP8 or MXFP4 (out_q and
+ * out_s, each value rounded once from fp32), or both. fp32 sums; a row whose sum
+ * of squares passes fp32's range gives rstd 0.
+ *   b [T, H] of b_dtype; residual [T, H] of s_dtype or NULL (zeros); gate f32 [T]
+ *   or NULL (ones); w_post [H] of post_dtype or NULL; w_pre [H] of pre_dtype or
+ *   NULL (then no y: sum_out alone); eps >= 0; 8 <= H <= 16384, a multiple of 8
+ *   (32 with out_q)
+ *   sum_out [T, H] of s_dtype or NULL (may be the residual itself, or b where the
+ *   type is the same); out bf16 [T, H] or NULL; q_format MOE4_X_MXFP8 or
+ *   MOE4_X_MXFP4 with out_q u8 [T, H] or [T, H/32, 16] and out_s u8 [T, H/32],
+ *   both or neither; rstd_post, rstd_pre f32 [T] or NULL
+ *   b, residual, sum_out, w_post, w_pre, out, out_q 16-byte aligned
+ */
+int moe4_join_norm(const void* b, int32_t b_dtype, const void* residual, int32_t s_dtype,
+                   float res_scale, float block_scale, const float* gate, const void* w_post,
+                   int32_t post_dtype, const void* w_pre, int32_t pre_dtype, int32_t T,
+                   int32_t H, float eps, void* sum_out, float* rstd_post, float* rstd_pre,
+                   uint16_t* out, uint8_t* out_q, uint8_t* out_s, int32_t q_format,
+                   void* stream);
+
+/*
+ * Its backward pass. With t = s * rstd_pre and m = b * rstd_post (m = b without
+ * w_post), ds the gradient that reaches s past the second norm:
+ *   dS = rstd_pre * (w_pre dy - t mean_h(w_pre dy t)) + ds      (ds without w_pre)
+ *   dres = res_scale * dS
+ *   q = w_post dS, D = sum_h q m                                (q = dS without w_post)
+ *   dgate[t] = block_scale * D
+ *   db = block_scale gate rstd_post (q - m D / H)    (block_scale gate dS without)
+ *   dw_post = block_scale sum_t gate dS m;  dw_pre = sum_t dy t
+ * (fp32 sums in a fixed order; dS is not rounded.)
+ *   dy [T, H] of dy_dtype and s [T, H] of s_dtype with rstd_pre f32 [T], needed
+ *   with w_pre, NULL without; ds [T, H] of s_dtype or NULL (needed without w_pre);
+ *   b [T, H] of b_dtype; rstd_post f32 [T], needed with w_post
+ *   db [T, H] out of b_dtype (may be b; or ds, dy or s where the type is the same)
+ *   dres [T, H] out of s_dtype or NULL (may be ds, dy or s likewise, not db)
+ *   dgate f32 [T] out or NULL; dw_post (with w_post), dw_pre (with w_pre) f32 [H]
+ *   out or NULL; zeros for T = 0
+ *   ws: at least moe4_join_norm_workspace_size bytes (256-byte aligned) with
+ *   dw_post or dw_pre, else unused; all [T, H] and [H] tensors 16-byte aligned
+ */
+int moe4_join_norm_backward(const void* dy, int32_t dy_dtype, const void* s, int32_t s_dtype,
+                            const void* b, int32_t b_dtype, const void* ds, float res_scale,
+                            float block_scale, const float* gate, const void* w_post,
+                            int32_t post_dtype, const void* w_pre, int32_t pre_dtype,
+                            const float* rstd_post, const float* rstd_pre, int32_t T, int32_t H,
+                            void* db, void* dres, float* dgate, float* dw_post, float* dw_pre,
+                            void* ws, size_t ws_bytes, void* stream);
+/* 0 if T or H is invalid; never less than for fewer rows */
+size_t moe4_join_norm_workspace_size(int32_t T, int32_t H);
+
 /*
  * Optional launch timing, for measurement. After this call the calling
  * thread's moe4_expert_forward records events[0] / events[1] (hipEvent_t
@@ -616,8 +704,8 @@ size_t moe4_workspace_size(const moe4_experts* ex, int32_t T, int32_t k);
 const char* moe4_last_error(void);
 
 /* Kernel family of the calling thread's last moe4_expert_forward,
- * moe4_expert_backward or moe4_ffn_forward: MOE4_VARIANT_SKINNY or MOE4_VARIANT_TILED (0 if none
- * ran), so callers can assert which kernel engaged. */
+ * moe4_expert_backward, moe4_ffn_forward or moe4_linear_forward: MOE4_VARIANT_SKINNY or
+ * MOE4_VARIANT_TILED (0 if none ran), so callers can assert which kernel engaged. */
 int moe4_last_variant(void);
 
 #ifdef __cplusplus
