@@ -163,6 +163,11 @@ hipError_t launch_join_norm_backward(const void* dy, int dy_dtype, const void* s
                                      const float* ro, const float* ri, int T, int H, void* db,
                                      void* dres, float* dgate, float* dw_post, float* dw_pre,
                                      void* ws, hipStream_t st);
+size_t layer_decode_ws_bytes(const moe4_experts& ex, int T, int k);
+hipError_t launch_layer_decode(const moe4_experts& ex, const uint16_t* x, const float* logits,
+                               int T, int k, int renorm, const void* residual, int res_dtype,
+                               void* out, int out_dtype, int32_t* topk_idx, float* topk_w,
+                               void* ws, hipStream_t s);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -1072,6 +1072,62 @@ int moe4_join_norm_backward(const void* dy, int32_t dy_dtype, const void* s, int
       "moe4_join_norm_backward");
 }
 
+static int check_layer_decode(const moe4_experts* ex, int32_t T, int32_t k) {
+  int rc = check_experts(ex);
+  if (rc) return rc;
+  if (ex->lora_A)
+    return fail(MOE4_EUNSUPPORTED, "moe4_layer_decode: adapters (lora_A) take moe4_expert_forward");
+  if (ex->variant == MOE4_VARIANT_TILED)
+    return fail(MOE4_EUNSUPPORTED, "moe4_layer_decode: moe4_experts.variant TILED");
+  if (ex->format == MOE4_FMT_NF4_DQ && (ex->H > 16384 || ex->I > 16384))
+    return fail(MOE4_EUNSUPPORTED, "moe4_layer_decode: double-quantised rows of H = %d, I = %d "
+                "beyond 16384", ex->H, ex->I);
+  // one launch's grid: slots x groups of 16 pairs
+  if (ex->H > 1 << 20 || ex->I > 1 << 20)
+    return fail(MOE4_ESHAPE, "moe4_layer_decode: H = %d, I = %d beyond 2^20", ex->H, ex->I);
+  // the scales and the activations are addressed with 32-bit byte offsets too
+  if (T < 0 || T > MOE4_LAYER_MOST_TOKENS)
+    return fail(MOE4_ESHAPE, "T = %d outside [0, %d]", T, (int)MOE4_LAYER_MOST_TOKENS);
+  if (k < 1 || k > ex->E) return fail(MOE4_ESHAPE, "k = %d outside [1, E = %d]", k, ex->E);
+  if ((int64_t)T * k > MOE4_LAYER_MOST_SLOTS)
+    return fail(MOE4_ESHAPE, "T * k = %lld beyond %d slots", (long long)T * k,
+                (int)MOE4_LAYER_MOST_SLOTS);
+  return MOE4_OK;
+}
+
+size_t moe4_layer_decode_workspace_size(const moe4_experts* ex, int32_t T, int32_t k) {
+  if (check_layer_decode(ex, T, k) != MOE4_OK) return 0;
+  ok();
+  const size_t need = moe4::layer_decode_ws_bytes(*ex, T, k);
+  return need < 256 ? 256 : need;
+}
+
+int moe4_layer_decode(const moe4_experts* ex, const uint16_t* x, const float* logits, int32_t T,
+                      int32_t k, int32_t renormalize, const void* residual, int32_t res_dtype,
+                      void* out, int32_t out_dtype, int32_t* topk_idx, float* topk_w, void* ws,
+                      size_t ws_bytes, void* stream) {
+  int rc = check_layer_decode(ex, T, k);
+  if (rc) return rc;
+  REQUIRE_DTYPE(out_dtype, "out_dtype");
+  if (residual) REQUIRE_DTYPE(res_dtype, "res_dtype");
+  if (T == 0) return ok();
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(logits, "logits");
+  REQUIRE_PTR(out, "out");
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(logits, 4, "logits");
+  REQUIRE_ALIGN(residual, 16, "residual");
+  REQUIRE_ALIGN(out, 16, "out");
+  REQUIRE_ALIGN(topk_idx, 4, "topk_idx");
+  REQUIRE_ALIGN(topk_w, 4, "topk_w");
+  rc = check_ws(ws, ws_bytes, moe4::layer_decode_ws_bytes(*ex, T, k), "moe4_layer_decode");
+  if (rc) return rc;
+  return launched(moe4::launch_layer_decode(*ex, x, logits, T, k, renormalize, residual, res_dtype,
+                                            out, out_dtype, topk_idx, topk_w, ws,
+                                            (hipStream_t)stream),
+                  "moe4_layer_decode");
+}
+
 size_t moe4_workspace_size(const moe4_experts* ex, int32_t T, int32_t k) {
   if (check_experts(ex) != MOE4_OK) return 0;
   if (T < 0 || k < 1 || k > ex->E || (int64_t)T * k >= ((int64_t)1 << 31)) {

@@ -32,6 +32,7 @@ MOE4_VARIANT_AUTO, MOE4_VARIANT_SKINNY, MOE4_VARIANT_TILED = 0, 1, 2
 MOE4_DTYPE_BF16, MOE4_DTYPE_F32 = 1, 2
 MOE4_NOALLOC_SCRATCH_BYTES = 16 << 20
 MOE4_FFN_BF16, MOE4_FFN_MXFP8 = 1, 2
+MOE4_LAYER_MOST_TOKENS, MOE4_LAYER_MOST_SLOTS = 32, 512
 MOE4_X_BF16, MOE4_X_MXFP8, MOE4_X_MXFP4 = 1, 2, 3
 
 # every symbol declared in include/moe4.h
@@ -44,7 +45,8 @@ EXPORTS = ("moe4_quantize_nf4", "moe4_compress_absmax", "moe4_expand_absmax",
            "moe4_quantize_mxfp8", "moe4_ffn_forward", "moe4_ffn_backward",
            "moe4_ffn_workspace_size", "moe4_grad_norm", "moe4_clip_grads",
            "moe4_grad_workspace_size", "moe4_quantize_mxfp4", "moe4_join_norm",
-           "moe4_join_norm_backward", "moe4_join_norm_workspace_size",
+           "moe4_join_norm_backward", "moe4_join_norm_workspace_size", "moe4_layer_decode",
+           "moe4_layer_decode_workspace_size",
            "moe4_workspace_size", "moe4_set_timing_events", "moe4_last_error",
            "moe4_last_variant")
 
@@ -126,6 +128,9 @@ _SIGS = {
                                  _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _sz, _vp], ctypes.c_int),
     "moe4_join_norm_workspace_size": ([_i32, _i32], ctypes.c_size_t),
+    "moe4_layer_decode": ([_P, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _sz,
+                           _vp], ctypes.c_int),
+    "moe4_layer_decode_workspace_size": ([_P, _i32, _i32], ctypes.c_size_t),
     "moe4_workspace_size": ([_P, _i32, _i32], ctypes.c_size_t),
     "moe4_set_timing_events": ([_vp, _i32], ctypes.c_int),
     "moe4_last_error": ([], ctypes.c_char_p),
@@ -807,3 +812,35 @@ def moe4_join_norm_backward(dy, s, b, w_pre, rstd_pre, db, dres=None, ds=None, r
         ptr(db, "db", sh, _FLOATS), ptr(dres, "dres", sh, _FLOATS), ptr(dgate, "dgate", (T,), _F32),
         ptr(dw_post, "dw_post", (H,), _F32), ptr(dw_pre, "dw_pre", (H,), _F32), pw, nw,
         c.stream(stream)))
+
+
+def moe4_layer_decode_workspace_size(ex, T, k):
+    _int32("layer_decode_workspace_size", T=T, k=k)
+    n = _lib.moe4_layer_decode_workspace_size(ctypes.byref(ex.desc), T, k)
+    if n == 0:
+        raise Moe4Error(MOE4_EINVAL, moe4_last_error())
+    return n
+
+
+def moe4_layer_decode(ex, x, logits, k, out, residual=None, topk_idx=None, topk_w=None,
+                      renormalize=True, ws=None, stream=None):
+    """The whole routed layer for up to MOE4_LAYER_MOST_TOKENS tokens: x bf16 [T, H], logits f32
+    [T, E] -> out bf16 or f32 [T, H] (+ residual bf16 or f32); topk_idx i32 and topk_w f32 [T, k]
+    take the routing."""
+    c = _Call("layer_decode")
+    T, H = x.shape[0], ex.H
+    if T >> 31:
+        _int32(c.fn, T=T)
+    _int32(c.fn, k=k)
+    c.place(ex.tensors[0], "gu_q")
+    ptr, sh = c.ptr, (T, H)
+    pw, nw = c.ws(ws)
+    rc = _lib.moe4_layer_decode(
+        ctypes.byref(ex.desc), ptr(x, "x", sh, _BF16), ptr(logits, "logits", (T, ex.E), _F32), T, k,
+        1 if renormalize else 0,
+        None if residual is None else ptr(residual, "residual", sh, _FLOATS), _dt(residual),
+        ptr(out, "out", sh, _FLOATS), _dt(out),
+        None if topk_idx is None else ptr(topk_idx, "topk_idx", (T, k), _I32),
+        None if topk_w is None else ptr(topk_w, "topk_w", (T, k), _F32), pw, nw, c.stream(stream))
+    if rc:
+        _check(rc)

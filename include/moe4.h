@@ -626,6 +626,38 @@ int moe4_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t R, int64_t K, ui
 /* 8- and 4-bit formats of activations (no default) */
 enum { MOE4_X_BF16 = 1, MOE4_X_MXFP8 = 2, MOE4_X_MXFP4 = 3 };
 
+/* most tokens, and most routed slots (T * k), of moe4_layer_decode */
+enum { MOE4_LAYER_MOST_TOKENS = 32, MOE4_LAYER_MOST_SLOTS = 512 };
+
+/*
+ * A whole routed layer for the few tokens of a decode step, in two launches:
+ *   top-k of the logits as moe4_route takes it, then for each slot
+ *   h = act(W_gu[e] x + b_gu[e]), and
+ *   out[t] = sum_j w[t, j] * (W_d[e] h + b_d[e]) (+ residual[t])
+ * Each expert that tokens chose is read once for every 8 of them. Weights are not
+ * rounded (MXFP4 is exact, NF4's level * absmax is multiplied to 2^-17, where
+ * moe4_expert_forward rounds the product to bf16), sums are fp32 in a fixed order,
+ * h is rounded once to bf16, out once to its type. A token's NaN stays with it. For more tokens, adapters, or what a backward pass needs:
+ * moe4_route_permute, moe4_expert_forward_gather and moe4_combine.
+ *   ex: without adapters (else MOE4_EUNSUPPORTED); variant AUTO or SKINNY; NF4_DQ
+ *   with H and I up to 16384
+ *   x bf16 [T, H] (16-byte aligned), logits f32 [T, E], 1 <= k <= E, T <=
+ *   MOE4_LAYER_MOST_TOKENS, T * k <= MOE4_LAYER_MOST_SLOTS (else MOE4_ESHAPE);
+ *   NaN logits give unspecified (but some k distinct) experts
+ *   residual [T, H] of res_dtype or NULL; out [T, H] of out_dtype (may be the
+ *   residual where the types are the same, or x)
+ *   topk_idx i32 [T, k] and topk_w f32 [T, k] out, each or NULL
+ *   ws: at least moe4_layer_decode_workspace_size(ex, T, k) bytes (256-byte
+ *   aligned)
+ */
+int moe4_layer_decode(const moe4_experts* ex, const uint16_t* x, const float* logits, int32_t T,
+                      int32_t k, int32_t renormalize, const void* residual, int32_t res_dtype,
+                      void* out, int32_t out_dtype, int32_t* topk_idx, float* topk_w, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* 0 if the descriptor, T or k is invalid; never less than for fewer tokens */
+size_t moe4_layer_decode_workspace_size(const moe4_experts* ex, int32_t T, int32_t k);
+
 /*
  * Between two blocks: a block's output is normed, gated and scaled, joins the
  * residual stream, and the stream is normed for the next block:

@@ -1,6 +1,8 @@
 """Refusals of the operators of a block held in 4 bits: every bad argument is named synchronously,
 before anything is enqueued, so no call here reaches a device. The same file runs against the
 library's ASan build (test_dense_abi_asan.py's way, in test_block4_abi_asan.py)."""
+import ctypes
+
 import pytest
 
 moe4 = pytest.importorskip("bit_mixture_experts_amd.moe4")
@@ -111,3 +113,48 @@ def test_join_of_no_rows_and_workspace():
     for H in (64, 1024, 2880, 16384):   # never falls as the rows grow
         sizes = [lib.moe4_join_norm_workspace_size(T, H) for T in (0, 1, 7, 500, 2047, 2048, 2049, 8192, 1 << 30)]
         assert sizes == sorted(sizes) and sizes[0] >= 256 and sizes[-1] <= 2048 * H * 8
+
+
+# ------------------------------------------------------------------- layer
+
+def _ex(**kw):
+    a = dict(format=moe4.MOE4_FMT_NF4, E=8, H=128, I=64, gu_layout=1, act=1, act_alpha=1.702, act_limit=7.0,
+             gu_q=P, gu_s=P, dn_q=P, dn_s=P)
+    a.update(kw)
+    return moe4.Moe4Experts(**a)
+
+
+def _layer(ex=None, **kw):
+    a = dict(x=P, lg=P, T=4, k=2, rn=1, res=None, rd=0, out=P, od=BF, idx=None, w=None, ws=P, n=1 << 24)
+    a.update(kw)
+    return lib.moe4_layer_decode(ctypes.byref(ex if ex is not None else _ex()), *a.values(), None)
+
+
+@pytest.mark.parametrize("ex,kw,code,msg", [
+    (dict(format=0), {}, EINVAL, "format unset"), (dict(act=0), {}, EINVAL, "act unset"),
+    (dict(H=100), {}, ESHAPE, "H = 100"), (dict(gu_q=None), {}, EINVAL, "gu_q is NULL"),
+    (dict(lora_A=P, lora_B=P, lora_r=4, lora_scale=1.0), {}, EUNSUP, "adapters"),
+    (dict(variant=moe4.MOE4_VARIANT_TILED), {}, EUNSUP, "TILED"),
+    (dict(format=moe4.MOE4_FMT_NF4_DQ, gu_s2=P, dn_s2=P, gu_soff=P, dn_soff=P, dq_book=P, H=16448), {}, EUNSUP,
+     "16384"),
+    ({}, dict(T=33), ESHAPE, "T = 33"), ({}, dict(T=-1), ESHAPE, "T = -1"), ({}, dict(k=0), ESHAPE, "k = 0"),
+    ({}, dict(k=9), ESHAPE, "k = 9"), (dict(E=32), dict(T=32, k=17), ESHAPE, "512 slots"),
+    ({}, dict(od=0), EINVAL, "out_dtype unset"), ({}, dict(res=P), EINVAL, "res_dtype unset"),
+    ({}, dict(x=None), EINVAL, "x is NULL"), ({}, dict(lg=None), EINVAL, "logits is NULL"),
+    ({}, dict(out=None), EINVAL, "out is NULL"), ({}, dict(x=MIS), EALIGN, "x is not"),
+    ({}, dict(lg=P + 2), EALIGN, "logits is not"), ({}, dict(res=MIS, rd=BF), EALIGN, "residual is not"),
+    ({}, dict(out=MIS), EALIGN, "out is not"), ({}, dict(idx=P + 1), EALIGN, "topk_idx is not"),
+    ({}, dict(w=P + 2), EALIGN, "topk_w is not"), ({}, dict(ws=None), EWS, "needed"),
+    ({}, dict(n=64), EWS, "64 bytes given"), ({}, dict(ws=P + 16), EALIGN, "256-byte"),
+])
+def test_layer_refusals(ex, kw, code, msg):
+    refused(_layer(_ex(**ex), **kw), code, msg)
+
+
+def test_layer_of_no_tokens_and_workspace():
+    assert _layer(T=0, x=None, lg=None, out=None, ws=None, n=0) == OK
+    e = _ex()
+    size = lambda T, k: lib.moe4_layer_decode_workspace_size(ctypes.byref(e), T, k)   # noqa: E731
+    assert size(33, 2) == 0 and size(4, 9) == 0 and size(0, 2) >= 256
+    sizes = [size(T, 8) for T in range(33)]
+    assert sizes == sorted(sizes)
