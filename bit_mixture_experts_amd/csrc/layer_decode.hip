@@ -1,16 +1,18 @@
 // A whole routed layer for the few tokens of a decode step, in two launches:
-//   1. k_layer_up: every workgroup takes one routed slot and some gate/up pairs. It finds the slot's
-//      expert from the logits itself and, among all tokens, those that chose the same expert; the
-//      first slot of an expert works for all of them, the others end. h goes to the workspace.
+//   1. k_layer_up: every workgroup routes all tokens itself, from which it knows the experts that
+//      were chosen and their rows, and takes an even share of their gate/up pairs. h goes to the
+//      workspace, with the list of experts and rows.
 //   2. k_layer_down: every workgroup takes 8 output columns and runs over all experts that were
 //      chosen, so the weighted sum over a token's slots stays inside it.
-// No counter, flag or order of arrival decides anything: sums are in a fixed order.
+// No counter, flag or order of arrival between workgroups decides anything: sums are in a fixed
+// order.
 //
 // Both stream 4-bit weights for a handful of rows. One tile of either is 8 weight rows, each cut
 // into two halves of k, as the 16 columns (c, q) of a 16x16x32 MFMA, against 8 tokens' activations
 // in the same two halves as its 16 rows (t, q'): the products with q = q' are wanted, the others
 // are not read. So a wave's 16-byte loads cover 256 k of 8 rows, a layer's rows give twice the
 // tiles that 16-row tiles would, and no operand is padded to 16 tokens.
+
 #include <type_traits>
 
 #include "common.hpp"
@@ -23,17 +25,17 @@
 namespace moe4 {
 namespace {
 
-constexpr int kMostT = MOE4_LAYER_MOST_TOKENS;
 constexpr int kRowsPass = 8;   // tokens that one pass over an expert's weights serves
-static_assert(kMostT <= 32, "a row list's entries hold a token in 5 bits");
+static_assert(MOE4_LAYER_MOST_TOKENS <= 32, "an expert's tokens are the bits of a word");
 
 // ---------------------------------------------------------------- weights
 
 // NF4 without rounding: a level is the sum of two bf16 (to 2^-17 of it), both multiply the
 // activations exactly, and the block's absmax is applied to the fp32 sums of its 64 products.
-// byte -> (high parts of its two levels, low parts); LDS holds kLutCopies copies, lane l reads
-// copy l % kLutCopies, which spreads the lookups of a wave over the banks.
-struct Nf4Split {
+// byte -> (high parts of its two levels, low parts): 8 bytes. LDS holds 32 copies of an entry, a row
+// of 256 bytes, and lane l reads copy l mod 32: no two lanes of a half wave meet in a bank, and a
+// lookup's address is its byte beside the lane's own (one v_perm).
+struct alignas(16) Nf4Split {
   uint32_t v[512];
 };
 constexpr uint32_t bits_of(float f) { return __builtin_bit_cast(uint32_t, f); }
@@ -54,15 +56,31 @@ constexpr Nf4Split make_nf4_split() {
   return s;
 }
 __device__ constexpr Nf4Split kNf4Split = make_nf4_split();
-constexpr int kLutCopies = 4;
-constexpr int kLutBytes = 2048 * kLutCopies;
+constexpr int kLutCopies = 32;
+constexpr int lut_bytes(int fmt) { return fmt == MOE4_FMT_MXFP4 ? 0 : 2048 * kLutCopies; }
 
-__device__ __forceinline__ void fill_lut(u32x2* lut) {
-  for (int i = threadIdx.x; i < 256; i += blockDim.x) {
-    const u32x2 v = {kNf4Split.v[2 * i], kNf4Split.v[2 * i + 1]};
+template <int FMT>
+__device__ __forceinline__ void fill_lut(uint8_t* lut) {
+  if constexpr (FMT != MOE4_FMT_MXFP4) {
+    // 16 bytes (two copies) at a time, four reads in flight
+    constexpr int kAll = 256 * kLutCopies / 2;
+    for (int i0 = threadIdx.x; i0 < kAll; i0 += 4 * blockDim.x) {
+      u32x2 v[4];
 #pragma unroll
-    for (int c = 0; c < kLutCopies; ++c) lut[i * kLutCopies + c] = v;
+      for (int u = 0; u < 4; ++u) {
+        const int e = min(i0 + u * (int)blockDim.x, kAll - 1) / (kLutCopies / 2);
+        v[u] = reinterpret_cast<const u32x2*>(kNf4Split.v)[e];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * (int)blockDim.x;
+        if (i < kAll) reinterpret_cast<u32x4*>(lut)[i] = __builtin_shufflevector(v[u], v[u], 0, 1, 0, 1);
+      }
+    }
   }
+}
+__device__ __forceinline__ u32x2 lookup(const uint8_t* lut, uint32_t w, int byte, uint32_t lane8) {
+  return *reinterpret_cast<const u32x2*>(lut + __builtin_amdgcn_perm(w, lane8, 0x0C0C0000u | (4 + byte) << 8));
 }
 
 // 4x4 transpose of dwords across the four 16-lane rows of a wave: row g holds D[g][0..3] before and
@@ -75,7 +93,7 @@ __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
   return u32x4{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)d[0], (uint32_t)d[1]};
 }
 
-// One expert's matrix [rows][K] as its kernels read it.
+// A stack's matrices [rows][K] as its kernels read them.
 struct Stack {
   const uint8_t* q;
   const void* s;
@@ -83,103 +101,130 @@ struct Stack {
   int K, rows;
 };
 
-// The scales of one lane's 128 k of a weight row: NF4 two blocks, MXFP4 the lane's own 32
-template <int FMT>
-struct LaneScale {
-  uint32_t v[FMT == MOE4_FMT_MXFP4 ? 1 : 2];
-  float a2[FMT == MOE4_FMT_NF4_DQ ? 2 : 1];
-};
-
-// A weight row's piece in a lane: 16 bytes (32 k) and what scales them. row < st.rows, k the first
-// of the lane's 128-k step (its own 32 k at k + 32 g); pieces past K read as zeros.
+// What one lane holds of a weight row: 16 bytes (32 k), and what scales them: NF4 the absmax of the
+// two blocks of the row's 128-k step, MXFP4 the scale byte of the lane's own block.
 template <int FMT>
 struct Piece {
   u32x4 w;
-  LaneScale<FMT> s;
-  __device__ __forceinline__ void load(const Stack& st, int e, int row, int k) {
-    const int g = lane_id() >> 4;
-    const rsrc_t rq = make_rsrc_uniform(st.q + (int64_t)e * st.rows * (st.K / 2),
-                                        (uint32_t)((int64_t)st.rows * (st.K / 2)));
-    const int kk = k + 32 * g;
-    w = buf_load_b128(rq, kk < st.K ? (int)((uint32_t)row * (st.K / 2) + kk / 2) : kOob);
+  uint32_t s[FMT == MOE4_FMT_MXFP4 ? 1 : 2];
+  float a2[FMT == MOE4_FMT_NF4_DQ ? 2 : 1];
+};
+
+// One expert's matrix from a row on, and a lane's place in it: its row (counted from there) and its
+// 128-k step at k (its own 32 k at k + 32 g). Loads past the matrix or past K give zeros.
+template <int FMT>
+struct Stream {
+  static constexpr int kBlock = Format<FMT>::kBlock, kSb = FMT == MOE4_FMT_NF4 ? 4 : 1;
+  const uint8_t *q, *s;
+  const float* s2;
+  uint32_t q_bytes, s_bytes;   // from there to the matrix' end
+  int first;                   // double-quantised: flat index of its first absmax, mod 256
+  uint32_t vq, vs;
+  bool second;                 // the step's second NF4 block is in K
+
+  __device__ __forceinline__ void open(const Stack& st, int e, int row0, bool on) {
+    const int nb = st.K / kBlock;
+    const int64_t r0 = (int64_t)e * st.rows + row0;
+    const int left = on ? st.rows - row0 : 0;
+    q = st.q + r0 * (st.K / 2);
+    s = static_cast<const uint8_t*>(st.s) + r0 * nb * kSb;
+    q_bytes = (uint32_t)left * (uint32_t)(st.K / 2);
+    s_bytes = (uint32_t)left * (uint32_t)(nb * kSb);
+    if constexpr (FMT == MOE4_FMT_NF4_DQ) {
+      s2 = st.s2 + ((r0 * nb) >> 8);
+      first = (int)((r0 * nb) & 255);
+    }
+  }
+  __device__ __forceinline__ void place(int K, int row, int k) {
+    const int kk = k + 32 * (lane_id() >> 4), nb = K / kBlock;
+    vq = kk < K ? (uint32_t)(row * (K / 2) + kk / 2) : (uint32_t)kOob;
+    vs = FMT == MOE4_FMT_MXFP4 ? (kk < K ? (uint32_t)(row * nb + kk / 32) : (uint32_t)kOob)
+                               : (k < K ? (uint32_t)(row * nb + k / 64) * kSb : (uint32_t)kOob);
+    second = k + 64 < K;
+  }
+  // the piece `rows` (uniform) rows further on
+  __device__ __forceinline__ void load(Piece<FMT>& p, int K, int rows) const {
+    const int nb = K / kBlock;
+    const rsrc_t rq = make_rsrc_uniform(q, q_bytes), rs = make_rsrc_uniform(s, s_bytes);
+    // (the rows as the loads' scalar offset: no vector register for each)
+    p.w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)vq, rows * (K / 2), 0));
     if constexpr (FMT == MOE4_FMT_MXFP4) {
-      const int nb = st.K / 32;
-      const rsrc_t rs = make_rsrc_uniform(static_cast<const uint8_t*>(st.s) + (int64_t)e * st.rows * nb,
-                                          (uint32_t)(st.rows * nb));
-      s.v[0] = buf_load_u8(rs, kk < st.K ? row * nb + kk / 32 : kOob);
+      p.s[0] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)vs, rows * nb, 0);
     } else if constexpr (FMT == MOE4_FMT_NF4) {
-      const int nb = st.K / 64;
-      const rsrc_t rs = make_rsrc_uniform(static_cast<const float*>(st.s) + (int64_t)e * st.rows * nb,
-                                          (uint32_t)(st.rows * nb) * 4);
-      // (a second block past the row's end belongs to the next row: its weights are zeros' codes
-      // against zero activations)
-      const u32x2 r = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                     rs, k < st.K ? (int)((uint32_t)(row * nb + k / 64) * 4) : kOob, 0, 0));
-      s.v[0] = r[0];
-      s.v[1] = k + 64 < st.K ? r[1] : 0u;
+      const u32x2 r =
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)vs, rows * nb * 4, 0));
+      p.s[0] = r[0];
+      p.s[1] = r[1];
     } else {
-      const int nb = st.K / 64;
-      const int64_t first = (int64_t)e * st.rows * nb;
-      const uint8_t* codes = static_cast<const uint8_t*>(st.s) + first;
-      const int at = row * nb + min(k, st.K - 64) / 64;
-      const int at1 = k + 64 < st.K ? at + 1 : at;
-      s.v[0] = codes[at];
-      s.v[1] = codes[at1];
-      s.a2[0] = st.s2[(first + at) >> 8];
-      s.a2[1] = st.s2[(first + at1) >> 8];
+      const int at = (int)(vs + (uint32_t)(rows * nb));
+      p.s[0] = buf_load_u8(rs, at);
+      p.s[1] = buf_load_u8(rs, second ? at + 1 : kOob);
+      const bool on = (uint32_t)at < s_bytes;
+      p.a2[0] = s2[on ? (first + at) >> 8 : 0];
+      p.a2[1] = s2[on && second ? (first + at + 1) >> 8 : 0];
     }
   }
 };
 
-// The activations of one lane for a 128-k step: four MFMA operands
+// The activations of one lane for a 128-k step as MFMA operands. MXFP4: four, of the lane's own 32
+// k. NF4: each operand serves two bytes of codes, {high, low parts} of each, so it holds their two
+// pairs of activations twice.
+template <int FMT>
 struct Acts {
-  u32x4 v[4];
+  u32x4 v[FMT == MOE4_FMT_MXFP4 ? 4 : 8];
+  __device__ __forceinline__ void set(int i, u32x4 x) {
+    if constexpr (FMT == MOE4_FMT_MXFP4) {
+      v[i] = x;
+    } else {
+      v[2 * i] = u32x4{x[0], x[0], x[1], x[1]};
+      v[2 * i + 1] = u32x4{x[2], x[2], x[3], x[3]};
+    }
+  }
 };
+// the first k, within the step, of the lane's i-th 8
+template <int FMT>
+__device__ __forceinline__ int act_k(int i) {
+  const int g = lane_id() >> 4;
+  return FMT == MOE4_FMT_MXFP4 ? 32 * g + 8 * i : 32 * i + 8 * g;
+}
 // off: byte offset of the lane's row in the resource (kOob: no row); its step starts at k
 template <int FMT>
-__device__ __forceinline__ void load_acts(Acts& x, rsrc_t r, int off, int k, int K) {
-  const int g = lane_id() >> 4;
+__device__ __forceinline__ void load_acts(Acts<FMT>& x, rsrc_t r, int off, int k, int K) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int kk = k + (FMT == MOE4_FMT_MXFP4 ? 32 * g + 8 * i : 32 * i + 8 * g);
-    x.v[i] = buf_load_b128(r, off != kOob && kk < K ? off + 2 * kk : kOob);
+    const int kk = k + act_k<FMT>(i);
+    x.set(i, buf_load_b128(r, off != kOob && kk < K ? off + 2 * kk : kOob));
   }
 }
 
 // acc += one step's products. MXFP4: the lane's 32 k are one block, each weight exact in bf16. NF4:
-// the codes are put in MFMA order, so that two operands make a block.
+// the codes are put in MFMA order, so that two dwords of a lane make a block.
 template <int FMT>
-__device__ __forceinline__ void step(const Piece<FMT>& p, const Acts& x, const u32x2* lut, float off,
-                                     const float* book, f32x4& acc) {
+__device__ __forceinline__ void step(const Piece<FMT>& p, bool second, const Acts<FMT>& x,
+                                     const uint8_t* lut, float off, const float* book, f32x4& acc) {
   if constexpr (FMT == MOE4_FMT_MXFP4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.v[i]),
-                                                    __builtin_bit_cast(bf16x8, mx4_bf16x8(p.w[i], p.s.v[0])),
-                                                    acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8, x.v[i]), __builtin_bit_cast(bf16x8, mx4_bf16x8(p.w[i], p.s[0])),
+          acc, 0, 0, 0);
   } else {
     const u32x4 w = transpose4(p.w);
-    const u32x2* mine = lut + (lane_id() & (kLutCopies - 1));
+    const uint32_t lane8 = 8 * (lane_id() & (kLutCopies - 1));
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 2 * b; i < 2 * b + 2; ++i) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x2 v = mine[((w[i] >> (8 * j)) & 255u) * kLutCopies];
-          hi[j] = v[0];
-          lo[j] = v[1];
-        }
-        const bf16x8 a = __builtin_bit_cast(bf16x8, x.v[i]);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, hi), d, 0, 0, 0);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, lo), d, 0, 0, 0);
+      for (int i = 4 * b; i < 4 * b + 4; ++i) {
+        const u32x2 v0 = lookup(lut, w[i / 2], 2 * (i & 1), lane8);
+        const u32x2 v1 = lookup(lut, w[i / 2], 2 * (i & 1) + 1, lane8);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, x.v[i]),
+            __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3)), d, 0, 0, 0);
       }
       float s;
-      if constexpr (FMT == MOE4_FMT_NF4) s = __uint_as_float(p.s.v[b]);
-      else s = mul_then_add(book[p.s.v[b]], p.s.a2[b], off);
+      if constexpr (FMT == MOE4_FMT_NF4) s = b && !second ? 0.0f : __uint_as_float(p.s[b]);
+      else s = mul_then_add(book[p.s[b]], p.a2[b], off);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, d[i], acc[i]);
     }
@@ -191,8 +236,19 @@ __host__ __device__ constexpr int half_k(int K) { return (K + 255) / 256 * 128; 
 
 // ------------------------------------------------------------------ launch 1
 
-// A row list's entry: the slot, and its token
-__device__ __forceinline__ uint32_t list_entry(int slot, int t) { return (uint32_t)(slot | t << 16); }
+// Up to 8 rows of one expert: the expert (10 bits), how many rows (4), the first one's place among
+// all rows, which are ordered by expert and token (9)
+__device__ __forceinline__ uint32_t make_entry(int e, int n, int row) { return (uint32_t)(e | n << 10 | row << 14); }
+__device__ __forceinline__ int entry_expert(uint32_t v) { return v & 1023; }
+__device__ __forceinline__ int entry_rows(uint32_t v) { return (v >> 10) & 15; }
+__device__ __forceinline__ int entry_first(uint32_t v) { return (v >> 14) & 511; }
+static_assert(MOE4_LAYER_MOST_SLOTS <= 512, "an entry holds a row in 9 bits");
+
+// What the second launch knows of an expert and a group of 8 tokens: the expert (10 bits), the group
+// (2), the expert's first row (9); and all tokens of the expert as bits
+struct Use {
+  uint32_t what, tokens;
+};
 
 struct LayerArgs {
   Stack gu, dn;
@@ -208,281 +264,488 @@ struct LayerArgs {
   int out_dtype;
   int32_t* user_idx;
   float* user_w;
+  // runs of 128-k steps of the second launch: how many, of how many, 2^32 / runs plus one
+  int runs, run_steps;
+  uint32_t per_run;
   // workspace
-  uint16_t* h;       // [T * k][I], by slot
-  int32_t* idx;      // [T * k]
-  float* w;          // [T * k]
-  int32_t* cnt;      // [T * k] rows of the expert whose first slot this is, else 0
-  uint32_t* list;    // [T * k][kMostT] those rows' entries, tokens ascending
+  uint16_t* h;       // [rows = T * k][I], weighted
+  int32_t* idx;      // [T * k] experts of the slots
+  float* w;          // [T * k] and their weights
+  Use* uses;         // [T * k]
+  int32_t* count;    // [1] how many
 };
 
-// A token's experts in the order of moe4_route, by one wave: each pick is the largest key below the
-// one before
-template <int NPL>
-struct Picks {
-  uint64_t key[NPL], last = ~0ull;
-  __device__ __forceinline__ void init(const float* row, int E) {
-    const int l = lane_id();
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      key[i] = l + kWave * i < E ? select_key(row[l + kWave * i], l + kWave * i) : 0;
-  }
-  // the next expert (the same in every lane)
-  __device__ __forceinline__ int next() {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) best = max_u64(best, key[i] < last ? key[i] : 0);
-    last = wave_max_u64(best);
-    return (int)~(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)last);
-  }
-};
-// How many experts a token puts before expert e, by one wave
-template <int NPL>
-__device__ __forceinline__ int rank_of_expert(const float* row, int E, int e) {
-  const int l = lane_id();
-  const uint64_t mine = select_key(row[e], e);
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int o = l + kWave * i;
-    n += __popcll(__ballot(o < E && select_key(row[min(o, E - 1)], o) > mine));
-  }
-  return n;
+// A logit as an unsigned number of moe4_route's order: larger first, +0 as -0, NaN below all; 0 is
+// no candidate. Equal ones: the lower expert first.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
+  return v != v ? 1u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t o) {
+  return o == 1u ? __uint_as_float(0x7FC00000u)
+                 : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+  x = max_dpp<0xB1>(x);    // quad_perm [1,0,3,2]
+  x = max_dpp<0x4E>(x);    // quad_perm [2,3,0,1]
+  x = max_dpp<0x141>(x);   // row_half_mirror
+  x = max_dpp<0x140>(x);   // row_mirror
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// TG tiles of 4 gate/up pairs to a workgroup; wave v takes the 128-k steps v, v + waves, ... of both
-// halves of k for all of them, so its activations stay in registers and its loads are weights.
-template <int FMT, int TG, int NPL>
-__global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
+// A token's keys in a wave: lane l holds experts l, l + 64, ...
+template <int NPL>
+struct Keys {
+  uint32_t key[NPL];
+  __device__ __forceinline__ void load(const float* row, int E) {
+    const int l = lane_id();
+    float v[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = row[min(l + kWave * i, E - 1)];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) key[i] = l + kWave * i < E ? order_key(v[i]) : 0u;
+  }
+  // takes the first expert of the order out; its key in *k
+  __device__ __forceinline__ int pick(uint32_t* k) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) best = max(best, key[i]);
+    best = __builtin_amdgcn_readfirstlane(wave_max_u32(best));
+    int e = -1;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const uint64_t b = __ballot(key[i] == best);
+      if (e < 0 && b) {
+        e = (__ffsll((long long)b) - 1) + kWave * i;
+        if ((e & (kWave - 1)) == lane_id()) key[i] = 0u;
+      }
+    }
+    *k = best;
+    return e;
+  }
+};
+
+// 4 gate/up pairs to a tile, kTiles tiles to an item; the items of all entries are dealt to the
+// workgroups in equal runs. Wave v takes the 128-k step v (ONE: there are no more steps than waves)
+// of both halves of k for all items, so its activations stay in registers and its loads are
+// weights, DEPTH items ahead of the arithmetic.
+constexpr int kTiles = 4;
+constexpr int kRed = 68;   // floats of a tile's sums [8 rows][8 tokens], padded
+
+// LDS of the first launch, after the table and the sums: tokens of an expert [E] as bits, its first
+// row [E], entries [S], tokens and weights of the rows [S], experts and weights of the slots [S]
+__host__ __device__ constexpr int route_lds(int E, int S) { return 8 * E + 20 * S; }
+
+template <int FMT, int NPL, bool ONE, int DEPTH, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_layer_up(const LayerArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  u32x2* lut = reinterpret_cast<u32x2*>(smem);
-  float* red = reinterpret_cast<float*>(smem + (FMT == MOE4_FMT_MXFP4 ? 0 : kLutBytes));
-  constexpr int kRed = 68;   // floats of a tile's half: [c][t], padded
-  __shared__ int s_rank[kMostT], s_idx[MOE4_LAYER_MOST_SLOTS];
-  __shared__ float s_w[MOE4_LAYER_MOST_SLOTS];
   const int nw = blockDim.x >> 6, wv = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-  const int ntg = a.I / (4 * TG);
-  const int slot = blockIdx.x / ntg, tg = blockIdx.x - slot * ntg;
-  const int t0 = slot / a.k, j0 = slot - t0 * a.k;
-  if constexpr (FMT != MOE4_FMT_MXFP4) fill_lut(lut);
-  Picks<NPL> picks;
-  picks.init(a.logits + (int64_t)t0 * a.E, a.E);
-  int e = picks.next();
-  for (int j = 0; j < j0; ++j) e = picks.next();
-  for (int t = wv; t < a.T; t += nw) {
-    const int r = t == t0 ? j0 : rank_of_expert<NPL>(a.logits + (int64_t)t * a.E, a.E, e);
-    if (l == 0) s_rank[t] = r;
-  }
-  __syncthreads();
-  // tokens that chose e, as bits: the same in every wave
-  const uint32_t chose = (uint32_t)__ballot(l < a.T && s_rank[min(l, kMostT - 1)] < a.k);
-  const bool first = (chose & ((1u << t0) - 1)) == 0;
-  const int n = __popc(chose);
-  if (tg == 0 && wv == 0) {
-    // what the second launch reads: the slot's rows, and a token's routing by its first slot
-    if (l == 0) a.cnt[slot] = first ? n : 0;
-    if (first && (chose >> l & 1) && l < kMostT) {
-      const int at = __popc(chose & ((1u << l) - 1));
-      a.list[slot * kMostT + at] = list_entry(l * a.k + s_rank[l], l);
-    }
-  }
-  if (first) {
-    const int Kh = half_k(a.H), steps = Kh / 128;
-    const int m = l & 15, c = m & 7, q = m >> 3;   // a weight column (c, q), an activation row (t, q)
-    // the row of the gate/up stack of column c: gates 0..3, ups 4..7 of the tile's pairs
-    const rsrc_t rx = make_rsrc_uniform(a.x, (uint32_t)(a.T * a.H * 2));
-    for (int pass = 0; pass * kRowsPass < n; ++pass) {
-      // the token of activation row c of this pass
-      uint32_t left = chose;
-      for (int i = 0; i < pass * kRowsPass + c; ++i) left &= left - 1;
-      const int xoff = left ? (__ffs(left) - 1) * a.H * 2 : kOob;
-      f32x4 acc[TG];
+  const int S = a.T * a.k;
+  uint8_t* lut = smem;
+  float* red = reinterpret_cast<float*>(smem + lut_bytes(FMT));
+  uint32_t* chose = reinterpret_cast<uint32_t*>(red + 2 * nw * 2 * kTiles * kRed);
+  int* base = reinterpret_cast<int*>(chose + a.E);
+  uint32_t* entries = reinterpret_cast<uint32_t*>(base + a.E);
+  int* row_t = reinterpret_cast<int*>(entries + S);
+  float* row_w = reinterpret_cast<float*>(row_t + S);
+  int* slot_e = reinterpret_cast<int*>(row_w + S);
+  float* slot_w = reinterpret_cast<float*>(slot_e + S);
+  __shared__ int s_count;
+  const int Kh = half_k(a.H), steps = Kh / 128;
+  const int c = l & 7, q = (l >> 3) & 1, g = l >> 4;   // a weight column (c, q), an activation row (t, q)
+  const bool writer = blockIdx.x == 0;                 // hands the routing on
+
+  // ---- routing: a token by one wave
+  auto route = [&](int t) {
+    Keys<NPL> keys;
+    keys.load(a.logits + (int64_t)t * a.E, a.E);
+    float all = 0.0f, some = 0.0f, top = 0.0f;
+    if (!a.renorm) {   // softmax over all experts, not over the chosen alone
+      uint32_t m = keys.key[0];
 #pragma unroll
-      for (int j = 0; j < TG; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int st = wv; st < steps; st += nw) {
-        const int k = q * Kh + 128 * st;
-        Acts x;
-        load_acts<FMT>(x, rx, xoff, k, a.H);
-        Piece<FMT> p[TG];
-#pragma unroll
-        for (int j = 0; j < TG; ++j) {
-          const int pair = (tg * TG + j) * 4 + (c & 3);
-          const int row = c < 4 ? gate_row(a.layout, a.I, pair) : up_row(a.layout, a.I, pair);
-          p[j].load(a.gu, e, row, k);
-        }
-        const float off = FMT == MOE4_FMT_NF4_DQ ? a.gu.soff[0] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < TG; ++j) step<FMT>(p[j], x, lut, off, a.gu.book, acc[j]);
-      }
-      // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2
-      const int g = l >> 4;
-      if (pass) __syncthreads();   // the sums of the pass before have been read
-      if ((g >> 1) == q) {
-#pragma unroll
-        for (int j = 0; j < TG; ++j)
-          *reinterpret_cast<f32x4*>(red + ((wv * 2 + q) * TG + j) * kRed + c * 8 + 4 * (g & 1)) = acc[j];
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < TG * 4 * kRowsPass; i += blockDim.x) {
-        const int p = i % (TG * 4), t = i / (TG * 4), j = p / 4, cp = p & 3;
-        const int r = pass * kRowsPass + t;
-        if (r >= n) continue;
-        uint32_t rest = chose;
-        for (int u = 0; u < r; ++u) rest &= rest - 1;
-        const int tok = __ffs(rest) - 1, pair = (tg * TG + j) * 4 + cp;
-        float gt = 0.0f, up = 0.0f;
-        for (int v = 0; v < 2 * nw; ++v) {
-          const float* s = red + (v * TG + j) * kRed + cp * 8 + t;
-          gt += s[0];
-          up += s[32];
-        }
-        if (a.gu_bias) {
-          const uint16_t* b = a.gu_bias + (int64_t)e * 2 * a.I;
-          gt += bf16_to_f32(b[gate_row(a.layout, a.I, pair)]);
-          up += bf16_to_f32(b[up_row(a.layout, a.I, pair)]);
-        }
-        float h;
-        if (a.act == MOE4_ACT_SWIGLU) {
-          h = gt * sigmoidf_(gt) * up;
-        } else {   // comparisons, so that a NaN stays one
-          const float gc = gt > a.limit ? a.limit : gt;
-          const float uc = up > a.limit ? a.limit : up < -a.limit ? -a.limit : up;
-          h = (uc + 1.0f) * gc * sigmoidf_(a.alpha * gc);
-        }
-        // rounded once to bf16, the operand type of the second product
-        a.h[(int64_t)(tok * a.k + s_rank[tok]) * a.I + pair] = f32_to_bf16(h);
-      }
-    }
-  }
-  if (tg == 0 && j0 == 0 && wv == nw - 1) {
-    // the token's whole choice and its weights
-    picks.init(a.logits + (int64_t)t0 * a.E, a.E);
-    picks.last = ~0ull;
-    for (int j = 0; j < a.k; ++j) {
-      const int i = picks.next();
-      if (l == 0) {
-        s_idx[j] = i;
-        s_w[j] = key_value(picks.last);
-      }
-    }
-    // softmax over the chosen or over all experts
-    const float top = s_w[0];
-    float part = 0.0f;
-    if (a.renorm) {
-      for (int j = l; j < a.k; j += kWave) part += expf(s_w[j] - top);
-    } else {
+      for (int i = 1; i < NPL; ++i) m = max(m, keys.key[i]);
+      top = key_logit(wave_max_u32(m));
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (l + kWave * i < a.E) part += expf(key_value(picks.key[i]) - top);
+        if (keys.key[i]) all += expf(key_logit(keys.key[i]) - top);
     }
-    const float denom = wave_sum_dpp(part);
+    for (int j0 = 0; j0 < a.k; j0 += kWave) {
+      int mine = 0;
+      uint32_t mykey = 0;
+      const int n = min(kWave, a.k - j0);
+      for (int j = 0; j < n; ++j) {
+        uint32_t key;
+        const int e = keys.pick(&key);
+        if (j0 + j == 0 && a.renorm) top = key_logit(key);
+        if (l == j) {
+          mine = e;
+          mykey = key;
+        }
+      }
+      if (l < n) {
+        const int s = t * a.k + j0 + l;
+        slot_e[s] = mine;
+        if (a.T > 1) atomicOr(&chose[mine], 1u << t);
+        const float v = expf(key_logit(mykey) - top);
+        slot_w[s] = v;
+        some += v;
+      }
+    }
+    const float denom = wave_sum_dpp(a.renorm ? some : all);
     for (int j = l; j < a.k; j += kWave) {
-      const int i = s_idx[j], at = t0 * a.k + j;
-      const float w = expf(s_w[j] - top) / denom;
-      a.idx[at] = i;
-      a.w[at] = w;
-      if (a.user_idx) a.user_idx[at] = i;
-      if (a.user_w) a.user_w[at] = w;
+      const int s = t * a.k + j;
+      const float w = slot_w[s] / denom;
+      slot_w[s] = w;
+      if (writer) {
+        a.idx[s] = slot_e[s];
+        a.w[s] = w;
+        if (a.user_idx) a.user_idx[s] = slot_e[s];
+        if (a.user_w) a.user_w[s] = w;
+      }
+    }
+  };
+  if (a.T == 1) {
+    // an expert's rows are one row each, in the order of the choice
+    if (wv == 0) {
+      route(0);
+      for (int j = l; j < a.k; j += kWave) {
+        entries[j] = make_entry(slot_e[j], 1, j);
+        row_t[j] = 0;
+        row_w[j] = slot_w[j];
+        if (writer) a.uses[j] = {(uint32_t)(slot_e[j] | j << 12), 1u};
+      }
+      if (l == 0) {
+        s_count = a.k;
+        if (writer) a.count[0] = a.k;
+      }
+    }
+    fill_lut<FMT>(lut);
+    __syncthreads();
+  } else {
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) chose[i] = 0;
+    __syncthreads();
+    for (int t = wv; t < a.T; t += nw) route(t);
+    fill_lut<FMT>(lut);
+    __syncthreads();
+    if (wv == 0) {
+      int rows = 0, count = 0, uses = 0;
+      for (int e0 = 0; e0 < a.E; e0 += kWave) {
+        const int e = e0 + l;
+        const uint32_t bits = e < a.E ? chose[e] : 0u;
+        const int n = __popc(bits), m = (n + kRowsPass - 1) / kRowsPass;
+        const int r = wave_scan_dpp(n), p = wave_scan_dpp(m);
+        if (e < a.E) base[e] = rows + r - n;
+        for (int i = 0; i < m; ++i)
+          entries[count + p - m + i] =
+              make_entry(e, min(n - i * kRowsPass, kRowsPass), rows + r - n + i * kRowsPass);
+        if (writer) {
+          int groups = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) groups += (bits >> (8 * i) & 255u) != 0;
+          const int u = wave_scan_dpp(groups);
+          int at = uses + u - groups;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (bits >> (8 * i) & 255u) a.uses[at++] = {(uint32_t)(e | i << 10 | (rows + r - n) << 12), bits};
+          uses += __builtin_amdgcn_readlane(u, 63);
+        }
+        rows += __builtin_amdgcn_readlane(r, 63);
+        count += __builtin_amdgcn_readlane(p, 63);
+      }
+      if (l == 0) {
+        s_count = count;
+        if (writer) a.count[0] = uses;
+      }
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < S; s += blockDim.x) {
+      const int t = s / a.k, e = slot_e[s];
+      const int r = base[e] + __popc(chose[e] & ((1u << t) - 1));
+      row_t[r] = t;
+      row_w[r] = slot_w[s];
+    }
+    __syncthreads();
+  }
+  const int count = __builtin_amdgcn_readfirstlane(s_count);
+
+  // ---- this workgroup's run of items: 16 pairs from 16 it on of an entry's expert, for !ONE in
+  // rounds of the 128-k steps; gates are columns 0..3 of a tile, ups 4..7
+  const int items = a.I / (4 * kTiles), rounds = ONE ? 1 : (steps + nw - 1) / nw;
+  const int all = count * items;
+  const int first = (int)((int64_t)all * blockIdx.x / gridDim.x), end = (int)((int64_t)all * (blockIdx.x + 1) / gridDim.x);
+  if (first >= end) return;
+  const int mult = a.layout == MOE4_GU_HALVES ? 1 : 2;
+  const int row = c < 4 ? gate_row(a.layout, a.I, c & 3) : up_row(a.layout, a.I, c & 3);
+  const rsrc_t rx = make_rsrc_uniform(a.x, (uint32_t)(a.T * a.H * 2));
+  const float off = FMT == MOE4_FMT_NF4_DQ ? a.gu.soff[0] : 0.0f;
+  const int tp = (threadIdx.x >> 2) & (4 * kTiles - 1);   // the pair of an item that the thread finishes
+  struct Item {
+    Piece<FMT> p[kTiles];
+    uint32_t bias[2];
+    uint32_t entry;
+    int it, rd;
+    bool on, second;
+  };
+  // where the loads are: entry, item, round
+  int at_n = first, at_e = first / items, at_i = first % items, at_r = 0;
+  uint32_t at = __builtin_amdgcn_readfirstlane(entries[at_e]);
+  Stream<FMT> in;
+  in.place(a.H, row, q * Kh + 128 * wv);
+  auto load = [&](Item& w) {
+    const int st = wv + at_r * nw;
+    w.on = at_n < end;
+    w.entry = at;
+    w.it = at_i;
+    w.rd = at_r;
+    const bool on = w.on && st < steps;
+    in.open(a.gu, entry_expert(at), on ? at_i * 4 * kTiles * mult : 0, on);
+    if (!ONE) in.place(a.H, row, q * Kh + 128 * st);
+    w.second = in.second;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) in.load(w.p[j], a.H, 4 * j * mult);
+    if (a.gu_bias) {
+      const rsrc_t rb = make_rsrc_uniform(a.gu_bias + (int64_t)entry_expert(at) * 2 * a.I, w.on ? 4 * a.I : 0);
+      const int pair = at_i * 4 * kTiles + tp;
+      w.bias[0] = __builtin_amdgcn_raw_buffer_load_b16(rb, 2 * gate_row(a.layout, a.I, pair), 0, 0);
+      w.bias[1] = __builtin_amdgcn_raw_buffer_load_b16(rb, 2 * up_row(a.layout, a.I, pair), 0, 0);
+    } else {
+      w.bias[0] = w.bias[1] = 0;
+    }
+    if (!ONE && ++at_r < rounds) return;
+    at_r = 0;
+    ++at_n;
+    if (++at_i == items) {
+      at_i = 0;
+      ++at_e;
+      at = __builtin_amdgcn_readfirstlane(entries[min(at_e, count - 1)]);
+    }
+  };
+  Acts<FMT> x;
+  f32x4 acc[kTiles];
+  uint32_t have = ~0u;   // the entry whose rows x holds
+  int buf = 0;
+  auto run = [&](const Item& w) {
+    if (!ONE || w.entry != have) {
+      const int st = wv + w.rd * nw;
+      const int xoff = c < entry_rows(w.entry) && st < steps ? row_t[entry_first(w.entry) + c] * a.H * 2 : kOob;
+      load_acts<FMT>(x, rx, xoff, q * Kh + 128 * st, a.H);
+      have = w.entry;
+    }
+    if (w.rd == 0) {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) step<FMT>(w.p[j], w.second, x, lut, off, a.gu.book, acc[j]);
+    if (w.rd + 1 < rounds) return;
+    // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2
+    if ((g >> 1) == q) {
+      float* mine = red + ((buf * nw + wv) * 2 + q) * kTiles * kRed + c * 8 + 4 * (g & 1);
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) *reinterpret_cast<f32x4*>(mine + j * kRed) = acc[j];
+    }
+    // One barrier an item: the sums of the item after next go to the buffer read here. (Not
+    // __syncthreads, which would wait for the loads in flight.)
+    wait_lgkm0();
+    lds_barrier();
+    // four threads a pair, a wave a row
+    for (int t = wv; t < entry_rows(w.entry); t += nw) {
+      const float* s = red + (buf * nw * 2 + (l & 3)) * kTiles * kRed + (tp / 4) * kRed + (tp & 3) * 8 + t;
+      float gt = 0.0f, up = 0.0f;
+#pragma unroll 4
+      for (int v = l & 3; v < 2 * nw; v += 4, s += 4 * kTiles * kRed) {
+        gt += s[0];
+        up += s[32];
+      }
+      gt += dpp_f32<0xB1>(gt);   // the quad's sums, in every lane of it
+      gt += dpp_f32<0x4E>(gt);
+      up += dpp_f32<0xB1>(up);
+      up += dpp_f32<0x4E>(up);
+      gt += bf16_to_f32(w.bias[0]);
+      up += bf16_to_f32(w.bias[1]);
+      float h;
+      if (a.act == MOE4_ACT_SWIGLU) {
+        h = gt * sigmoidf_(gt) * up;
+      } else {   // comparisons, so that a NaN stays one
+        const float gc = gt > a.limit ? a.limit : gt;
+        const float uc = up > a.limit ? a.limit : up < -a.limit ? -a.limit : up;
+        h = (uc + 1.0f) * gc * sigmoidf_(a.alpha * gc);
+      }
+      // weighted, and rounded once to bf16, the operand type of the second product
+      const int r = entry_first(w.entry) + t;
+      if ((l & 3) == 0) a.h[(int64_t)r * a.I + w.it * 4 * kTiles + tp] = f32_to_bf16(h * row_w[r]);
+    }
+    buf ^= 1;
+  };
+  // (the loads stand before the arithmetic they overlap, in straight line with it)
+  Item w[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) load(w[d]);
+  for (;;) {
+    // (unrolled by hand: the compiler does not unroll a loop that is left from within)
+    auto turn = [&](Item& i) {
+      run(i);
+      __builtin_amdgcn_sched_barrier(0);
+      load(i);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (!w[0].on) return;
+    turn(w[0]);
+    if (!w[1].on) return;
+    turn(w[1]);
+    if constexpr (DEPTH > 2) {
+      if (!w[2].on) return;
+      turn(w[2]);
+    }
+    if constexpr (DEPTH > 3) {
+      if (!w[3].on) return;
+      turn(w[3]);
     }
   }
 }
 
 // ------------------------------------------------------------------ launch 2
 
-// 8 output columns to a workgroup; a unit is one expert (8 of its rows) and one 128-k step of both
-// halves of its k, and wave v takes the units v, v + waves, ... Each wave sums into its own part of
-// LDS, weighted, in its units' order; the parts are added in the waves' order.
-template <int FMT>
-__global__ __launch_bounds__(1024) void k_layer_down(const LayerArgs a) {
+// 8 output columns to a workgroup. A unit is one expert's rows of a group of 8 tokens and a run of its
+// 128-k steps (of both halves of k; 1 KiB of weights each); wave v takes the units v, v + waves, ...,
+// step after step, DEPTH steps ahead of the arithmetic. A token's row of activations stands at the
+// token's place in the MFMA's first operand (zeros where it did not choose the expert), and h is
+// weighted, so a wave's sums over all experts stay in its accumulators, one set for each group. The
+// waves' sums are added in their order.
+template <int FMT, int GROUPS, int DEPTH, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  constexpr int nw = THREADS / 64;
   const int S = a.T * a.k;
-  const int nw = blockDim.x >> 6, wv = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-  // LDS: table | sums [nw][2][T][8] | weights [S] | experts [S] | units [2 S] | their count
-  u32x2* lut = reinterpret_cast<u32x2*>(smem);
-  float* sums = reinterpret_cast<float*>(smem + (FMT == MOE4_FMT_MXFP4 ? 0 : kLutBytes));
-  float* sw = sums + nw * 2 * a.T * 8;
-  int* se = reinterpret_cast<int*>(sw + S);
-  uint32_t* units = reinterpret_cast<uint32_t*>(se + S);
-  __shared__ int s_units;
-  if constexpr (FMT != MOE4_FMT_MXFP4) fill_lut(lut);
-  for (int i = threadIdx.x; i < nw * 2 * a.T * 8; i += blockDim.x) sums[i] = 0.0f;
-  for (int i = threadIdx.x; i < S; i += blockDim.x) {
-    sw[i] = a.w[i];
-    se[i] = a.idx[i];
-  }
-  if (wv == 0) {
-    // experts in the order of their first slots, every 8 rows of one an entry of its own: the
-    // slot, which 8, and how many
-    int base = 0;
-    for (int s0 = 0; s0 < S; s0 += kWave) {
-      const int s = s0 + l, n = s < S ? a.cnt[s] : 0, passes = (n + kRowsPass - 1) / kRowsPass;
-      const int incl = wave_scan_dpp(passes), at = base + incl - passes;
-      for (int p = 0; p < passes; ++p)
-        units[at + p] = (uint32_t)s | (uint32_t)p << 16 | (uint32_t)min(n - p * kRowsPass, kRowsPass) << 24;
-      base += __builtin_amdgcn_readlane(incl, 63);
-    }
-    if (l == 0) s_units = base;
-  }
-  __syncthreads();
-  const int Kh = half_k(a.I), steps = Kh / 128;
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+  // LDS: table | sums [nw][2][8 GROUPS][8] | uses [S]
+  uint8_t* lut = smem;
+  float* sums = reinterpret_cast<float*>(smem + lut_bytes(FMT));
+  Use* uses = reinterpret_cast<Use*>(sums + nw * 2 * GROUPS * 64);
   const int c0 = blockIdx.x * 8;
-  const int m = l & 15, c = m & 7, q = m >> 3, g = l >> 4;
+  const int c = l & 7, q = (l >> 3) & 1, g = l >> 4;
+  const int count = a.count[0];
+  for (int i = threadIdx.x; i < S; i += THREADS)
+    if (i < count) uses[i] = a.uses[i];
+  fill_lut<FMT>(lut);
+  __syncthreads();
+  // the biases' sum of the thread's output
+  float bias = 0.0f;
+  if (a.dn_bias && (int)threadIdx.x < a.T * 8) {
+    const int t = threadIdx.x >> 3, col = c0 + (threadIdx.x & 7);
+    for (int j = 0; j < a.k; ++j) {
+      const int s = t * a.k + j;
+      bias = fmaf(a.w[s], bf16_to_f32(a.dn_bias[(int64_t)a.idx[s] * a.H + col]), bias);
+    }
+  }
+  const int Kh = half_k(a.I), steps = Kh / 128;
   const rsrc_t rh = make_rsrc_uniform(a.h, (uint32_t)(S * a.I * 2));
-  const int total = __builtin_amdgcn_readfirstlane(s_units) * steps;
+  const int total = __builtin_amdgcn_readfirstlane(count) * a.runs;
   const float off = FMT == MOE4_FMT_NF4_DQ ? a.dn.soff[0] : 0.0f;
-  struct Unit {
+  struct Step {
     Piece<FMT> p;
-    Acts x;
-    uint32_t row[4];   // list entries of the lane's four output rows
-    int rows;          // rows of the unit
+    u32x4 x[4];
+    uint32_t tokens;   // of the group that chose the expert, as bits
+    int group;
+    bool second, first, last, on;
   };
-  auto load = [&](Unit& u, int i) {
-    const bool on = i < total;
-    const uint32_t w = __builtin_amdgcn_readfirstlane(units[on ? i / steps : 0]);
-    const int st = on ? i % steps : 0;
-    const int s = w & 0xFFFF, pass = (w >> 16) & 255, n = on ? w >> 24 : 0;
-    const int e = __builtin_amdgcn_readfirstlane(se[s]);
-    const uint32_t* list = a.list + s * kMostT + pass * kRowsPass;
-    const int k = q * Kh + 128 * st;
-    u.rows = n;
-    u.p.load(a.dn, e, c0 + c, on ? k : a.I);
-    const uint32_t mine = c < n ? list[c] : 0;
-    load_acts<FMT>(u.x, rh, c < n ? (int)(mine & 0xFFFF) * a.I * 2 : kOob, k, a.I);
+  // where the loads are: unit, step, the end of its run, the lane's row
+  int at_u = wv, at_s = 0, at_end = 0, group = 0, xoff = kOob;
+  uint32_t tokens = 0;
+  bool fresh = true;
+  Stream<FMT> in;
+  auto open = [&] {
+    const bool on = at_u < total;
+    const int n = !on ? 0 : a.runs == 1 ? at_u : (int)__umulhi((uint32_t)at_u, a.per_run);   // at_u / runs
+    const int run = on ? at_u - n * a.runs : 0;
+    const uint32_t what = __builtin_amdgcn_readfirstlane(uses[n].what);
+    const uint32_t all = on ? __builtin_amdgcn_readfirstlane(uses[n].tokens) : 0u;
+    group = (what >> 10) & 3;
+    at_s = run * a.run_steps;
+    at_end = min(at_s + a.run_steps, steps);
+    fresh = true;
+    in.open(a.dn, what & 1023, c0, on);
+    tokens = all >> (8 * group) & 255u;
+    const int t = 8 * group + c;
+    const int r = (int)(what >> 12) + __popc(all & ((1u << t) - 1));
+    xoff = tokens >> c & 1 ? r * a.I * 2 : kOob;
+  };
+  auto load = [&](Step& u) {
+    u.on = at_u < total;
+    u.group = group;
+    u.tokens = tokens;
+    u.first = fresh;
+    fresh = false;
+    const int k = q * Kh + 128 * at_s;
+    in.place(a.I, c, k);
+    in.load(u.p, a.I, 0);
+    u.second = in.second;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) u.row[r] = 4 * (g & 1) + r < n ? list[4 * (g & 1) + r] : 0;
+    for (int i = 0; i < 4; ++i) {
+      // (MXFP4: the lane's 32 k are in K or not; NF4: a block of 64)
+      const int kk = FMT == MOE4_FMT_MXFP4 ? k + 32 * g : k + 64 * (i / 2);
+      u.x[i] = buf_load_b128(rh, xoff != kOob && kk < a.I ? xoff + 2 * (k + act_k<FMT>(i)) : kOob);
+    }
+    u.last = ++at_s == at_end;
+    if (u.last && u.on) {
+      at_u += nw;
+      open();
+    }
   };
-  auto finish = [&](const Unit& u) {
-    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-    step<FMT>(u.p, u.x, lut, off, a.dn.book, d);
-    if ((g >> 1) == q) {
-      float* mine = sums + (wv * 2 + q) * a.T * 8 + c;
+  f32x4 acc[GROUPS], d;
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto finish = [&](const Step& u) {
+    Acts<FMT> x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.set(i, u.x[i]);
+    if (u.first) d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    step<FMT>(u.p, u.second, x, lut, off, a.dn.book, d);
+    if (u.last) {
+      // (a token that did not choose the expert takes nothing of it: its zeros times an infinite
+      // or NaN weight are no zeros)
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i)
+        if (GROUPS == 1 || u.group == i) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][r] += u.tokens >> (4 * (g & 1) + r) & 1 ? d[r] : 0.0f;
+        }
+    }
+  };
+  Step u[DEPTH];
+  open();
+#pragma unroll
+  for (int j = 0; j < DEPTH; ++j) load(u[j]);
+  while (u[0].on) {
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) {
+      finish(u[j]);   // (a step past the last: zeros)
+      __builtin_amdgcn_sched_barrier(0);
+      load(u[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2
+  if ((g >> 1) == q) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (4 * (g & 1) + r < u.rows)
-          mine[(u.row[r] >> 16) * 8] += sw[u.row[r] & 0xFFFF] * d[r];
-    }
-  };
-  Unit u0, u1;
-  int i = wv;
-  load(u0, i);
-  while (i < total) {
-    load(u1, i + nw);
-    finish(u0);
-    i += nw;
-    if (i >= total) break;
-    load(u0, i + nw);
-    finish(u1);
-    i += nw;
+        sums[(((wv * 2 + q) * GROUPS + i) * 8 + 4 * (g & 1) + r) * 8 + c] = acc[i][r];
   }
   __syncthreads();
-  for (int o = threadIdx.x; o < a.T * 8; o += blockDim.x) {
-    const int t = o >> 3, col = c0 + (o & 7);
-    float v = 0.0f;
-    for (int p = 0; p < 2 * nw; ++p) v += sums[p * a.T * 8 + o];
-    if (a.dn_bias) {
-      for (int j = 0; j < a.k; ++j)
-        v = fmaf(sw[t * a.k + j], bf16_to_f32(a.dn_bias[(int64_t)se[t * a.k + j] * a.H + col]), v);
-    }
+  if ((int)threadIdx.x < a.T * 8) {
+    const int t = threadIdx.x >> 3, col = c0 + (threadIdx.x & 7);
+    float v = bias;
+#pragma unroll
+    for (int p = 0; p < 2 * nw; ++p) v += sums[p * GROUPS * 64 + threadIdx.x];
     const int64_t at = (int64_t)t * a.H + col;
     if (a.residual)
       v += a.res_dtype == MOE4_DTYPE_F32 ? static_cast<const float*>(a.residual)[at]
@@ -492,50 +755,75 @@ __global__ __launch_bounds__(1024) void k_layer_down(const LayerArgs a) {
   }
 }
 
-// Waves that share a workgroup's 128-k steps: as many rounds of them as eight, six or four waves
-// need, whichever leaves fewest idle
-int up_waves(int H) {
-  const int steps = half_k(H) / 128;
-  int best = 8;
-  for (int n : {6, 4})
-    if ((steps + n - 1) / n * n < (steps + best - 1) / best * best) best = n;
-  return best;
-}
-
 struct LayerWs {
-  size_t idx, w, cnt, list, end;
+  size_t idx, w, uses, count, end;
   LayerWs(int I, int T, int k) {
     const size_t S = (size_t)T * k;
     idx = align_up(S * I * 2, 256);
     w = idx + align_up(S * 4, 256);
-    cnt = w + align_up(S * 4, 256);
-    list = cnt + align_up(S * 4, 256);
-    end = list + S * kMostT * 4;
+    uses = w + align_up(S * 4, 256);
+    count = uses + align_up(S * sizeof(Use), 256);
+    end = count + 256;
   }
 };
 
+// dynamic LDS above 64 KiB has to be asked for once per kernel and device
+template <typename K>
+hipError_t allow_lds(K* kernel, int bytes) {
+  return bytes <= 64 * 1024 ? hipSuccess
+                            : hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <int FMT>
-hipError_t launch_layer(const LayerArgs& a, hipStream_t s) {
+hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   const int S = a.T * a.k;
-  const int nw = up_waves(a.H);
-  auto up = [&](auto tc, auto pc) {
-    constexpr int TG = decltype(tc)::value;
-    const int lds = (FMT == MOE4_FMT_MXFP4 ? 0 : kLutBytes) + nw * 2 * TG * 68 * 4;
-    k_layer_up<FMT, TG, decltype(pc)::value><<<S * (a.I / (4 * TG)), nw * 64, lds, s>>>(a);
+  constexpr bool kMx = FMT == MOE4_FMT_MXFP4;
+  // A wave for each 128-k step, up to eight; up to sixteen where all steps then have one.
+  const int steps = half_k(a.H) / 128;
+  const bool big = kMx && a.E <= 128 && steps > 8 && steps <= 16;
+  const int nw = big ? steps : steps < 4 ? 4 : steps < 8 ? steps : 8;
+  const int dsteps = half_k(a.I) / 128;
+  a.runs = (dsteps + 3) / 4;
+  a.run_steps = (dsteps + a.runs - 1) / a.runs;
+  a.runs = (dsteps + a.run_steps - 1) / a.run_steps;
+  a.per_run = (uint32_t)(((uint64_t)1 << 32) / a.runs) + 1;
+  // the workgroups that the chip holds at once, or one for every item
+  const int64_t items = (int64_t)S * (a.I / (4 * kTiles)), room = 256;
+  auto up = [&](auto* k) {
+    const int bytes = lut_bytes(FMT) + 2 * nw * 2 * kTiles * kRed * 4 + route_lds(a.E, S);
+    hipError_t e = allow_lds(k, bytes);
+    if (e != hipSuccess) return e;
+    k<<<(uint32_t)(items < room ? items : room), nw * 64, bytes, s>>>(a);
     return hipGetLastError();
   };
-  using I2 = std::integral_constant<int, 2>;
-  using I16 = std::integral_constant<int, 16>;
-  using I4 = std::integral_constant<int, 4>;
-  using I8 = std::integral_constant<int, 8>;
-  const bool wide = (int64_t)S * (a.I / 32) >= 512;
-  hipError_t e = a.E <= 128 ? (wide ? up(I8{}, I2{}) : up(I4{}, I2{}))
-                            : (wide ? up(I8{}, I16{}) : up(I4{}, I16{}));
+  constexpr int D = kMx ? 4 : FMT == MOE4_FMT_NF4 ? 3 : 2;
+  hipError_t e = hipSuccess;
+  if (big) {
+    if constexpr (kMx) e = up(&k_layer_up<FMT, 2, true, 2, 1024>);
+  } else if (a.E <= 128) {
+    e = steps <= nw ? up(&k_layer_up<FMT, 2, true, D, 512>) : up(&k_layer_up<FMT, 2, false, D, 512>);
+  } else {
+    e = steps <= nw ? up(&k_layer_up<FMT, 16, true, D, 512>) : up(&k_layer_up<FMT, 16, false, D, 512>);
+  }
   if (e != hipSuccess) return e;
-  const int dw = 8;
-  const int lds = (FMT == MOE4_FMT_MXFP4 ? 0 : kLutBytes) + dw * 2 * a.T * 8 * 4 + S * 8 + S * 8;
-  k_layer_down<FMT><<<a.H / 8, dw * 64, lds, s>>>(a);
-  return hipGetLastError();
+  auto down = [&](auto* k, int groups, int threads) {
+    const int bytes = lut_bytes(FMT) + threads / 64 * 2 * groups * 256 + S * (int)sizeof(Use);
+    hipError_t r = allow_lds(k, bytes);
+    if (r != hipSuccess) return r;
+    k<<<a.H / 8, threads, bytes, s>>>(a);
+    return hipGetLastError();
+  };
+  constexpr int DD = kMx ? 4 : 3;
+  auto by_threads = [&](auto gc) {
+    constexpr int G = decltype(gc)::value;
+    if constexpr (FMT != MOE4_FMT_NF4_DQ)
+      if (a.H <= 2048) return down(&k_layer_down<FMT, G, DD, 1024>, G, 1024);
+    return down(&k_layer_down<FMT, G, DD, 512>, G, 512);
+  };
+  if (a.T <= 8) return by_threads(std::integral_constant<int, 1>{});
+  if (a.T <= 16) return by_threads(std::integral_constant<int, 2>{});
+  return by_threads(std::integral_constant<int, 4>{});
 }
 
 }  // namespace
@@ -574,8 +862,8 @@ hipError_t launch_layer_decode(const moe4_experts& ex, const uint16_t* x, const 
   a.h = reinterpret_cast<uint16_t*>(w8);
   a.idx = reinterpret_cast<int32_t*>(w8 + at.idx);
   a.w = reinterpret_cast<float*>(w8 + at.w);
-  a.cnt = reinterpret_cast<int32_t*>(w8 + at.cnt);
-  a.list = reinterpret_cast<uint32_t*>(w8 + at.list);
+  a.uses = reinterpret_cast<Use*>(w8 + at.uses);
+  a.count = reinterpret_cast<int32_t*>(w8 + at.count);
   if (ex.format == MOE4_FMT_NF4) return launch_layer<MOE4_FMT_NF4>(a, s);
   if (ex.format == MOE4_FMT_MXFP4) return launch_layer<MOE4_FMT_MXFP4>(a, s);
   return launch_layer<MOE4_FMT_NF4_DQ>(a, s);
