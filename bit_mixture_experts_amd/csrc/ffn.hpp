@@ -103,31 +103,10 @@ struct FfnProduct {
   float* part;          // [splits][nb][na] sums to be joined
 };
 
-template <typename S, int MA, int MB, bool FP8>
-__device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, int ib, int split,
-                                                 uint8_t* lds) {
-  const int a0 = ia * S::BA, b0 = ib * S::BB;
-  OpLoader<S, MA, S::BA, FP8> la;
-  OpLoader<S, MB, S::BB, FP8> lb;
-  constexpr int es = FP8 ? 1 : 2;
-  const KPart k(p.K, es, split, S::kSplits ? p.splits : 1);
-  if constexpr (MA == kOpRow) {
-    const int n = min(S::BA, p.na - a0);
-    la.init_row(p.A.from_row(k.kt0), es, k.K, a0, n, [=](int r) { return r < n ? r : -1; });
-  } else {
-    la.init_col(p.A.from_col(k.kt0), k.K, a0);
-  }
-  if constexpr (MB == kOpRow) {
-    const int n = min(S::BB, p.nb - b0);
-    lb.init_row(p.B.from_row(k.kt0), es, k.K, b0, n, [=](int r) { return r < n ? r : -1; });
-  } else {
-    lb.init_col(p.B.from_col(k.kt0), k.K, b0);
-  }
-  const MxScales mx = {p.A.s, p.B.s, p.na_s, p.nb_s, p.K / 32, k.kt0 * 4};
-  f32x16 acc[S::TA][S::TB];
-  gemm_loop<S, MA, MB, FP8>(
-      acc, lds, la, lb, k.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
-      [&](int r) { return b0 + r < p.nb ? b0 + r : -1; });
+// The tile's end: its sums go to the part's place, or are finished and stored.
+template <typename S>
+__device__ __forceinline__ void ffn_product_end(const FfnProduct& p, const f32x16 (&acc)[S::TA][S::TB],
+                                                int a0, int b0, int split, uint8_t* lds) {
   if constexpr (S::kSplits) {
     if (p.splits > 1) {
       float* part = p.part + (int64_t)split * p.nb * p.na;
@@ -172,6 +151,34 @@ __device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, in
         }
         store8_dt(p.out, p.out_dtype, (int64_t)b * p.na + c, v);
       });
+}
+
+template <typename S, int MA, int MB, bool FP8>
+__device__ __forceinline__ void ffn_product_tile(const FfnProduct& p, int ia, int ib, int split,
+                                                 uint8_t* lds) {
+  const int a0 = ia * S::BA, b0 = ib * S::BB;
+  OpLoader<S, MA, S::BA, FP8> la;
+  OpLoader<S, MB, S::BB, FP8> lb;
+  constexpr int es = FP8 ? 1 : 2;
+  const KPart k(p.K, es, split, S::kSplits ? p.splits : 1);
+  if constexpr (MA == kOpRow) {
+    const int n = min(S::BA, p.na - a0);
+    la.init_row(p.A.from_row(k.kt0), es, k.K, a0, n, [=](int r) { return r < n ? r : -1; });
+  } else {
+    la.init_col(p.A.from_col(k.kt0), k.K, a0);
+  }
+  if constexpr (MB == kOpRow) {
+    const int n = min(S::BB, p.nb - b0);
+    lb.init_row(p.B.from_row(k.kt0), es, k.K, b0, n, [=](int r) { return r < n ? r : -1; });
+  } else {
+    lb.init_col(p.B.from_col(k.kt0), k.K, b0);
+  }
+  const MxScales mx = {p.A.s, p.B.s, p.na_s, p.nb_s, p.K / 32, k.kt0 * 4};
+  f32x16 acc[S::TA][S::TB];
+  gemm_loop<S, MA, MB, FP8>(
+      acc, lds, la, lb, k.K, mx, [&](int r) { return a0 + r < p.na ? a0 + r : -1; },
+      [&](int r) { return b0 + r < p.nb ? b0 + r : -1; });
+  ffn_product_end<S>(p, acc, a0, b0, split, lds);
 }
 
 template <typename S, int MA, int MB, bool FP8>

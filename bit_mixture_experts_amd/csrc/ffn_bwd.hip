@@ -255,16 +255,6 @@ __global__ __launch_bounds__(256) void k_col_sums(const uint16_t* m, int T, int 
 }
 
 constexpr int kMostGradSplits = 32;
-constexpr int kColParts = 128;
-int col_parts(int T) { return T < kColParts ? (T > 0 ? T : 1) : kColParts; }
-
-hipError_t col_sums(const uint16_t* m, int T, int N, float* part, void* out, int dtype,
-                    hipStream_t s) {
-  const int P = col_parts(T);
-  k_col_sums<<<dim3((N + 511) / 512, P), 256, 0, s>>>(m, T, N, part);
-  hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_sum_rows(part, P, N, out, dtype, s);
-}
 
 template <typename S, int LAYOUT, int ACT>
 hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
@@ -279,6 +269,16 @@ hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+static int col_parts(int T) { return T < kColParts ? (T > 0 ? T : 1) : kColParts; }
+
+hipError_t launch_col_sums(const uint16_t* m, int T, int N, float* part, void* out, int dtype,
+                    hipStream_t s) {
+  const int P = col_parts(T);
+  k_col_sums<<<dim3((N + 511) / 512, P), 256, 0, s>>>(m, T, N, part);
+  hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_sum_rows(part, P, N, out, dtype, s);
+}
 
 // workspace: dGU, h, the partial sums of the two biases' gradients, of dH where it is split along
 // k, and of the products after it: one whose reduction is several times a workgroup's share of
@@ -385,7 +385,7 @@ hipError_t launch_ffn_backward(const moe4_ffn& f, const uint16_t* x, int T, cons
     if (e == hipSuccess && joins) e = launch_join(join, joins, s);
     if (e != hipSuccess) return e;
   }
-  return db_dn ? col_sums(dy, T, H, part_dn, db_dn, dw_dtype, s) : hipSuccess;
+  return db_dn ? launch_col_sums(dy, T, H, part_dn, db_dn, dw_dtype, s) : hipSuccess;
 }
 
 }  // namespace moe4

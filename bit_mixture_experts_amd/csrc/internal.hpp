@@ -117,6 +117,10 @@ hipError_t launch_sum_rows_of(const float* part, int P, int ld, int N, void* out
 // the same with the columns from `cut` on in another output
 hipError_t launch_sum_rows2(const float* part, int P, int N, void* out, int dtype, int cut,
                             void* out2, hipStream_t s);
+// out[c] (of dtype) = sum over the rows of m bf16 [T, N]; part: kColParts x N floats
+constexpr int kColParts = 128;
+hipError_t launch_col_sums(const uint16_t* m, int T, int N, float* part, void* out, int dtype,
+                           hipStream_t s);
 hipError_t launch_add_rmsnorm(const void* x, int x_dtype, const void* res, int res_dtype, void* sum,
                               const void* w, int w_dtype, int T, int H, float eps, uint16_t* out,
                               uint8_t* q, uint8_t* qs, float* rstd, hipStream_t s);
@@ -163,6 +167,13 @@ hipError_t launch_join_norm_backward(const void* dy, int dy_dtype, const void* s
                                      const float* ro, const float* ri, int T, int H, void* db,
                                      void* dres, float* dgate, float* dw_post, float* dw_pre,
                                      void* ws, hipStream_t st);
+size_t linear_ws_bytes(const moe4_linear& l, int64_t T, bool backward);
+hipError_t launch_linear_forward(const moe4_linear& l, const void* x, int x_format,
+                                 const uint8_t* x_s, int T, const void* residual, int res_dtype,
+                                 void* out, int out_dtype, void* ws, int* variant, hipStream_t s);
+hipError_t launch_linear_backward(const moe4_linear& l, const uint16_t* dy, int T,
+                                  const void* dx_add, int add_dtype, void* dx, int dx_dtype,
+                                  void* db, int db_dtype, void* ws, hipStream_t s);
 size_t layer_decode_ws_bytes(const moe4_experts& ex, int T, int k);
 hipError_t launch_layer_decode(const moe4_experts& ex, const uint16_t* x, const float* logits,
                                int T, int k, int renorm, const void* residual, int res_dtype,

@@ -1,0 +1,687 @@
+// The dense product with an MXFP4 weight, y = x W^T + bias + residual, on bf16, MXFP8 or MXFP4
+// activations, and its input gradient dx = dY W.
+//
+// Many tokens: tiles as in dense_gemm.hpp (256 x 256 of eight waves or 128 x 128 of four), the weight
+// as the matrix instruction's first operand.
+//   * MXFP8 and MXFP4 activations: the scaled e2m1 instructions on the codes as they are, 64 k a
+//     step.
+//   * bf16 activations: a lane reads 16 bytes of codes, one block, as the operands of the four
+//     16-k steps of a k-tile (which k a step takes is free as long as both operands agree), and
+//     converts them in registers while the matrix cores are busy: four conversions for two MFMAs
+//     of 32 cycles each.
+//   * dx: the reduction runs over the weight's rows, so the codes are converted once, by the thread
+//     that loads them, and written to LDS as bf16 in the layout of the transposing reads.
+// Few tokens: the weight is streamed once, K split over the waves of a workgroup.
+#include <algorithm>
+
+#include "ffn.hpp"
+
+namespace moe4 {
+namespace {
+
+constexpr int kXB = MOE4_X_BF16, kX8 = MOE4_X_MXFP8, kX4 = MOE4_X_MXFP4;
+
+// k runs in turns of 256, eight blocks of every row, whose scales travel together; a k-tile is 128
+// bytes of a row of activations.
+template <int XF>
+struct LinK {
+  static constexpr int kTile = XF == kXB ? 64 : XF == kX8 ? 128 : 256;   // k of a k-tile
+  static constexpr int kSub = 256 / kTile;                               // k-tiles of a turn
+  static constexpr int kRbA = kTile / 2;                                 // bytes of a weight row
+  static constexpr int kSteps = XF == kX8 ? 2 : 4;
+  // bytes of k values of a row of activations
+  static __host__ __device__ constexpr int64_t bytes(int64_t k) { return k * 128 / kTile; }
+};
+
+// The scales of a turn, eight bytes for each row of the tile, through LDS: thread t of the workgroup
+// reads those of tile row t (A's rows, then B's). Rows start at any byte, so the aligned dwords
+// around them are loaded and shifted. Blocks past K take scale 0: the bytes there belong to the next
+// row and may be e8m0 NaNs.
+template <typename S>
+struct TurnScales {
+  static_assert(S::kThreads == S::BA + S::BB, "a thread for every row");
+  static constexpr int kBytes = S::kThreads * 8;
+  rsrc_t r;
+  int nb;
+  uint32_t off;
+  u32x2 raw;
+  uint32_t more;
+  template <typename RowA, typename RowB>
+  __device__ __forceinline__ void init(const MxScales& m, int blocks, RowA row_a, RowB row_b) {
+    const int t = threadIdx.x;
+    const bool is_a = __builtin_amdgcn_readfirstlane(wave_id()) * 64 < S::BA;   // whole waves
+    r = make_rsrc_uniform(is_a ? m.sa : m.sb, (uint32_t)(((is_a ? m.na : m.nb) + 3) & ~(int64_t)3));
+    nb = blocks;
+    const int row = is_a ? row_a(t) : row_b(t - S::BA);
+    off = row >= 0 ? (uint32_t)row * m.pitch + m.first : (uint32_t)kOob;
+  }
+  __device__ __forceinline__ void load(int turn) {
+    const int at = (int)((off & ~3u) + 8 * turn);
+    raw = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+    more = buf_load_b32(r, at + 8);
+  }
+  __device__ __forceinline__ void store(int turn, uint8_t* lds) const {
+    const int left = nb - 8 * turn;   // blocks of this turn
+    const uint32_t sh = off & 3;
+    u32x2 v = {__builtin_amdgcn_alignbyte(raw[1], raw[0], sh), __builtin_amdgcn_alignbyte(more, raw[1], sh)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = left - 4 * i;
+      v[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+    }
+    reinterpret_cast<u32x2*>(lds)[threadIdx.x] = v;
+  }
+  // of a tile row: the bytes of the lane's half in the turn's four 64-k units
+  static __device__ __forceinline__ uint32_t get(const uint8_t* lds, int row) {
+    const u32x2 v = reinterpret_cast<const u32x2*>(lds)[row];
+    return __builtin_amdgcn_perm(v[1], v[0], lane_id() & 32 ? 0x07050301u : 0x06040200u);
+  }
+};
+
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+
+// one 64-k MFMA of a weight operand (e2m1) with activations in e4m3 or e2m1; the scales are the low
+// bytes
+template <int XF, typename FB>
+__device__ __forceinline__ f32x16 mfma_scaled(i32x4 a, FB b, f32x16 c, uint32_t sa, uint32_t sb) {
+  if constexpr (XF == kX8)
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), b, c, 4, 0, 0, (int)sa, 0, (int)sb);
+  else
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), widen(b), c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+template <typename S, int XF>
+using WLoader = Loader<kOpRow, S::BA, S::kThreads, LinK<XF>::kRbA>;
+template <typename S>
+using XLoader = Loader<kOpRow, S::BB, S::kThreads, 128>;
+
+// The k loop: acc += W x^T. Two stages; a k-tile's loads go out between the MFMAs, part behind the
+// barrier that frees their stage, part at the next tile's beginning; the operands of a step are
+// read from LDS while the step before multiplies.
+template <typename S, int XF, typename RowA, typename RowB>
+__device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* lds, const WLoader<S, XF>& la,
+                                         const XLoader<S>& lb, int K, const MxScales& mx, RowA row_a,
+                                         RowB row_b) {
+  using P = LinK<XF>;
+  constexpr int kA = S::BA * P::kRbA, kStage = kA + S::BB * 128;
+  static_assert(2 * kStage <= S::kLds, "the stages fit");
+  constexpr int kSub = P::kSub, kSteps = P::kSteps;
+  const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+  const int wa = w % S::WA, wb = w / S::WA, r = l & 31, half = l >> 5;
+  const int turns = (K + 255) / 256;
+  // first byte of the lane's row, and the place of its first chunk there
+  const int arow = (wa * S::TA * 32 + r) * P::kRbA, brow = (wb * S::TB * 32 + r) * 128;
+  const int akey = P::kRbA == 128 ? (r >> 1) & 7 : P::kRbA == 64 ? (r >> 2) & 3 : (r >> 3) & 1;
+  const int bkey = (r >> 1) & 7;
+  // weights: 16 bytes of step s (bf16: of the whole k-tile)
+  auto read_a = [&](const uint8_t* st, int t, int s) {
+    const int chunk = XF == kXB ? half : 2 * s + half;
+    return *reinterpret_cast<const i32x4*>(st + arow + t * 32 * P::kRbA + ((chunk ^ akey) * 16));
+  };
+  using FB = std::conditional_t<XF == kX8, i32x8, i32x4>;
+  auto read_b = [&](const uint8_t* st, int t, int s) {
+    const uint8_t* p = st + kA + brow + t * 32 * 128;
+    auto chunk = [&](int c) { return *reinterpret_cast<const i32x4*>(p + ((c ^ bkey) * 16)); };
+    if constexpr (XF == kXB) return chunk(4 * half + s);      // 8 k of the half's block
+    else if constexpr (XF == kX4) return chunk(2 * s + half);  // 32 k
+    else   // k = 32 c + 16 half .. + 15 in the c-th 16 bytes
+      return __builtin_shufflevector(chunk(4 * s + half), chunk(4 * s + 2 + half), 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  i32x4 fa[S::TA];
+  FB fb[2][S::TB];
+  TurnScales<S> sc;
+  uint8_t* const sclds = lds + S::kLds;
+  uint32_t xa[S::TA], xb[S::TB], na[S::TA], nb[S::TB];
+  auto next_scales = [&](int turn) {
+    const uint8_t* p = sclds + (turn & 1) * TurnScales<S>::kBytes;
+#pragma unroll
+    for (int t = 0; t < S::TA; ++t) na[t] = sc.get(p, (wa * S::TA + t) * 32 + r);
+    if constexpr (XF != kXB) {
+#pragma unroll
+      for (int u = 0; u < S::TB; ++u) nb[u] = sc.get(p, S::BA + (wb * S::TB + u) * 32 + r);
+    }
+  };
+  constexpr int kLa = WLoader<S, XF>::kLoads, kLoads = kLa + XLoader<S>::kLoads, kEarly = kLoads / 2;
+  auto issue = [&](int kt, int i0, int i1, uint8_t* st) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < i0 || i >= i1) continue;
+      if (i < kLa) la.template issue<false>(kt, i, st);
+      else lb.template issue<false>(kt, i - kLa, st + kA);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < S::TA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TB; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+
+  sc.init(mx, K / 32, row_a, row_b);
+  sc.load(0);
+  TurnScales<S> first = sc;
+  sc.load(1);
+  issue(0, 0, kLoads, lds);
+  issue(1, 0, kEarly, lds + kStage);
+  wait_vmcnt<kEarly>();
+  first.store(0, sclds);
+  wait_lgkm0();
+  lds_barrier();
+  next_scales(0);
+#pragma unroll
+  for (int t = 0; t < S::TA; ++t) fa[t] = read_a(lds, t, 0);
+#pragma unroll
+  for (int t = 0; t < S::TB; ++t) fb[0][t] = read_b(lds, t, 0);
+  for (int kp = 0; kp < turns; ++kp) {
+#pragma unroll
+    for (int t = 0; t < S::TA; ++t) xa[t] = na[t];
+    if constexpr (XF != kXB) {
+#pragma unroll
+      for (int u = 0; u < S::TB; ++u) xb[u] = nb[u];
+    }
+    sc.store(kp + 1, sclds + ((kp + 1) & 1) * TurnScales<S>::kBytes);
+    sc.load(kp + 2);
+#pragma unroll
+    for (int h = 0; h < kSub; ++h) {
+      const int kt = kp * kSub + h, par = kSub > 1 ? h & 1 : kp & 1;
+      uint8_t* const cur = lds + par * kStage;
+      uint8_t* const nxt = lds + (par ^ 1) * kStage;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const bool last = s == kSteps - 1;
+        const int sn = (s + 1) % kSteps;
+        const uint8_t* from = last ? nxt : cur;
+        if (last) {
+          // the tile's barrier: the wave's loads of the next tile have landed, its reads of this one
+          // are done, and so are the others'
+          wait_vmcnt<0>();
+          wait_lgkm0();
+          lds_barrier();
+          if (h == kSub - 1) next_scales(kp + 1);
+        }
+        // (past the last tile: stale values, read and never used)
+#pragma unroll
+        for (int u = 0; u < S::TB; ++u) fb[(s + 1) & 1][u] = read_b(from, u, sn);
+        const int unit = XF == kXB ? h : h * kSteps + s;   // of the turn's four 64-k units
+        bf16x8 ahead;
+        auto convert = [&](int t) {
+          return __builtin_bit_cast(bf16x8, mx4_bf16x8((uint32_t)fa[t][s], xa[t] >> (8 * unit) & 255u));
+        };
+        if constexpr (XF == kXB) ahead = convert(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < S::TA; ++t) {
+          if constexpr (XF == kXB) {
+            const bf16x8 a = ahead;
+            if (t + 1 < S::TA) ahead = convert(t + 1);
+#pragma unroll
+            for (int u = 0; u < S::TB; ++u)
+              acc[t][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(bf16x8, fb[s & 1][u]),
+                                                                  acc[t][u], 0, 0, 0);
+            if (last) fa[t] = read_a(nxt, t, 0);
+          } else {
+#pragma unroll
+            for (int u = 0; u < S::TB; ++u)
+              acc[t][u] = mfma_scaled<XF>(fa[t], fb[s & 1][u], acc[t][u], xa[t] >> (8 * unit), xb[u] >> (8 * unit));
+            fa[t] = read_a(from, t, sn);
+          }
+          if (last) issue(kt + 2, kEarly * t / S::TA, kEarly * (t + 1) / S::TA, cur);
+          if (s == 0)
+            issue(kt + 1, kEarly + (kLoads - kEarly) * t / S::TA, kEarly + (kLoads - kEarly) * (t + 1) / S::TA, nxt);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  }
+  wait_vmcnt<0>();   // the zeros of the tiles past the last, before the stages are used again
+}
+
+template <typename S>
+constexpr int kLinLds = S::kLds + 2 * TurnScales<S>::kBytes;
+
+// FfnProduct: A the weight (p codes, s scales), B the activations; K in values
+template <typename S, int XF>
+__global__ __launch_bounds__(S::kThreads, 2) void k_linear(const FfnProduct p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
+  const int na = (p.na + S::BA - 1) / S::BA, nb = (p.nb + S::BB - 1) / S::BB;
+  int ia, ib;
+  const int id = xcd_remap(blockIdx.x, gridDim.x), split = id / (na * nb);
+  tile_of(id % (na * nb), na, nb, ia, ib);
+  const int a0 = ia * S::BA, b0 = ib * S::BB;
+  const int n_a = min(S::BA, p.na - a0), n_b = min(S::BB, p.nb - b0);
+  // this part's turns of k
+  const int turns = (p.K + 255) / 256, parts = S::kSplits ? p.splits : 1;
+  const int t0 = (int)((int64_t)turns * split / parts), t1 = (int)((int64_t)turns * (split + 1) / parts);
+  const int K = min(t1 * 256, p.K) - t0 * 256;
+  WLoader<S, XF> la;
+  XLoader<S> lb;
+  const Operand A = {static_cast<const uint8_t*>(p.A.p) + (int64_t)t0 * 128, nullptr, p.K / 2, p.na};
+  const Operand B = {static_cast<const uint8_t*>(p.B.p) + LinK<XF>::bytes(256) * t0, nullptr,
+                     LinK<XF>::bytes(p.K), p.nb};
+  la.init_row(A, 1, K / 2, a0, n_a, [=](int r) { return r < n_a ? r : -1; });
+  lb.init_row(B, 1, (int)LinK<XF>::bytes(K), b0, n_b, [=](int r) { return r < n_b ? r : -1; });
+  const MxScales mx = {p.A.s, p.B.s, p.na_s, p.nb_s, p.K / 32, t0 * 8};
+  f32x16 acc[S::TA][S::TB];
+  lin_loop<S, XF>(
+      acc, stage_mem, la, lb, K, mx, [&](int r) { return r < n_a ? a0 + r : -1; },
+      [&](int r) { return XF != kXB && r < n_b ? b0 + r : -1; });
+  ffn_product_end<S>(p, acc, a0, b0, split, stage_mem);
+}
+
+// --------------------------------------------------------------- gradient
+
+// Weight codes of one k-tile (64 weight rows x BA columns) in registers: 16 bytes, one block, and its
+// scale to a thread.
+template <typename S>
+struct GradCodes {
+  static constexpr int kPer = S::BA / 32;   // threads of a weight row
+  static_assert(64 * kPer == S::kThreads, "a block to a thread");
+  const uint8_t *q, *sc;
+  int K, N;
+  uint32_t off, soff;
+  int lds[4];       // where the thread's four 16-byte pieces of bf16 go
+  bool odd, two;    // and how its dwords are turned so that they follow those places
+  u32x4 w;
+  uint32_t s;
+  __device__ __forceinline__ void init(const void* codes, const uint8_t* scales, int K_, int N_, int col0) {
+    const int n = threadIdx.x / kPer, b = threadIdx.x % kPer;
+    q = static_cast<const uint8_t*>(codes);
+    sc = scales;
+    K = K_;
+    N = N_;
+    const bool on = col0 + 32 * b < K;
+    off = on ? (uint32_t)(n * (K / 2) + col0 / 2 + 16 * b) : (uint32_t)kOob;
+    soff = on ? (uint32_t)(n * (K / 32) + col0 / 32 + b) : (uint32_t)kOob;
+    // Row n of the tile at n * 2 BA, its 64-byte runs b at b ^ (n & 3) (two of the 32-byte units that
+    // the transposing reads swizzle). The pieces of a run are written in an order that differs
+    // between the four lanes of 16 whose runs share the banks.
+    const int turn = kPer == 8 ? ((b >> 2) + 2 * (n & 1)) & 3 : n & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds[i] = n * 2 * S::BA + ((b ^ (n & 3)) * 64) + ((i + turn) & 3) * 16;
+    odd = turn & 1;
+    two = turn & 2;
+  }
+  __device__ __forceinline__ void load(int kt) {
+    const int left = max(min(N - kt * 64, 64), 0);
+    w = buf_load_b128(make_rsrc_uniform(q + (int64_t)kt * 64 * (K / 2), (uint32_t)(left * (K / 2))), (int)off);
+    s = buf_load_u8(make_rsrc_uniform(sc + (int64_t)kt * 64 * (K / 32), (uint32_t)(left * (K / 32))), (int)soff);
+  }
+  // the dwords in the order of their places
+  __device__ __forceinline__ void turn_dwords() {
+    const u32x4 a = {odd ? w[1] : w[0], odd ? w[2] : w[1], odd ? w[3] : w[2], odd ? w[0] : w[3]};
+    w = u32x4{two ? a[2] : a[0], two ? a[3] : a[1], two ? a[0] : a[2], two ? a[1] : a[3]};
+  }
+  __device__ __forceinline__ void store(int i, uint8_t* st) const {
+    *reinterpret_cast<u32x4*>(st + lds[i]) = mx4_bf16x8(w[i], s);
+  }
+};
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, 2) void k_linear_dx(const FfnProduct p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
+  uint8_t* const lds = stage_mem;
+  const int na = (p.na + S::BA - 1) / S::BA, nb = (p.nb + S::BB - 1) / S::BB;
+  int ia, ib;
+  const int id = xcd_remap(blockIdx.x, gridDim.x), split = id / (na * nb);
+  tile_of(id % (na * nb), na, nb, ia, ib);
+  const int a0 = ia * S::BA, b0 = ib * S::BB, n_b = min(S::BB, p.nb - b0);
+  const KPart k(p.K, 2, split, S::kSplits ? p.splits : 1);   // weight rows, 64 to a k-tile
+  const int N = k.K, nk = (N + 63) / 64;
+  constexpr int kA = S::BA * 128, kStage = kA + S::BB * 128;
+  GradCodes<S> ga;
+  ga.init(static_cast<const uint8_t*>(p.A.p) + (int64_t)k.kt0 * 64 * (p.na / 2),
+          p.A.s + (int64_t)k.kt0 * 64 * (p.na / 32), p.na, N, a0);
+  XLoader<S> lb;
+  lb.init_row(p.B.from_row(k.kt0), 2, N, b0, n_b, [=](int r) { return r < n_b ? r : -1; });
+  const int w = __builtin_amdgcn_readfirstlane(wave_id());
+  Reader<kOpCol, S::BA, S::TA, 128> ra;
+  Reader<kOpRow, S::BB, S::TB, 128> rb;
+  ra.init((w % S::WA) * S::TA * 32);
+  rb.init((w / S::WA) * S::TB * 32);
+  f32x16 acc[S::TA][S::TB];
+#pragma unroll
+  for (int i = 0; i < S::TA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TB; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  constexpr int kLoads = XLoader<S>::kLoads, kEarly = kLoads / 2;
+  auto issue = [&](int kt, int i0, int i1, uint8_t* st) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (i >= i0 && i < i1) lb.template issue<true>(kt, i, st + kA);
+  };
+  // codes of the first two k-tiles into LDS, those of the third into registers
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    ga.load(t);
+    ga.turn_dwords();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ga.store(i, lds + t * kStage);
+  }
+  ga.load(2);
+  issue(0, 0, kLoads, lds);
+  issue(1, 0, kEarly, lds + kStage);
+  wait_vmcnt<kEarly>();
+  wait_lgkm0();
+  lds_barrier();
+  bf16x8 fa[S::TA], fb[2][S::TB];
+#pragma unroll
+  for (int t = 0; t < S::TA; ++t) fa[t] = ra.bf16(lds, t, 0);
+#pragma unroll
+  for (int t = 0; t < S::TB; ++t) fb[0][t] = rb.bf16(lds + kA, t, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    uint8_t* const cur = lds + (kt & 1) * kStage;
+    uint8_t* const nxt = lds + ((kt + 1) & 1) * kStage;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const bool last = s == 3;
+      const int sn = (s + 1) & 3;
+      const uint8_t* from = last ? nxt : cur;
+      if (last) {
+        // the tile's barrier: the next tile has landed whole, this one has been read by all
+        wait_vmcnt<0>();
+        wait_lgkm0();
+        lds_barrier();
+        ga.turn_dwords();
+      }
+#pragma unroll
+      for (int u = 0; u < S::TB; ++u) fb[(s + 1) & 1][u] = rb.bf16(from + kA, u, sn);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < S::TA; ++t) {
+#pragma unroll
+        for (int u = 0; u < S::TB; ++u)
+          acc[t][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[t], fb[s & 1][u], acc[t][u], 0, 0, 0);
+        fa[t] = ra.bf16(from, t, sn);
+        if (last) {
+          // the tile after next: its codes (converted here) and part of its activations take the
+          // stage that the barrier freed
+#pragma unroll
+          for (int i = 4 * t / S::TA; i < 4 * (t + 1) / S::TA; ++i) ga.store(i, cur);
+          if (t == S::TA - 1) ga.load(kt + 3);
+          issue(kt + 2, kEarly * t / S::TA, kEarly * (t + 1) / S::TA, cur);
+        }
+        if (s == 0)
+          issue(kt + 1, kEarly + (kLoads - kEarly) * t / S::TA, kEarly + (kLoads - kEarly) * (t + 1) / S::TA, nxt);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  wait_vmcnt<0>();
+  ffn_product_end<S>(p, acc, a0, b0, split, lds);
+}
+
+// ------------------------------------------------------------- few tokens
+
+// One workgroup takes 16 RT weight rows and NT tiles of 16 tokens; its eight waves split K, 128 k
+// (four blocks) a step, and meet in LDS in their order. A lane holds a block of its weight row a
+// step, as the operands of four MFMAs, and its tokens' same 32 k; all are multiplied as bf16
+// (MXFP8 and MXFP4 are exact there). The next batch of steps is in flight while one is multiplied.
+template <int RT, int NT, int XF>
+struct LinSkinny {
+  static constexpr int KS = 8, kThreads = KS * 64;
+  static constexpr int kX = XF == kXB ? 4 : XF == kX8 ? 2 : 1;   // 16-byte loads of a token's step
+  static constexpr int kU = RT + NT * kX > 8 ? 1 : 2;            // steps of a batch
+  static constexpr int kLds = KS * RT * NT * 256 * 4;
+  struct Batch {
+    u32x4 w[kU][RT], x[kU][NT][kX];
+    uint32_t ws[kU][RT], xs[kU][NT];
+  };
+};
+
+template <int RT, int NT, int XF>
+__global__ __launch_bounds__(512) void k_linear_skinny(const FfnProduct p) {
+  using C = LinSkinny<RT, NT, XF>;
+  extern __shared__ __attribute__((aligned(16))) float red[];
+  const int a0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * 16 * NT, nt = min(16 * NT, p.nb - t0);
+  const int ks = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), n = l & 15, g = l >> 4;
+  const int K = p.K, nb = K / 32;
+  const int64_t xb = LinK<XF>::bytes(K);
+  // what the end needs from memory is asked for first: bias and addend of the thread's values
+  constexpr int kAll = 16 * NT * 16 * RT, kTurns = (kAll + 511) / 512;
+  uint32_t bias[kTurns], add[kTurns];
+  const bool add32 = p.add_dtype == MOE4_DTYPE_F32;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int o = i * 512 + threadIdx.x, m = o / (16 * RT), c = o % (16 * RT);
+      if (m < nt && a0 + c < p.na) f(i, m, c, (int64_t)(t0 + m) * p.na + a0 + c);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) bias[i] = add[i] = 0;
+  each([&](int i, int, int c, int64_t at) {
+    if (p.bias) bias[i] = p.bias[a0 + c];
+    if (p.add)
+      add[i] = add32 ? static_cast<const uint32_t*>(p.add)[at] : static_cast<const uint16_t*>(p.add)[at];
+  });
+  const rsrc_t rw = make_rsrc_uniform(p.A.p, (uint32_t)((int64_t)p.na * (K / 2)));
+  const rsrc_t rws = make_rsrc_uniform(p.A.s, (uint32_t)(p.na * nb));
+  const rsrc_t rx = make_rsrc_uniform(static_cast<const uint8_t*>(p.B.p) + t0 * xb, (uint32_t)(nt * xb));
+  const rsrc_t rxs = make_rsrc_uniform(XF == kXB ? p.A.s : p.B.s + (int64_t)t0 * nb, XF == kXB ? 0u : (uint32_t)(nt * nb));
+  uint32_t wo[RT], wso[RT], xo[NT], xso[NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = a0 + 16 * i + n;
+    wo[i] = r < p.na ? (uint32_t)r * (K / 2) + 16 * g : (uint32_t)kOob;
+    wso[i] = r < p.na ? (uint32_t)r * nb + g : (uint32_t)kOob;
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int t = 16 * i + n;
+    xo[i] = t < nt ? (uint32_t)(t * xb) + C::kX * 16 * g : (uint32_t)kOob;
+    xso[i] = t < nt ? (uint32_t)(t * nb + g) : (uint32_t)kOob;
+  }
+  const int steps = (K + 127) / 128, s0 = steps * ks / C::KS, s1 = steps * (ks + 1) / C::KS;
+  auto load = [&](typename C::Batch& b, int s) {
+#pragma unroll
+    for (int i = 0; i < C::kU; ++i) {
+      const int st = s + i;
+      const bool on = st < s1 && 128 * st + 32 * g < K;
+#pragma unroll
+      for (int j = 0; j < RT; ++j) b.w[i][j] = buf_load_b128(rw, on ? (int)(wo[j] + 64 * st) : kOob);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < C::kX; ++c)
+          b.x[i][j][c] = buf_load_b128(rx, on ? (int)(xo[j] + C::kX * 64 * st + 16 * c) : kOob);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) b.ws[i][j] = buf_load_u8(rws, on ? (int)(wso[j] + 4 * st) : kOob);
+      if constexpr (XF != kXB) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b.xs[i][j] = buf_load_u8(rxs, on ? (int)(xso[j] + 4 * st) : kOob);
+      }
+    }
+  };
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto mul = [&](const typename C::Batch& b) {
+#pragma unroll
+    for (int i = 0; i < C::kU; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        bf16x8 x[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const u32x4* v = b.x[i][j];
+          if constexpr (XF == kXB) x[j] = __builtin_bit_cast(bf16x8, v[c]);
+          else if constexpr (XF == kX8) x[j] = mx_bf16x8(v[c / 2][2 * (c % 2)], v[c / 2][2 * (c % 2) + 1], b.xs[i][j]);
+          else x[j] = __builtin_bit_cast(bf16x8, mx4_bf16x8(v[0][c], b.xs[i][j]));
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const bf16x8 w = __builtin_bit_cast(bf16x8, mx4_bf16x8(b.w[i][r][c], b.ws[i][r]));
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[j], acc[r][j], 0, 0, 0);
+        }
+      }
+  };
+  // (a batch that follows is asked for in straight line with the one before it: behind a branch of
+  // its own the compiler would wait for all loads in flight)
+  typename C::Batch b0, b1;
+  int s = s0;
+  load(b0, s);
+  for (;;) {
+    if (s + C::kU >= s1) {
+      mul(b0);
+      break;
+    }
+    load(b1, s + C::kU);
+    mul(b0);
+    s += C::kU;
+    if (s + C::kU >= s1) {
+      mul(b1);
+      break;
+    }
+    load(b0, s + C::kU);
+    mul(b1);
+    s += C::kU;
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<f32x4*>(red + ((ks * RT + i) * NT + j) * 256 + l * 4) = acc[i][j];
+  __syncthreads();
+  each([&](int i, int m, int c, int64_t at) {
+    const int from = ((c >> 4) * NT + (m >> 4)) * 256 + (((c & 15) >> 2) * 16 + (m & 15)) * 4 + (c & 3);
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < C::KS; ++k) v += red[k * RT * NT * 256 + from];
+    v += __uint_as_float(bias[i] << 16);
+    v += __uint_as_float(add32 ? add[i] : add[i] << 16);
+    if (p.out_dtype == MOE4_DTYPE_F32) static_cast<float*>(p.out)[at] = v;
+    else static_cast<uint16_t*>(p.out)[at] = f32_to_bf16(v);
+  });
+}
+
+template <int XF, int NT>
+hipError_t launch_skinny(const FfnProduct& p, hipStream_t s) {
+  auto run = [&](auto rc) {
+    constexpr int RT = decltype(rc)::value;
+    using C = LinSkinny<RT, NT, XF>;
+    auto* k = &k_linear_skinny<RT, NT, XF>;
+    hipError_t e = allow_lds(k, C::kLds);
+    if (e != hipSuccess) return e;
+    k<<<dim3((p.na + 16 * RT - 1) / (16 * RT), (p.nb + 16 * NT - 1) / (16 * NT)), 512, C::kLds, s>>>(p);
+    return hipGetLastError();
+  };
+  // more row tiles save token loads, as long as there is a workgroup for most CUs
+  if (p.na >= 32 * 192) return run(std::integral_constant<int, 2>{});
+  return run(std::integral_constant<int, 1>{});
+}
+
+template <int XF>
+hipError_t launch_tiled(const FfnProduct& p, hipStream_t s) {
+  auto run = [&](auto* k, int64_t tiles, int threads, int bytes) {
+    hipError_t e = allow_lds(k, bytes);
+    if (e != hipSuccess) return e;
+    k<<<(uint32_t)(tiles * p.splits), threads, bytes, s>>>(p);
+    return hipGetLastError();
+  };
+  if (p.splits == 1 && large_tiles_for(p.na, p.nb))
+    return run(&k_linear<Tile256, XF>, tiles_of<Tile256>(p.na, p.nb), Tile256::kThreads, kLinLds<Tile256>);
+  hipError_t e = run(&k_linear<Tile128, XF>, tiles_of<Tile128>(p.na, p.nb), Tile128::kThreads, kLinLds<Tile128>);
+  if (e != hipSuccess || p.splits == 1) return e;
+  JoinArgs j = {};
+  j.p[0] = p;
+  return launch_join(j, 1, s);
+}
+
+// Parts of k for n tiles of 128 x 128 that leave most of a round (512) empty: as many as fill it,
+// each of at least 512 k, 1024 or 2048 (the same time on the matrix cores, which pays for the
+// launch that joins them).
+int lin_splits(int64_t n128, int K, int x_format) {
+  const int64_t turns = (K + 255) / 256, most = 512 / n128;
+  const int64_t s = std::min(most, turns / (x_format == kXB ? 2 : x_format == kX8 ? 4 : 8));
+  return s < 2 ? 1 : (int)std::min<int64_t>(s, kMostSplits);
+}
+
+int linear_variant(const moe4_linear& l, int64_t T) {
+  if (l.variant != MOE4_VARIANT_AUTO) return l.variant;
+  return T <= 32 ? MOE4_VARIANT_SKINNY : MOE4_VARIANT_TILED;
+}
+
+}  // namespace
+
+size_t linear_ws_bytes(const moe4_linear& l, int64_t T, bool backward) {
+  if (!backward) {
+    const int64_t most = (l.N + 127) / 128 > 256 ? 1 : std::min<int64_t>((l.K + 255) / 256 / 2, kMostSplits);
+    return (size_t)part_bytes(l.N, T, most);
+  }
+  return align_up((size_t)part_bytes(l.K, T, most_k_splits(l.K, l.N, 2)), 256) + (size_t)kColParts * l.N * 4;
+}
+
+hipError_t launch_linear_forward(const moe4_linear& l, const void* x, int x_format,
+                                 const uint8_t* x_s, int T, const void* residual, int res_dtype,
+                                 void* out, int out_dtype, void* ws, int* variant, hipStream_t s) {
+  FfnProduct p = {};
+  p.A = {l.w_q, l.w_s, l.K, l.N};
+  p.B = {x, x_s, l.K, T};
+  p.na_s = (int64_t)l.N * (l.K / 32);
+  p.nb_s = x_format == kXB ? 0 : (int64_t)T * (l.K / 32);
+  p.K = l.K;
+  p.na = l.N;
+  p.nb = T;
+  p.bias = l.bias;
+  p.add = residual;
+  p.add_dtype = residual ? res_dtype : MOE4_DTYPE_BF16;
+  p.out = out;
+  p.out_dtype = out_dtype;
+  p.splits = lin_splits(tiles_of<Tile128>(l.N, T), l.K, x_format);
+  p.part = static_cast<float*>(ws);
+  *variant = linear_variant(l, T);
+  auto go = [&](auto fc) {
+    constexpr int XF = decltype(fc)::value;
+    if (*variant == MOE4_VARIANT_TILED) return launch_tiled<XF>(p, s);
+    return T <= 16 ? launch_skinny<XF, 1>(p, s) : launch_skinny<XF, 2>(p, s);
+  };
+  if (x_format == kXB) return go(std::integral_constant<int, kXB>{});
+  if (x_format == kX8) return go(std::integral_constant<int, kX8>{});
+  return go(std::integral_constant<int, kX4>{});
+}
+
+hipError_t launch_linear_backward(const moe4_linear& l, const uint16_t* dy, int T,
+                                  const void* dx_add, int add_dtype, void* dx, int dx_dtype,
+                                  void* db, int db_dtype, void* ws, hipStream_t s) {
+  float* const part = static_cast<float*>(ws);
+  const size_t parts = align_up((size_t)part_bytes(l.K, T, most_k_splits(l.K, l.N, 2)), 256);
+  if (dx) {
+    FfnProduct p = {};
+    p.A = {l.w_q, l.w_s, l.K, l.N};
+    p.B = {dy, nullptr, l.N, T};
+    p.K = l.N;
+    p.na = l.K;
+    p.nb = T;
+    p.add = dx_add;
+    p.add_dtype = dx_add ? add_dtype : MOE4_DTYPE_BF16;
+    p.out = dx;
+    p.out_dtype = dx_dtype;
+    p.splits = k_splits(tiles_of<Tile128>(l.K, T), l.N, 2);
+    p.part = part;
+    auto run = [&](auto* k, int64_t tiles, int threads, int bytes) {
+      hipError_t e = allow_lds(k, bytes);
+      if (e != hipSuccess) return e;
+      k<<<(uint32_t)(tiles * p.splits), threads, bytes, s>>>(p);
+      return hipGetLastError();
+    };
+    hipError_t e = p.splits == 1 && large_tiles_for(l.K, T)
+                       ? run(&k_linear_dx<Tile256>, tiles_of<Tile256>(l.K, T), Tile256::kThreads, Tile256::kLds)
+                       : run(&k_linear_dx<Tile128>, tiles_of<Tile128>(l.K, T), Tile128::kThreads, Tile128::kLds);
+    if (e == hipSuccess && p.splits > 1) {
+      JoinArgs j = {};
+      j.p[0] = p;
+      e = launch_join(j, 1, s);
+    }
+    if (e != hipSuccess) return e;
+  }
+  if (!db) return hipSuccess;
+  return launch_col_sums(dy, T, l.N, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + parts), db, db_dtype, s);
+}
+
+}  // namespace moe4

@@ -1072,6 +1072,104 @@ int moe4_join_norm_backward(const void* dy, int32_t dy_dtype, const void* s, int
       "moe4_join_norm_backward");
 }
 
+static int check_linear(const moe4_linear* l, int32_t T) {
+  if (l == nullptr) return fail(MOE4_EINVAL, "moe4_linear is NULL");
+  if (l->variant != MOE4_VARIANT_AUTO && l->variant != MOE4_VARIANT_SKINNY &&
+      l->variant != MOE4_VARIANT_TILED)
+    return fail(MOE4_EINVAL, "moe4_linear.variant unknown (%d)", l->variant);
+  if (l->N <= 0 || l->N % 8)
+    return fail(MOE4_ESHAPE, "moe4_linear.N = %d is not a positive multiple of 8", l->N);
+  if (l->K <= 0 || l->K % 32)
+    return fail(MOE4_ESHAPE, "moe4_linear.K = %d is not a positive multiple of 32", l->K);
+  if ((int64_t)l->N * l->K / 2 >= kByteSpan)
+    return fail(MOE4_ESHAPE, "moe4_linear: N * K = %lld; the codes must stay under 2 GiB",
+                (long long)l->N * l->K);
+  const int64_t wide = l->N > l->K ? l->N : l->K;
+  if (256 * 4 * wide >= kByteSpan)
+    return fail(MOE4_ESHAPE, "moe4_linear: max(N, K) = %lld; 256 rows must stay under 2 GiB",
+                (long long)wide);
+  REQUIRE_PTR(l->w_q, "moe4_linear.w_q");
+  REQUIRE_PTR(l->w_s, "moe4_linear.w_s");
+  REQUIRE_ALIGN(l->w_q, 16, "moe4_linear.w_q");
+  REQUIRE_ALIGN(l->w_s, 4, "moe4_linear.w_s");
+  REQUIRE_ALIGN(l->bias, 16, "moe4_linear.bias");
+  if (T < 0) return fail(MOE4_ESHAPE, "T = %d is negative", T);
+  if (l->variant == MOE4_VARIANT_SKINNY && T > 1 << 20)
+    return fail(MOE4_ESHAPE, "T = %d: the skinny variant takes at most 2^20 tokens", T);
+  if (T * (wide / 32) >= kByteSpan)
+    return fail(MOE4_ESHAPE, "T = %d: the activations' scales must stay under 2 GiB", T);
+  // workgroups of the smallest tiles, 256 threads each, in one 32-bit launch
+  if (((int64_t)T + 127) / 128 * ((wide + 127) / 128) >= (int64_t)1 << 23)
+    return fail(MOE4_ESHAPE, "T = %d with max(N, K) = %lld is beyond one launch", T, (long long)wide);
+  return MOE4_OK;
+}
+
+size_t moe4_linear_workspace_size(const moe4_linear* l, int32_t T, int32_t backward) {
+  if (check_linear(l, T) != MOE4_OK) return 0;
+  ok();
+  const size_t need = moe4::linear_ws_bytes(*l, T, backward != 0);
+  return need < 256 ? 256 : need;
+}
+
+int moe4_linear_forward(const moe4_linear* l, const void* x, int32_t x_format,
+                        const uint8_t* x_s, int32_t T, const void* residual, int32_t res_dtype,
+                        void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  g_variant = 0;
+  int rc = check_linear(l, T);
+  if (rc) return rc;
+  if (x_format != MOE4_X_BF16 && x_format != MOE4_X_MXFP8 && x_format != MOE4_X_MXFP4)
+    return fail(MOE4_EINVAL, "x_format %s (%d)", x_format ? "unknown" : "unset", x_format);
+  REQUIRE_DTYPE(out_dtype, "out_dtype");
+  if (residual) REQUIRE_DTYPE(res_dtype, "res_dtype");
+  if (x_s && x_format == MOE4_X_BF16) return fail(MOE4_EINVAL, "x_s given for bf16 activations");
+  if (T == 0) return ok();
+  REQUIRE_PTR(x, "x");
+  if (x_format != MOE4_X_BF16) REQUIRE_PTR(x_s, "x_s");
+  REQUIRE_PTR(out, "out");
+  REQUIRE_ALIGN(x, 16, "x");
+  REQUIRE_ALIGN(x_s, 4, "x_s");
+  REQUIRE_ALIGN(residual, 16, "residual");
+  REQUIRE_ALIGN(out, 16, "out");
+  rc = check_ws(ws, ws_bytes, moe4::linear_ws_bytes(*l, T, false), "moe4_linear_forward");
+  if (rc) return rc;
+  int variant = 0;
+  hipError_t e = moe4::launch_linear_forward(*l, x, x_format, x_s, T, residual, res_dtype, out,
+                                             out_dtype, ws, &variant, (hipStream_t)stream);
+  rc = launched(e, "moe4_linear_forward");
+  if (rc == MOE4_OK) g_variant = variant;
+  return rc;
+}
+
+int moe4_linear_backward(const moe4_linear* l, const uint16_t* dy, int32_t T, const void* dx_add,
+                         int32_t add_dtype, void* dx, int32_t dx_dtype, void* db,
+                         int32_t db_dtype, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_linear(l, T);
+  if (rc) return rc;
+  if (dx) REQUIRE_DTYPE(dx_dtype, "dx_dtype");
+  if (dx_add) {
+    if (!dx && T > 0) return fail(MOE4_EINVAL, "dx_add given without dx");
+    REQUIRE_DTYPE(add_dtype, "add_dtype");
+  }
+  if (db) REQUIRE_DTYPE(db_dtype, "db_dtype");
+  if (T > 0 && (dx || db)) REQUIRE_PTR(dy, "dy");
+  REQUIRE_ALIGN(dy, 16, "dy");
+  REQUIRE_ALIGN(dx_add, 16, "dx_add");
+  REQUIRE_ALIGN(dx, 16, "dx");
+  REQUIRE_ALIGN(db, 16, "db");
+  hipStream_t s = (hipStream_t)stream;
+  if (T == 0)   // no token: a zero gradient (by a fill kernel, so that the call can be captured)
+    return db ? launched(moe4::launch_zero_i32(static_cast<int32_t*>(db),
+                                               db_dtype == MOE4_DTYPE_F32 ? l->N : l->N / 2, s),
+                         "moe4_linear_backward")
+              : ok();
+  if (!dx && !db) return ok();
+  rc = check_ws(ws, ws_bytes, moe4::linear_ws_bytes(*l, T, true), "moe4_linear_backward");
+  if (rc) return rc;
+  return launched(moe4::launch_linear_backward(*l, dy, T, dx_add, add_dtype, dx, dx_dtype, db,
+                                               db_dtype, ws, s),
+                  "moe4_linear_backward");
+}
+
 static int check_layer_decode(const moe4_experts* ex, int32_t T, int32_t k) {
   int rc = check_experts(ex);
   if (rc) return rc;

@@ -46,7 +46,8 @@ EXPORTS = ("moe4_quantize_nf4", "moe4_compress_absmax", "moe4_expand_absmax",
            "moe4_ffn_workspace_size", "moe4_grad_norm", "moe4_clip_grads",
            "moe4_grad_workspace_size", "moe4_quantize_mxfp4", "moe4_join_norm",
            "moe4_join_norm_backward", "moe4_join_norm_workspace_size", "moe4_layer_decode",
-           "moe4_layer_decode_workspace_size",
+           "moe4_layer_decode_workspace_size", "moe4_linear_forward", "moe4_linear_backward",
+           "moe4_linear_workspace_size",
            "moe4_workspace_size", "moe4_set_timing_events", "moe4_last_error",
            "moe4_last_variant")
 
@@ -81,9 +82,18 @@ class Moe4Ffn(ctypes.Structure):
     ]
 
 
+class Moe4Linear(ctypes.Structure):
+    """Mirror of the C struct moe4_linear."""
+    _fields_ = [
+        ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("variant", ctypes.c_int32),
+        ("w_q", ctypes.c_void_p), ("w_s", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+    ]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _P = ctypes.POINTER(Moe4Experts)
 _PF = ctypes.POINTER(Moe4Ffn)
+_PL = ctypes.POINTER(Moe4Linear)
 _f32c = ctypes.c_float
 _SIGS = {
     "moe4_quantize_nf4": ([_vp, _i64, _i32, _vp, _vp, _vp], ctypes.c_int),
@@ -128,6 +138,11 @@ _SIGS = {
                                  _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _sz, _vp], ctypes.c_int),
     "moe4_join_norm_workspace_size": ([_i32, _i32], ctypes.c_size_t),
+    "moe4_linear_forward": ([_PL, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _sz, _vp],
+                            ctypes.c_int),
+    "moe4_linear_backward": ([_PL, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _sz, _vp],
+                             ctypes.c_int),
+    "moe4_linear_workspace_size": ([_PL, _i32, _i32], ctypes.c_size_t),
     "moe4_layer_decode": ([_P, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _sz,
                            _vp], ctypes.c_int),
     "moe4_layer_decode_workspace_size": ([_P, _i32, _i32], ctypes.c_size_t),
@@ -844,3 +859,74 @@ def moe4_layer_decode(ex, x, logits, k, out, residual=None, topk_idx=None, topk_
         None if topk_w is None else ptr(topk_w, "topk_w", (T, k), _F32), pw, nw, c.stream(stream))
     if rc:
         _check(rc)
+
+
+class Linear:
+    """Owns references to a dense MXFP4 weight's tensors and the C descriptor (moe4_linear): w_q u8
+    [N, K/32, 16] and w_s [N, K/32] (moe4_quantize_mxfp4), bias bf16 [N]."""
+
+    def __init__(self, w_q, w_s, *, N, K, bias=None, variant=MOE4_VARIANT_AUTO):
+        c = _Call("Linear")
+        _int32("Linear", N=N, K=K)
+        self.tensors = (w_q, w_s, bias)
+        self.desc = Moe4Linear(N=N, K=K, variant=variant,
+                               w_q=c.ptr(w_q, "w_q", (N, K // 32, 16), _U8),
+                               w_s=c.ptr(w_s, "w_s", (N, K // 32), _SCALES),
+                               bias=c.ptr(bias, "bias", (N,), _BF16))
+        self.N, self.K = N, K
+        self.ref = ctypes.byref(self.desc)
+
+    def with_variant(self, variant):
+        d = Moe4Linear()
+        ctypes.pointer(d)[0] = self.desc
+        d.variant = variant
+        out = object.__new__(Linear)
+        out.__dict__.update(self.__dict__)
+        out.desc, out.ref = d, ctypes.byref(d)
+        return out
+
+
+def moe4_linear_workspace_size(lin, T, backward=False):
+    _int32("linear_workspace_size", T=T)
+    n = _lib.moe4_linear_workspace_size(lin.ref, T, int(bool(backward)))
+    if n == 0:
+        raise Moe4Error(MOE4_EINVAL, moe4_last_error())
+    return n
+
+
+def moe4_linear_forward(lin, x, out, x_s=None, residual=None, ws=None, stream=None):
+    """out [T, N] (bf16 or f32) = x W^T + bias + residual (bf16 or f32); x bf16 [T, K], or with
+    scales x_s [T, K/32] MXFP8 codes [T, K] or MXFP4 codes [T, K/32, 16]."""
+    c = _Call("linear_forward")
+    c.place(lin.tensors[0], "w_q")
+    T, K, sh = x.shape[0], lin.K, (x.shape[0], lin.N)
+    if T >> 31:
+        _int32(c.fn, T=T)
+    if x_s is None:
+        fmt, px = MOE4_X_BF16, c.ptr(x, "x", (T, K), _BF16)
+    elif x.dim() == 3:
+        fmt, px = MOE4_X_MXFP4, c.ptr(x, "x", (T, K // 32, 16), _U8)
+    else:
+        fmt, px = MOE4_X_MXFP8, c.ptr(x, "x", (T, K), _CODES)
+    pw, nw = c.ws(ws)
+    rc = _lib.moe4_linear_forward(
+        lin.ref, px, fmt, None if x_s is None else c.ptr(x_s, "x_s", (T, K // 32), _SCALES), T,
+        None if residual is None else c.ptr(residual, "residual", sh, _FLOATS), _dt(residual),
+        c.ptr(out, "out", sh, _FLOATS), _dt(out), pw, nw, c.stream(stream))
+    if rc:
+        _check(rc)
+
+
+def moe4_linear_backward(lin, dy, dx=None, dx_add=None, db=None, ws=None, stream=None):
+    """Gradients of moe4_linear_forward through the frozen weight, from dy bf16 [T, N]: dx [T, K]
+    (bf16 or f32; dx_add is added), db [N] (bf16 or f32); each may be None."""
+    c = _Call("linear_backward")
+    c.place(lin.tensors[0], "w_q")
+    T, sh = dy.shape[0], (dy.shape[0], lin.K)
+    if T >> 31:
+        _int32(c.fn, T=T)
+    pw, nw = c.ws(ws)
+    _check(_lib.moe4_linear_backward(
+        lin.ref, c.ptr(dy, "dy", (T, lin.N), _BF16), T, c.ptr(dx_add, "dx_add", sh, _FLOATS),
+        _dt(dx_add), c.ptr(dx, "dx", sh, _FLOATS), _dt(dx), c.ptr(db, "db", (lin.N,), _FLOATS),
+        _dt(db), pw, nw, c.stream(stream)))

@@ -623,8 +623,59 @@ size_t moe4_grad_workspace_size(int32_t n);
 int moe4_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t R, int64_t K, uint8_t* blocks,
                         uint8_t* scales, uint16_t* values, void* stream);
 
-/* 8- and 4-bit formats of activations (no default) */
+/* format of activations (no default) */
 enum { MOE4_X_BF16 = 1, MOE4_X_MXFP8 = 2, MOE4_X_MXFP4 = 3 };
+
+/*
+ * A dense weight in MXFP4: w_q u8 [N, K/32, 16] and w_s u8 [N, K/32]
+ * (moe4_quantize_mxfp4's, or a released stack's), row n output feature n; bias
+ * bf16 [N] or NULL. variant: MOE4_VARIANT_*; AUTO picks by the number of tokens.
+ * Bounds (else MOE4_ESHAPE): N a positive multiple of 8, K of 32; the codes and
+ * 256 rows of fp32 activations of max(N, K) under 2^31 - 2^24 bytes.
+ * w_q and bias 16-byte aligned, w_s 4.
+ */
+typedef struct moe4_linear {
+  int32_t N, K;
+  int32_t variant;
+  const void* w_q;
+  const uint8_t* w_s;
+  const uint16_t* bias;
+} moe4_linear;
+
+/*
+ * out = x W^T + bias + residual, summed in fp32 on the matrix cores, rounded
+ * once. Weights and activations are exact operands in every kernel; the tiled
+ * kernels' instruction for MXFP8 activations keeps the 32 products of a block
+ * each to 2^-16 of the block's largest. A scale byte 255 (NaN) of a
+ * weight row makes the row's outputs NaN, one of a token's block the token's.
+ *   x [T, K]: bf16, x_s NULL (MOE4_X_BF16); e4m3 codes u8 [T, K] with x_s u8
+ *   [T, K/32] (MXFP8); codes u8 [T, K/32, 16] with x_s u8 [T, K/32] (MXFP4)
+ *   residual [T, N] of res_dtype or NULL; out [T, N] of out_dtype (may be the
+ *   residual where the types are the same)
+ *   ws: at least moe4_linear_workspace_size(l, T, 0) bytes (256-byte aligned)
+ *   x, residual, out 16-byte aligned, x_s 4
+ */
+int moe4_linear_forward(const moe4_linear* l, const void* x, int32_t x_format,
+                        const uint8_t* x_s, int32_t T, const void* residual, int32_t res_dtype,
+                        void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of moe4_linear_forward through the frozen weight:
+ *   dx = dY W (+ dx_add);   db = sum_t dY      (fp32 sums in a fixed order)
+ *   dy bf16 [T, N]; dx [T, K] of dx_dtype; dx_add [T, K] of add_dtype or NULL
+ *   (may be dx where the types are the same); db [N] of db_dtype; dx and db each
+ *   may be NULL and are then not computed; db is zeros for T = 0
+ *   ws: at least moe4_linear_workspace_size(l, T, 1) bytes (256-byte aligned)
+ *   all tensors 16-byte aligned
+ */
+int moe4_linear_backward(const moe4_linear* l, const uint16_t* dy, int32_t T, const void* dx_add,
+                         int32_t add_dtype, void* dx, int32_t dx_dtype, void* db,
+                         int32_t db_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe4_linear_forward (backward == 0) or moe4_linear_backward
+ * at T tokens; 0 if the descriptor or T is invalid. Never less than for fewer
+ * tokens. */
+size_t moe4_linear_workspace_size(const moe4_linear* l, int32_t T, int32_t backward);
 
 /* most tokens, and most routed slots (T * k), of moe4_layer_decode */
 enum { MOE4_LAYER_MOST_TOKENS = 32, MOE4_LAYER_MOST_SLOTS = 512 };

@@ -158,3 +158,88 @@ def test_layer_of_no_tokens_and_workspace():
     assert size(33, 2) == 0 and size(4, 9) == 0 and size(0, 2) >= 256
     sizes = [size(T, 8) for T in range(33)]
     assert sizes == sorted(sizes)
+
+
+# ------------------------------------------------------------------ linear
+
+def _lin(**kw):
+    d = dict(N=64, K=64, variant=moe4.MOE4_VARIANT_AUTO, w_q=P, w_s=P, bias=None)
+    d.update(kw)
+    return ctypes.byref(moe4.Moe4Linear(**d))
+
+
+def _lin_fwd(lin=None, **kw):
+    a = dict(x=P, fmt=moe4.MOE4_X_BF16, xs=None, T=4, res=None, rd=0, out=P, od=BF, ws=P, n=1 << 30)
+    a.update(kw)
+    return lib.moe4_linear_forward(_lin(**(lin or {})), *a.values(), None)
+
+
+def _lin_bwd(lin=None, **kw):
+    a = dict(dy=P, T=4, add=None, ad=0, dx=P, xd=BF, db=P, bd=F32, ws=P, n=1 << 30)
+    a.update(kw)
+    return lib.moe4_linear_backward(_lin(**(lin or {})), *a.values(), None)
+
+
+LINEAR = [
+    (dict(N=0), ESHAPE, "N = 0"), (dict(N=12), ESHAPE, "N = 12"), (dict(K=48), ESHAPE, "K = 48"),
+    (dict(K=-32), ESHAPE, "K = -32"), (dict(N=1 << 16, K=1 << 16), ESHAPE, "under 2 GiB"),
+    (dict(N=1 << 21, K=32), ESHAPE, "256 rows"), (dict(variant=9), EINVAL, "variant unknown"),
+    (dict(w_q=None), EINVAL, "w_q is NULL"), (dict(w_s=None), EINVAL, "w_s is NULL"),
+    (dict(w_q=MIS), EALIGN, "w_q is not"), (dict(w_s=P + 2), EALIGN, "w_s is not"),
+    (dict(bias=MIS), EALIGN, "bias is not"),
+]
+
+
+@pytest.mark.parametrize("lin,code,msg", LINEAR)
+def test_linear_descriptor_refusals(lin, code, msg):
+    refused(_lin_fwd(lin), code, msg)
+    refused(_lin_bwd(lin), code, msg)
+    assert lib.moe4_linear_workspace_size(_lin(**lin), 4, 0) == 0
+    assert lib.moe4_linear_workspace_size(_lin(**lin), 4, 1) == 0
+
+
+def test_linear_without_descriptor():
+    refused(lib.moe4_linear_forward(None, P, 1, None, 4, None, 0, P, BF, P, 1 << 30, None), EINVAL, "moe4_linear is NULL")
+    refused(lib.moe4_linear_backward(None, P, 4, None, 0, P, BF, P, F32, P, 1 << 30, None), EINVAL, "moe4_linear is NULL")
+
+
+@pytest.mark.parametrize("lin,kw,code,msg", [
+    ({}, dict(fmt=0), EINVAL, "x_format unset"), ({}, dict(fmt=4), EINVAL, "x_format unknown"),
+    ({}, dict(od=0), EINVAL, "out_dtype unset"), ({}, dict(res=P, rd=3), EINVAL, "res_dtype unknown"),
+    ({}, dict(xs=P), EINVAL, "x_s given"), ({}, dict(fmt=X8), EINVAL, "x_s is NULL"),
+    ({}, dict(fmt=X4), EINVAL, "x_s is NULL"), ({}, dict(T=-1), ESHAPE, "negative"),
+    ({}, dict(x=None), EINVAL, "x is NULL"), ({}, dict(out=None), EINVAL, "out is NULL"),
+    ({}, dict(x=MIS), EALIGN, "x is not"), ({}, dict(fmt=X8, xs=P + 2), EALIGN, "x_s is not"),
+    ({}, dict(res=MIS, rd=BF), EALIGN, "residual is not"), ({}, dict(out=MIS), EALIGN, "out is not"),
+    (dict(K=4096), dict(ws=None), EWS, "workspace of 0 bytes"), (dict(K=4096), dict(T=64, n=256), EWS, "workspace"),
+    (dict(K=4096), dict(ws=MIS), EALIGN, "256"), (dict(variant=moe4.MOE4_VARIANT_SKINNY), dict(T=(1 << 20) + 1), ESHAPE, "2^20"),
+    (dict(K=1 << 20, N=8), dict(T=1 << 17), ESHAPE, "scales"),
+    (dict(N=1 << 18, K=32), dict(T=1 << 18), ESHAPE, "scales"), (dict(N=8, K=32), dict(T=1 << 30), ESHAPE, "launch"),
+])
+def test_linear_refusals(lin, kw, code, msg):
+    refused(_lin_fwd(lin, **kw), code, msg)
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(xd=0), EINVAL, "dx_dtype unset"), (dict(dx=None, add=P, ad=BF), EINVAL, "dx_add given without dx"),
+    (dict(add=P, ad=5), EINVAL, "add_dtype unknown"), (dict(bd=0), EINVAL, "db_dtype unset"),
+    (dict(dy=None), EINVAL, "dy is NULL"), (dict(dy=MIS), EALIGN, "dy is not"),
+    (dict(add=MIS, ad=BF), EALIGN, "dx_add is not"), (dict(dx=MIS), EALIGN, "dx is not"),
+    (dict(db=MIS), EALIGN, "db is not"), (dict(n=256), EWS, "workspace"), (dict(T=-3), ESHAPE, "negative"),
+])
+def test_linear_backward_refusals(kw, code, msg):
+    refused(_lin_bwd(**kw), code, msg)
+
+
+def test_linear_of_nothing_and_workspace():
+    assert _lin_fwd(T=0, x=None, out=None, ws=None, n=0) == OK
+    assert _lin_bwd(T=0, dy=None, dx=None, db=None, ws=None, n=0) == OK
+    assert _lin_bwd(dy=None, dx=None, db=None, ws=None, n=0) == OK
+    for lin in (dict(), dict(N=264, K=4160), dict(N=8, K=16384), dict(N=16384, K=32), dict(N=4096, K=4096)):
+        for back in (0, 1):   # never less than for fewer tokens
+            last = 0
+            for T in (0, 1, 16, 17, 33, 64, 129, 500, 1000, 4096, 70000):
+                n = lib.moe4_linear_workspace_size(_lin(**lin), T, back)
+                assert n >= max(last, 256)
+                last = n
+    assert lib.moe4_linear_workspace_size(_lin(), -1, 0) == 0
