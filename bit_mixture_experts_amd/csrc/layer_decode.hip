@@ -7,11 +7,12 @@
 // No counter, flag or order of arrival between workgroups decides anything: sums are in a fixed
 // order.
 //
-// Both stream 4-bit weights for a handful of rows. One tile of either is 8 weight rows, each cut
-// into two halves of k, as the 16 columns (c, q) of a 16x16x32 MFMA, against 8 tokens' activations
-// in the same two halves as its 16 rows (t, q'): the products with q = q' are wanted, the others
-// are not read. So a wave's 16-byte loads cover 256 k of 8 rows, a layer's rows give twice the
-// tiles that 16-row tiles would, and no operand is padded to 16 tokens.
+// Both stream 4-bit weights for a handful of rows. One tile of either is 8 weight rows, and a step
+// 256 k of them: its two halves of 128 k as the 16 columns (c, q) of a 16x16x32 MFMA, against 8
+// tokens' activations in the same halves as its 16 rows (t, q'): the products with q = q' are
+// wanted, the others are not read. So a wave's 16-byte loads take whole lines of 128 bytes of 8
+// rows, a layer's rows give twice the tiles that 16-row tiles would, and no operand is padded to 16
+// tokens.
 
 #include <type_traits>
 
@@ -57,10 +58,16 @@ constexpr Nf4Split make_nf4_split() {
 }
 __device__ constexpr Nf4Split kNf4Split = make_nf4_split();
 constexpr int kLutCopies = 32;
-constexpr int lut_bytes(int fmt) { return fmt == MOE4_FMT_MXFP4 ? 0 : 2048 * kLutCopies; }
+// (double-quantised: the codebook of the absmax behind it)
+constexpr int lut_bytes(int fmt) {
+  return fmt == MOE4_FMT_MXFP4 ? 0 : 2048 * kLutCopies + (fmt == MOE4_FMT_NF4_DQ ? 1024 : 0);
+}
 
 template <int FMT>
-__device__ __forceinline__ void fill_lut(uint8_t* lut) {
+__device__ __forceinline__ void fill_lut(uint8_t* lut, const float* book) {
+  if constexpr (FMT == MOE4_FMT_NF4_DQ) {
+    if (threadIdx.x < 256) reinterpret_cast<float*>(lut + 2048 * kLutCopies)[threadIdx.x] = book[threadIdx.x];
+  }
   if constexpr (FMT != MOE4_FMT_MXFP4) {
     // 16 bytes (two copies) at a time, four reads in flight
     constexpr int kAll = 256 * kLutCopies / 2;
@@ -101,26 +108,33 @@ struct Stack {
   int K, rows;
 };
 
-// What one lane holds of a weight row: 16 bytes (32 k), and what scales them: NF4 the absmax of the
-// two blocks of the row's 128-k step, MXFP4 the scale byte of the lane's own block.
-template <int FMT>
-struct Piece {
-  u32x4 w;
-  uint32_t s[FMT == MOE4_FMT_MXFP4 ? 1 : 2];
-  float a2[FMT == MOE4_FMT_NF4_DQ ? 2 : 1];
-};
+constexpr int kStep = 256;   // k of a step: two halves of 128
+__host__ __device__ constexpr int steps_of(int K) { return (K + kStep - 1) / kStep; }
 
 // One expert's matrix from a row on, and a lane's place in it: its row (counted from there) and its
-// 128-k step at k (its own 32 k at k + 32 g). Loads past the matrix or past K give zeros.
+// half of a step. Loads past the matrix or past K give zeros. (A load that is to give zeros everywhere
+// has no scalar offset: the range check subtracts that from the size.)
+//
+// Scales come for a run of four steps at once, those of step g to the lanes of row g of the
+// wave (16 lanes), and are handed to all rows where their step is multiplied: a load of scales costs
+// the memory pipeline as much as one of weights.
 template <int FMT>
 struct Stream {
+  static constexpr bool kMx = FMT == MOE4_FMT_MXFP4, kDq = FMT == MOE4_FMT_NF4_DQ;
   static constexpr int kBlock = Format<FMT>::kBlock, kSb = FMT == MOE4_FMT_NF4 ? 4 : 1;
+  // as loaded: NF4 two absmax; MXFP4 the dwords around the step's four bytes; double-quantised the
+  // two codes, and the blocks' second absmax
+  struct Raw {
+    uint32_t v[2];
+    uint32_t at;   // MXFP4: where the first byte is among them
+    float a2[2];
+  };
   const uint8_t *q, *s;
   const float* s2;
   uint32_t q_bytes, s_bytes;   // from there to the matrix' end
   int first;                   // double-quantised: flat index of its first absmax, mod 256
+  int k0;                      // the lane's first k of a step
   uint32_t vq, vs;
-  bool second;                 // the step's second NF4 block is in K
 
   __device__ __forceinline__ void open(const Stack& st, int e, int row0, bool on) {
     const int nb = st.K / kBlock;
@@ -130,41 +144,83 @@ struct Stream {
     s = static_cast<const uint8_t*>(st.s) + r0 * nb * kSb;
     q_bytes = (uint32_t)left * (uint32_t)(st.K / 2);
     s_bytes = (uint32_t)left * (uint32_t)(nb * kSb);
-    if constexpr (FMT == MOE4_FMT_NF4_DQ) {
+    if constexpr (kDq) {
       s2 = st.s2 + ((r0 * nb) >> 8);
       first = (int)((r0 * nb) & 255);
     }
   }
-  __device__ __forceinline__ void place(int K, int row, int k) {
-    const int kk = k + 32 * (lane_id() >> 4), nb = K / kBlock;
-    vq = kk < K ? (uint32_t)(row * (K / 2) + kk / 2) : (uint32_t)kOob;
-    vs = FMT == MOE4_FMT_MXFP4 ? (kk < K ? (uint32_t)(row * nb + kk / 32) : (uint32_t)kOob)
-                               : (k < K ? (uint32_t)(row * nb + k / 64) * kSb : (uint32_t)kOob);
-    second = k + 64 < K;
+  __device__ __forceinline__ void place(int K, int row, int q_) {
+    k0 = 128 * q_;
+    vq = (uint32_t)(row * (K / 2) + k0 / 2 + 16 * (lane_id() >> 4));
+    vs = (uint32_t)((row * (K / kBlock) + k0 / kBlock) * kSb);
   }
-  // the piece `rows` (uniform) rows further on
-  __device__ __forceinline__ void load(Piece<FMT>& p, int K, int rows) const {
-    const int nb = K / kBlock;
-    const rsrc_t rq = make_rsrc_uniform(q, q_bytes), rs = make_rsrc_uniform(s, s_bytes);
-    // (the rows as the loads' scalar offset: no vector register for each)
-    p.w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)vq, rows * (K / 2), 0));
-    if constexpr (FMT == MOE4_FMT_MXFP4) {
-      p.s[0] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)vs, rows * nb, 0);
-    } else if constexpr (FMT == MOE4_FMT_NF4) {
-      const u32x2 r =
-          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)vs, rows * nb * 4, 0));
-      p.s[0] = r[0];
-      p.s[1] = r[1];
+  // 16 bytes, the lane's 32 k of step st, `rows` (uniform) rows further on
+  __device__ __forceinline__ u32x4 codes(int K, int st, int rows, bool on) const {
+    const rsrc_t r = make_rsrc_uniform(q, on ? q_bytes : 0u);
+    const int at = k0 + kStep * st + 32 * (lane_id() >> 4) < K ? (int)(vq + kStep / 2 * st) : kOob;
+    // (the rows as the load's scalar offset: no vector register for each)
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, on ? rows * (K / 2) : 0, 0));
+  }
+  // the scales of the four steps from st on
+  __device__ __forceinline__ void scales(Raw& p, int K, int st, int rows, bool on) const {
+    const int nb = K / kBlock, k = k0 + kStep * (st + (lane_id() >> 4));
+    const bool in = k < K;
+    if constexpr (kMx) {
+      // They start at any byte: the aligned dwords around them (the last may reach up to 3 bytes past
+      // the scales' end, never past the aligned dword that holds their last byte).
+      const uint64_t from = reinterpret_cast<uint64_t>(s) + (uint32_t)(rows * nb);
+      const int lead = (int)(from & 3);
+      const uint32_t size = on ? (uint32_t)((int)s_bytes - rows * nb + lead + 3) & ~3u : 0u;
+      const rsrc_t r = make_rsrc_uniform(reinterpret_cast<const void*>(from & ~(uint64_t)3), size);
+      const uint32_t at = vs + lead + (st + (lane_id() >> 4)) * 8;
+      const u32x2 v = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, in ? (int)(at & ~3u) : kOob, 0, 0));
+      p.v[0] = v[0];
+      p.v[1] = v[1];
+      p.at = at & 3;
+    } else if constexpr (!kDq) {
+      const rsrc_t r = make_rsrc_uniform(s, on ? s_bytes : 0u);
+      const u32x2 v = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                     r, in ? (int)(vs + (st + (lane_id() >> 4)) * 16) : kOob, on ? rows * nb * 4 : 0, 0));
+      p.v[0] = v[0];
+      p.v[1] = v[1];
     } else {
-      const int at = (int)(vs + (uint32_t)(rows * nb));
-      p.s[0] = buf_load_u8(rs, at);
-      p.s[1] = buf_load_u8(rs, second ? at + 1 : kOob);
-      const bool on = (uint32_t)at < s_bytes;
-      p.a2[0] = s2[on ? (first + at) >> 8 : 0];
-      p.a2[1] = s2[on && second ? (first + at + 1) >> 8 : 0];
+      const rsrc_t r = make_rsrc_uniform(s, on ? s_bytes : 0u);
+      const int at = (int)(vs + (st + (lane_id() >> 4)) * 4 + rows * nb);
+      const bool here = on && in && (uint32_t)at < s_bytes, both = here && k + 64 < K;
+      p.v[0] = buf_load_u8(r, here ? at : kOob);
+      p.v[1] = buf_load_u8(r, both ? at + 1 : kOob);
+      p.a2[0] = s2[here ? (first + at) >> 8 : 0];
+      p.a2[1] = s2[both ? (first + at + 1) >> 8 : 0];
+    }
+  }
+  // them as they multiply: NF4 two fp32, MXFP4 four bytes; 0 past K (what was loaded there belongs to
+  // the next row)
+  __device__ __forceinline__ void finish(Raw& p, int K, int st, const float* book, float off) const {
+    const int k = k0 + kStep * (st + (lane_id() >> 4));
+    if constexpr (kMx) {
+      const int left = (K - k) / 32;
+      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+      p.v[0] = __builtin_amdgcn_alignbyte(p.v[1], p.v[0], p.at) & keep;
+    } else {
+      if constexpr (kDq) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          p.v[i] = __float_as_uint(mul_then_add(book[p.v[i]], p.a2[i], off));
+        if (k >= K) p.v[0] = 0u;
+      }
+      if (k + 64 >= K) p.v[1] = 0u;
     }
   }
 };
+// the value that the lanes of row S of the wave hold, in all of them
+template <int S>
+__device__ __forceinline__ uint32_t from_row(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(a[S / 2], a[S / 2], false, false);
+  return b[S % 2];
+}
 
 // The activations of one lane for a 128-k step as MFMA operands. MXFP4: four, of the lane's own 32
 // k. NF4: each operand serves two bytes of codes, {high, low parts} of each, so it holds their two
@@ -197,42 +253,65 @@ __device__ __forceinline__ void load_acts(Acts<FMT>& x, rsrc_t r, int off, int k
   }
 }
 
-// acc += one step's products. MXFP4: the lane's 32 k are one block, each weight exact in bf16. NF4:
-// the codes are put in MFMA order, so that two dwords of a lane make a block.
-template <int FMT>
-__device__ __forceinline__ void step(const Piece<FMT>& p, bool second, const Acts<FMT>& x,
-                                     const uint8_t* lut, float off, const float* book, f32x4& acc) {
+// acc += one step's products of TT tiles; s0, s1: their scales (NF4 two fp32, MXFP4 the four bytes in
+// s0). MXFP4: the lane's 32 k are one block, each weight exact in bf16. NF4: the codes are put in
+// MFMA order, so that two dwords of a lane make a block; lookups run ahead of the MFMAs that take
+// them, by as much as covers LDS' latency, and the two blocks and the tiles take turns, so that no
+// MFMA waits for the one before it. (Left to the compiler, which looked four bytes up, waited and
+// multiplied, the first launch took 59 us for 16 tokens through
+// 81 of 128 experts of 2048 x 768, and takes 53 so.)
+template <int FMT, int TT>
+__device__ __forceinline__ void step(const u32x4 (&codes)[TT], const uint32_t (&s0)[TT], const uint32_t (&s1)[TT],
+                                     const Acts<FMT>& x, const uint8_t* lut, f32x4 (&acc)[TT]) {
   if constexpr (FMT == MOE4_FMT_MXFP4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          __builtin_bit_cast(bf16x8, x.v[i]), __builtin_bit_cast(bf16x8, mx4_bf16x8(p.w[i], p.s[0])),
-          acc, 0, 0, 0);
-  } else {
-    const u32x4 w = transpose4(p.w);
-    const uint32_t lane8 = 8 * (lane_id() & (kLutCopies - 1));
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 4 * b; i < 4 * b + 4; ++i) {
-        const u32x2 v0 = lookup(lut, w[i / 2], 2 * (i & 1), lane8);
-        const u32x2 v1 = lookup(lut, w[i / 2], 2 * (i & 1) + 1, lane8);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+      for (int j = 0; j < TT; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
             __builtin_bit_cast(bf16x8, x.v[i]),
-            __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3)), d, 0, 0, 0);
-      }
-      float s;
-      if constexpr (FMT == MOE4_FMT_NF4) s = b && !second ? 0.0f : __uint_as_float(p.s[b]);
-      else s = mul_then_add(book[p.s[b]], p.a2[b], off);
+            __builtin_bit_cast(bf16x8, mx4_bf16x8(codes[j][i], s0[j] >> (8 * (lane_id() >> 4)) & 255u)), acc[j], 0, 0, 0);
+  } else {
+    constexpr int kAhead = TT >= 4 ? 1 : 4 / TT;
+    const uint32_t lane8 = 8 * (lane_id() & (kLutCopies - 1));
+    u32x4 w[TT];
+    u32x2 v[kAhead + 1][TT][2];
+    f32x4 d[TT][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, d[i], acc[i]);
+    for (int j = 0; j < TT; ++j) {
+      w[j] = transpose4(codes[j]);
+      d[j][0] = d[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    auto look = [&](int m) {   // block m % 2, its (m / 2)-th pair of bytes
+      const int i = 4 * (m & 1) + m / 2;
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[m % (kAhead + 1)][j][h] = lookup(lut, w[j][i / 2], 2 * (i & 1) + h, lane8);
+    };
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m) look(m);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      if (m + kAhead < 8) look(m + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const u32x2* e = v[m % (kAhead + 1)][j];
+        d[j][m & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, x.v[4 * (m & 1) + m / 2]),
+            __builtin_bit_cast(bf16x8, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3)), d[j][m & 1], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[j][i] = fmaf(__uint_as_float(s1[j]), d[j][1][i], fmaf(__uint_as_float(s0[j]), d[j][0][i], acc[j][i]));
   }
 }
-
-// first k of the second half of a row: a multiple of 128, so that steps and blocks stay whole
-__host__ __device__ constexpr int half_k(int K) { return (K + 255) / 256 * 128; }
 
 // ------------------------------------------------------------------ launch 1
 
@@ -264,7 +343,7 @@ struct LayerArgs {
   int out_dtype;
   int32_t* user_idx;
   float* user_w;
-  // runs of 128-k steps of the second launch: how many, of how many, 2^32 / runs plus one
+  // runs of steps of the second launch: how many, of how many, 2^32 / runs plus one
   int runs, run_steps;
   uint32_t per_run;
   // workspace
@@ -332,25 +411,25 @@ struct Keys {
   }
 };
 
-// 4 gate/up pairs to a tile, kTiles tiles to an item; the items of all entries are dealt to the
-// workgroups in equal runs. Wave v takes the 128-k step v (ONE: there are no more steps than waves)
-// of both halves of k for all items, so its activations stay in registers and its loads are
-// weights, DEPTH items ahead of the arithmetic.
-constexpr int kTiles = 4;
-constexpr int kRed = 68;   // floats of a tile's sums [8 rows][8 tokens], padded
+// A tile is 4 gate/up pairs (gates are its rows 0..3, ups 4..7). The tiles of all entries are dealt to
+// all waves in equal runs, and a wave takes its run by itself, up to four tiles of an entry at a
+// time over all of k: the activations' operands serve all four, and no wave waits for another
+// after the routing. (The waves of a workgroup splitting k of the same tiles, with a barrier
+// and a sum through LDS for each 16 pairs, took as
+// long for many tokens and 2 us more for one.)
 
-// LDS of the first launch, after the table and the sums: tokens of an expert [E] as bits, its first
+// LDS of the first launch, after the table: tokens of an expert [E] as bits, its first
 // row [E], entries [S], tokens and weights of the rows [S], experts and weights of the slots [S]
 __host__ __device__ constexpr int route_lds(int E, int S) { return 8 * E + 20 * S; }
 
-template <int FMT, int NPL, bool ONE, int DEPTH, int THREADS>
-__global__ __launch_bounds__(THREADS) void k_layer_up(const LayerArgs a) {
+template <int FMT, int NPL>
+__global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int nw = blockDim.x >> 6, wv = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+  constexpr int nw = 8;
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
   const int S = a.T * a.k;
   uint8_t* lut = smem;
-  float* red = reinterpret_cast<float*>(smem + lut_bytes(FMT));
-  uint32_t* chose = reinterpret_cast<uint32_t*>(red + 2 * nw * 2 * kTiles * kRed);
+  uint32_t* chose = reinterpret_cast<uint32_t*>(smem + lut_bytes(FMT));
   int* base = reinterpret_cast<int*>(chose + a.E);
   uint32_t* entries = reinterpret_cast<uint32_t*>(base + a.E);
   int* row_t = reinterpret_cast<int*>(entries + S);
@@ -358,7 +437,7 @@ __global__ __launch_bounds__(THREADS) void k_layer_up(const LayerArgs a) {
   int* slot_e = reinterpret_cast<int*>(row_w + S);
   float* slot_w = reinterpret_cast<float*>(slot_e + S);
   __shared__ int s_count;
-  const int Kh = half_k(a.H), steps = Kh / 128;
+  const int steps = steps_of(a.H);
   const int c = l & 7, q = (l >> 3) & 1, g = l >> 4;   // a weight column (c, q), an activation row (t, q)
   const bool writer = blockIdx.x == 0;                 // hands the routing on
 
@@ -426,13 +505,13 @@ __global__ __launch_bounds__(THREADS) void k_layer_up(const LayerArgs a) {
         if (writer) a.count[0] = a.k;
       }
     }
-    fill_lut<FMT>(lut);
+    fill_lut<FMT>(lut, a.gu.book);
     __syncthreads();
   } else {
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) chose[i] = 0;
     __syncthreads();
     for (int t = wv; t < a.T; t += nw) route(t);
-    fill_lut<FMT>(lut);
+    fill_lut<FMT>(lut, a.gu.book);
     __syncthreads();
     if (wv == 0) {
       int rows = 0, count = 0, uses = 0;
@@ -475,101 +554,98 @@ __global__ __launch_bounds__(THREADS) void k_layer_up(const LayerArgs a) {
   }
   const int count = __builtin_amdgcn_readfirstlane(s_count);
 
-  // ---- this workgroup's run of items: 16 pairs from 16 it on of an entry's expert, for !ONE in
-  // rounds of the 128-k steps; gates are columns 0..3 of a tile, ups 4..7
-  const int items = a.I / (4 * kTiles), rounds = ONE ? 1 : (steps + nw - 1) / nw;
-  const int all = count * items;
-  const int first = (int)((int64_t)all * blockIdx.x / gridDim.x), end = (int)((int64_t)all * (blockIdx.x + 1) / gridDim.x);
-  if (first >= end) return;
+  // ---- this wave's run of tiles
+  const int per = a.I / 4, all = count * per, wid = blockIdx.x * nw + wv, waves = gridDim.x * nw;
+  const int first = (int)((int64_t)all * wid / waves), end = (int)((int64_t)all * (wid + 1) / waves);
   const int mult = a.layout == MOE4_GU_HALVES ? 1 : 2;
-  const int row = c < 4 ? gate_row(a.layout, a.I, c & 3) : up_row(a.layout, a.I, c & 3);
   const rsrc_t rx = make_rsrc_uniform(a.x, (uint32_t)(a.T * a.H * 2));
+  const float* book = FMT == MOE4_FMT_NF4_DQ ? reinterpret_cast<const float*>(lut + 2048 * kLutCopies) : nullptr;
   const float off = FMT == MOE4_FMT_NF4_DQ ? a.gu.soff[0] : 0.0f;
-  const int tp = (threadIdx.x >> 2) & (4 * kTiles - 1);   // the pair of an item that the thread finishes
-  struct Item {
-    Piece<FMT> p[kTiles];
-    uint32_t bias[2];
-    uint32_t entry;
-    int it, rd;
-    bool on, second;
-  };
-  // where the loads are: entry, item, round
-  int at_n = first, at_e = first / items, at_i = first % items, at_r = 0;
-  uint32_t at = __builtin_amdgcn_readfirstlane(entries[at_e]);
   Stream<FMT> in;
-  in.place(a.H, row, q * Kh + 128 * wv);
-  auto load = [&](Item& w) {
-    const int st = wv + at_r * nw;
-    w.on = at_n < end;
-    w.entry = at;
-    w.it = at_i;
-    w.rd = at_r;
-    const bool on = w.on && st < steps;
-    in.open(a.gu, entry_expert(at), on ? at_i * 4 * kTiles * mult : 0, on);
-    if (!ONE) in.place(a.H, row, q * Kh + 128 * st);
-    w.second = in.second;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) in.load(w.p[j], a.H, 4 * j * mult);
+  in.place(a.H, c < 4 ? gate_row(a.layout, a.I, c & 3) : up_row(a.layout, a.I, c & 3), q);
+  // TT tiles (n of them there) from tile j0 of an entry on
+  auto run = [&](auto tc, uint32_t entry, int j0, int n) {
+    constexpr int TT = decltype(tc)::value;
+    constexpr int kDepth = TT > 2 ? 2 : 4;   // steps in flight
+    const int rows = entry_rows(entry);
+    in.open(a.gu, entry_expert(entry), 4 * j0 * mult, true);
+    const int xoff = c < rows ? row_t[entry_first(entry) + c] * a.H * 2 + 2 * in.k0 : kOob;
+    // the lane's tile, pair and tokens at the end: tile 2 (g / 2) + q, pair c & 3 (gates in lanes c < 4),
+    // tokens 4 (g % 2) ...
+    const int mj = 2 * (g >> 1) + q, pair = 4 * (j0 + mj) + (c & 3);
+    uint32_t bias = 0;
     if (a.gu_bias) {
-      const rsrc_t rb = make_rsrc_uniform(a.gu_bias + (int64_t)entry_expert(at) * 2 * a.I, w.on ? 4 * a.I : 0);
-      const int pair = at_i * 4 * kTiles + tp;
-      w.bias[0] = __builtin_amdgcn_raw_buffer_load_b16(rb, 2 * gate_row(a.layout, a.I, pair), 0, 0);
-      w.bias[1] = __builtin_amdgcn_raw_buffer_load_b16(rb, 2 * up_row(a.layout, a.I, pair), 0, 0);
-    } else {
-      w.bias[0] = w.bias[1] = 0;
+      const rsrc_t rb = make_rsrc_uniform(a.gu_bias + (int64_t)entry_expert(entry) * 2 * a.I, 4 * a.I);
+      const int at = c < 4 ? gate_row(a.layout, a.I, pair) : up_row(a.layout, a.I, pair);
+      bias = __builtin_amdgcn_raw_buffer_load_b16(rb, mj < n ? 2 * at : kOob, 0, 0);
     }
-    if (!ONE && ++at_r < rounds) return;
-    at_r = 0;
-    ++at_n;
-    if (++at_i == items) {
-      at_i = 0;
-      ++at_e;
-      at = __builtin_amdgcn_readfirstlane(entries[min(at_e, count - 1)]);
-    }
-  };
-  Acts<FMT> x;
-  f32x4 acc[kTiles];
-  uint32_t have = ~0u;   // the entry whose rows x holds
-  int buf = 0;
-  auto run = [&](const Item& w) {
-    if (!ONE || w.entry != have) {
-      const int st = wv + w.rd * nw;
-      const int xoff = c < entry_rows(w.entry) && st < steps ? row_t[entry_first(w.entry) + c] * a.H * 2 : kOob;
-      load_acts<FMT>(x, rx, xoff, q * Kh + 128 * st, a.H);
-      have = w.entry;
-    }
-    if (w.rd == 0) {
+    u32x4 w[kDepth][TT], xr[kDepth][4];
+    typename Stream<FMT>::Raw sc[TT], next[TT];
+    auto load = [&](int d, int st) {
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+      for (int j = 0; j < TT; ++j) w[d][j] = in.codes(a.H, st, 4 * j * mult, j < n);
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) step<FMT>(w.p[j], w.second, x, lut, off, a.gu.book, acc[j]);
-    if (w.rd + 1 < rounds) return;
-    // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2
-    if ((g >> 1) == q) {
-      float* mine = red + ((buf * nw + wv) * 2 + q) * kTiles * kRed + c * 8 + 4 * (g & 1);
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j) *reinterpret_cast<f32x4*>(mine + j * kRed) = acc[j];
-    }
-    // One barrier an item: the sums of the item after next go to the buffer read here. (Not
-    // __syncthreads, which would wait for the loads in flight.)
-    wait_lgkm0();
-    lds_barrier();
-    // four threads a pair, a wave a row
-    for (int t = wv; t < entry_rows(w.entry); t += nw) {
-      const float* s = red + (buf * nw * 2 + (l & 3)) * kTiles * kRed + (tp / 4) * kRed + (tp & 3) * 8 + t;
-      float gt = 0.0f, up = 0.0f;
-#pragma unroll 4
-      for (int v = l & 3; v < 2 * nw; v += 4, s += 4 * kTiles * kRed) {
-        gt += s[0];
-        up += s[32];
+      for (int i = 0; i < 4; ++i) {
+        const int k = kStep * st + act_k<FMT>(i);
+        xr[d][i] = buf_load_b128(rx, xoff != kOob && in.k0 + k < a.H ? xoff + 2 * k : kOob);
       }
-      gt += dpp_f32<0xB1>(gt);   // the quad's sums, in every lane of it
-      gt += dpp_f32<0x4E>(gt);
-      up += dpp_f32<0xB1>(up);
-      up += dpp_f32<0x4E>(up);
-      gt += bf16_to_f32(w.bias[0]);
-      up += bf16_to_f32(w.bias[1]);
+    };
+    f32x4 acc[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      in.scales(next[j], a.H, 0, 4 * j * mult, j < n);
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(d, d);
+    for (int s0 = 0; s0 < steps; s0 += 4) {
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        sc[j] = next[j];
+        in.finish(sc[j], a.H, s0, book, off);
+        in.scales(next[j], a.H, s0 + 4, 4 * j * mult, j < n);
+      }
+      auto one = [&](auto ic) {   // (steps past the last: zeros)
+        constexpr int i = decltype(ic)::value, d = i % kDepth;
+        Acts<FMT> x;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x.set(v, xr[d][v]);
+        uint32_t lo[TT], hi[TT];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          lo[j] = from_row<i>(sc[j].v[0]);
+          hi[j] = FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i>(sc[j].v[1]);
+        }
+        step<FMT, TT>(w[d], lo, hi, x, lut, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        load(d, s0 + i + kDepth);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      one(std::integral_constant<int, 0>{});
+      one(std::integral_constant<int, 1>{});
+      one(std::integral_constant<int, 2>{});
+      one(std::integral_constant<int, 3>{});
+    }
+    // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2. The halves' sum of
+    // tile mj to the lanes of mj.
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const uint32_t b = __float_as_uint(acc[j][r]);
+        const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);   // tokens' first, second half
+        const float own = __uint_as_float(q ? h[1] : h[0]);
+        const float sum = own + dpp_f32<0x128>(own);   // row_ror:8
+        v[r] = j == 0 || mj == j ? sum : v[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r >= rows) break;
+      const int t = 4 * (g & 1) + r;
+      const float u = v[r] + bf16_to_f32(bias);
+      const float gt = u, up = dpp_f32<0x104>(u);   // row_shl:4: lane c takes c + 4's
       float h;
       if (a.act == MOE4_ACT_SWIGLU) {
         h = gt * sigmoidf_(gt) * up;
@@ -579,42 +655,34 @@ __global__ __launch_bounds__(THREADS) void k_layer_up(const LayerArgs a) {
         h = (uc + 1.0f) * gc * sigmoidf_(a.alpha * gc);
       }
       // weighted, and rounded once to bf16, the operand type of the second product
-      const int r = entry_first(w.entry) + t;
-      if ((l & 3) == 0) a.h[(int64_t)r * a.I + w.it * 4 * kTiles + tp] = f32_to_bf16(h * row_w[r]);
+      if (c < 4 && t < rows && mj < n) {
+        const int at = entry_first(entry) + t;
+        a.h[(int64_t)at * a.I + pair] = f32_to_bf16(h * row_w[at]);
+      }
     }
-    buf ^= 1;
   };
-  // (the loads stand before the arithmetic they overlap, in straight line with it)
-  Item w[DEPTH];
-#pragma unroll
-  for (int d = 0; d < DEPTH; ++d) load(w[d]);
-  for (;;) {
-    // (unrolled by hand: the compiler does not unroll a loop that is left from within)
-    auto turn = [&](Item& i) {
-      run(i);
-      __builtin_amdgcn_sched_barrier(0);
-      load(i);
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    if (!w[0].on) return;
-    turn(w[0]);
-    if (!w[1].on) return;
-    turn(w[1]);
-    if constexpr (DEPTH > 2) {
-      if (!w[2].on) return;
-      turn(w[2]);
+  // (double-quantised scales take more registers: two tiles at a time)
+  constexpr int kMost = FMT == MOE4_FMT_NF4_DQ ? 2 : 4;
+  for (int at = first; at < end;) {
+    const int e = at / per, j0 = at - e * per, n = min(min(end - at, per - j0), kMost);
+    const uint32_t entry = __builtin_amdgcn_readfirstlane(entries[e]);
+    if constexpr (kMost == 4) {
+      if (n > 2) {
+        run(std::integral_constant<int, 4>{}, entry, j0, n);
+        at += n;
+        continue;
+      }
     }
-    if constexpr (DEPTH > 3) {
-      if (!w[3].on) return;
-      turn(w[3]);
-    }
+    if (n == 2) run(std::integral_constant<int, 2>{}, entry, j0, n);
+    else run(std::integral_constant<int, 1>{}, entry, j0, n);
+    at += n;
   }
 }
 
 // ------------------------------------------------------------------ launch 2
 
 // 8 output columns to a workgroup. A unit is one expert's rows of a group of 8 tokens and a run of its
-// 128-k steps (of both halves of k; 1 KiB of weights each); wave v takes the units v, v + waves, ...,
+// steps (1 KiB of weights each); wave v takes the units v, v + waves, ...,
 // step after step, DEPTH steps ahead of the arithmetic. A token's row of activations stands at the
 // token's place in the MFMA's first operand (zeros where it did not choose the expert), and h is
 // weighted, so a wave's sums over all experts stay in its accumulators, one set for each group. The
@@ -634,7 +702,7 @@ __global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
   const int count = a.count[0];
   for (int i = threadIdx.x; i < S; i += THREADS)
     if (i < count) uses[i] = a.uses[i];
-  fill_lut<FMT>(lut);
+  fill_lut<FMT>(lut, a.dn.book);
   __syncthreads();
   // the biases' sum of the thread's output
   float bias = 0.0f;
@@ -645,22 +713,25 @@ __global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
       bias = fmaf(a.w[s], bf16_to_f32(a.dn_bias[(int64_t)a.idx[s] * a.H + col]), bias);
     }
   }
-  const int Kh = half_k(a.I), steps = Kh / 128;
+  const int steps = steps_of(a.I);
   const rsrc_t rh = make_rsrc_uniform(a.h, (uint32_t)(S * a.I * 2));
   const int total = __builtin_amdgcn_readfirstlane(count) * a.runs;
   const float off = FMT == MOE4_FMT_NF4_DQ ? a.dn.soff[0] : 0.0f;
+  const float* book = FMT == MOE4_FMT_NF4_DQ ? reinterpret_cast<const float*>(lut + 2048 * kLutCopies) : nullptr;
   struct Step {
-    Piece<FMT> p;
-    u32x4 x[4];
+    u32x4 w[1], x[4];
+    typename Stream<FMT>::Raw s;
+    int st, from;      // which of the run's steps, and the run's first
     uint32_t tokens;   // of the group that chose the expert, as bits
     int group;
-    bool second, first, last, on;
+    bool first, last, on;
   };
   // where the loads are: unit, step, the end of its run, the lane's row
-  int at_u = wv, at_s = 0, at_end = 0, group = 0, xoff = kOob;
+  int at_u = wv, at_s = 0, from = 0, at_end = 0, group = 0, xoff = kOob;
   uint32_t tokens = 0;
   bool fresh = true;
   Stream<FMT> in;
+  in.place(a.I, c, q);
   auto open = [&] {
     const bool on = at_u < total;
     const int n = !on ? 0 : a.runs == 1 ? at_u : (int)__umulhi((uint32_t)at_u, a.per_run);   // at_u / runs
@@ -668,7 +739,7 @@ __global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
     const uint32_t what = __builtin_amdgcn_readfirstlane(uses[n].what);
     const uint32_t all = on ? __builtin_amdgcn_readfirstlane(uses[n].tokens) : 0u;
     group = (what >> 10) & 3;
-    at_s = run * a.run_steps;
+    at_s = from = run * a.run_steps;
     at_end = min(at_s + a.run_steps, steps);
     fresh = true;
     in.open(a.dn, what & 1023, c0, on);
@@ -683,10 +754,11 @@ __global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
     u.tokens = tokens;
     u.first = fresh;
     fresh = false;
-    const int k = q * Kh + 128 * at_s;
-    in.place(a.I, c, k);
-    in.load(u.p, a.I, 0);
-    u.second = in.second;
+    const int k = 128 * q + kStep * at_s;
+    u.w[0] = in.codes(a.I, at_s, 0, true);
+    u.st = at_s - from;
+    u.from = from;
+    in.scales(u.s, a.I, u.st ? steps + 4 : from, 0, true);   // (with a run's first step only)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (MXFP4: the lane's 32 k are in K or not; NF4: a block of 64)
@@ -699,15 +771,23 @@ __global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
       open();
     }
   };
-  f32x4 acc[GROUPS], d;
+  f32x4 acc[GROUPS], d[1];
+  typename Stream<FMT>::Raw sc;
 #pragma unroll
   for (int i = 0; i < GROUPS; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto finish = [&](const Step& u) {
     Acts<FMT> x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) x.set(i, u.x[i]);
-    if (u.first) d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    step<FMT>(u.p, u.second, x, lut, off, a.dn.book, d);
+    if (u.first) {
+      d[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      sc = u.s;
+      in.finish(sc, a.I, u.from, book, off);
+    }
+    const int at = (16 * u.st + (l & 15)) * 4;
+    const uint32_t s0[1] = {(uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)sc.v[0])};
+    const uint32_t s1[1] = {FMT == MOE4_FMT_MXFP4 ? 0u : (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)sc.v[1])};
+    step<FMT, 1>(u.w, s0, s1, x, lut, d);
     if (u.last) {
       // (a token that did not choose the expert takes nothing of it: its zeros times an infinite
       // or NaN weight are no zeros)
@@ -715,7 +795,7 @@ __global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
       for (int i = 0; i < GROUPS; ++i)
         if (GROUPS == 1 || u.group == i) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][r] += u.tokens >> (4 * (g & 1) + r) & 1 ? d[r] : 0.0f;
+          for (int r = 0; r < 4; ++r) acc[i][r] += u.tokens >> (4 * (g & 1) + r) & 1 ? d[0][r] : 0.0f;
         }
     }
   };
@@ -779,33 +859,21 @@ template <int FMT>
 hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   const int S = a.T * a.k;
   constexpr bool kMx = FMT == MOE4_FMT_MXFP4;
-  // A wave for each 128-k step, up to eight; up to sixteen where all steps then have one.
-  const int steps = half_k(a.H) / 128;
-  const bool big = kMx && a.E <= 128 && steps > 8 && steps <= 16;
-  const int nw = big ? steps : steps < 4 ? 4 : steps < 8 ? steps : 8;
-  const int dsteps = half_k(a.I) / 128;
+  const int dsteps = steps_of(a.I);
   a.runs = (dsteps + 3) / 4;
   a.run_steps = (dsteps + a.runs - 1) / a.runs;
   a.runs = (dsteps + a.run_steps - 1) / a.run_steps;
   a.per_run = (uint32_t)(((uint64_t)1 << 32) / a.runs) + 1;
-  // the workgroups that the chip holds at once, or one for every item
-  const int64_t items = (int64_t)S * (a.I / (4 * kTiles)), room = 256;
+  // as many workgroups as the chip holds at once, or a wave for every tile
+  const int64_t tiles = (int64_t)S * (a.I / 4), room = 256;
   auto up = [&](auto* k) {
-    const int bytes = lut_bytes(FMT) + 2 * nw * 2 * kTiles * kRed * 4 + route_lds(a.E, S);
+    const int bytes = lut_bytes(FMT) + route_lds(a.E, S);
     hipError_t e = allow_lds(k, bytes);
     if (e != hipSuccess) return e;
-    k<<<(uint32_t)(items < room ? items : room), nw * 64, bytes, s>>>(a);
+    k<<<(uint32_t)((tiles + 7) / 8 < room ? (tiles + 7) / 8 : room), 512, bytes, s>>>(a);
     return hipGetLastError();
   };
-  constexpr int D = kMx ? 4 : FMT == MOE4_FMT_NF4 ? 3 : 2;
-  hipError_t e = hipSuccess;
-  if (big) {
-    if constexpr (kMx) e = up(&k_layer_up<FMT, 2, true, 2, 1024>);
-  } else if (a.E <= 128) {
-    e = steps <= nw ? up(&k_layer_up<FMT, 2, true, D, 512>) : up(&k_layer_up<FMT, 2, false, D, 512>);
-  } else {
-    e = steps <= nw ? up(&k_layer_up<FMT, 16, true, D, 512>) : up(&k_layer_up<FMT, 16, false, D, 512>);
-  }
+  hipError_t e = a.E <= 128 ? up(&k_layer_up<FMT, 2>) : up(&k_layer_up<FMT, 16>);
   if (e != hipSuccess) return e;
   auto down = [&](auto* k, int groups, int threads) {
     const int bytes = lut_bytes(FMT) + threads / 64 * 2 * groups * 256 + S * (int)sizeof(Use);
@@ -814,12 +882,9 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
     k<<<a.H / 8, threads, bytes, s>>>(a);
     return hipGetLastError();
   };
-  constexpr int DD = kMx ? 4 : 3;
   auto by_threads = [&](auto gc) {
     constexpr int G = decltype(gc)::value;
-    if constexpr (FMT != MOE4_FMT_NF4_DQ)
-      if (a.H <= 2048) return down(&k_layer_down<FMT, G, DD, 1024>, G, 1024);
-    return down(&k_layer_down<FMT, G, DD, 512>, G, 512);
+    return down(&k_layer_down<FMT, G, 3, 512>, G, 512);
   };
   if (a.T <= 8) return by_threads(std::integral_constant<int, 1>{});
   if (a.T <= 16) return by_threads(std::integral_constant<int, 2>{});
