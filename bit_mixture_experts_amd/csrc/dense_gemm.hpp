@@ -17,8 +17,7 @@
 //
 //  * Row operand: LDS [rows][128 B]; the 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7),
 //    so that the 16 rows of an operand read hit 16 different 16-byte bank groups (two rows
-//    share a 256-byte bank line). 64-byte rows: c ^ ((r >> 2) & 3) (four rows a line); 32-byte
-//    rows: c ^ ((r >> 3) & 1).
+//    share a 256-byte bank line). 64-byte rows: c ^ ((r >> 2) & 3) (four rows a line).
 //  * Col operand: LDS [64 k][rows * 2 B] as in memory; the MFMA wants 8 consecutive k of one
 //    row in a lane, which ds_read_b64_tr_b16 delivers: 16 lanes read a 4 (k) x 16 (row)
 //    block of 8 bytes each and get its transpose. The 32-byte unit u of row k sits at
@@ -159,9 +158,7 @@ struct Loader {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int piece = i * THREADS + t, r = piece / (RB / 16);
-      const int c = RB == 128   ? (piece & 7) ^ ((r >> 1) & 7)
-                    : RB == 64 ? (piece & 3) ^ ((r >> 2) & 3)
-                               : (piece & 1) ^ ((r >> 3) & 1);
+      const int c = RB == 128 ? (piece & 7) ^ ((r >> 1) & 7) : (piece & 3) ^ ((r >> 2) & 3);
       chunk = c * 16;   // the same for every i: loads are a multiple of 16 rows apart
       const int rr = row_of(r);
       off[i] = rr >= 0 ? (uint32_t)(rr * ldb) + c * 16 : (uint32_t)kOob;

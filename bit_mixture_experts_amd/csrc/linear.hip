@@ -1,7 +1,7 @@
 // The dense product with an MXFP4 weight, y = x W^T + bias + residual, on bf16, MXFP8 or MXFP4
 // activations, and its input gradient dx = dY W.
 //
-// Many tokens: tiles as in dense_gemm.hpp (256 x 256 of eight waves or 128 x 128 of four), the weight
+// Many tokens: tiles as in dense_gemm.hpp (256 x 256, 256 x 128 or 128 x 64), the weight
 // as the matrix instruction's first operand.
 //   * MXFP8 and MXFP4 activations: the scaled e2m1 instructions on the codes as they are, 64 k a
 //     step.
@@ -21,55 +21,73 @@ namespace {
 
 constexpr int kXB = MOE4_X_BF16, kX8 = MOE4_X_MXFP8, kX4 = MOE4_X_MXFP4;
 
-// k runs in turns of 256, eight blocks of every row, whose scales travel together; a k-tile is 128
-// bytes of a row of activations.
+// k runs in turns of 256: 128 bytes, a whole line, and eight scales of every row of the weight, which
+// travel together; a k-tile is 128 bytes of a row of activations. (With the weight's 32 bytes of a
+// k-tile loaded for each, 2048 tokens bf16 at 4096 took 68 us: lines were asked for four times.)
 template <int XF>
 struct LinK {
   static constexpr int kTile = XF == kXB ? 64 : XF == kX8 ? 128 : 256;   // k of a k-tile
   static constexpr int kSub = 256 / kTile;                               // k-tiles of a turn
-  static constexpr int kRbA = kTile / 2;                                 // bytes of a weight row
   static constexpr int kSteps = XF == kX8 ? 2 : 4;
   // bytes of k values of a row of activations
   static __host__ __device__ constexpr int64_t bytes(int64_t k) { return k * 128 / kTile; }
 };
 
 // The scales of a turn, eight bytes for each row of the tile, through LDS: thread t of the workgroup
-// reads those of tile row t (A's rows, then B's). Rows start at any byte, so the aligned dwords
-// around them are loaded and shifted. Blocks past K take scale 0: the bytes there belong to the next
-// row and may be e8m0 NaNs.
+// reads those of tile row t (A's rows, then B's), of two turns at a time (rows are far apart, so that
+// a load of few bytes moves as much as one of 16; 8192 MXFP4 tokens at N 8192, K 4096 took 187 us with
+// a load for every turn, 170 so). Rows start at any byte, so the aligned dwords around them are
+// loaded and shifted. Blocks past K take scale 0: the bytes there belong to the next row and may be
+// e8m0 NaNs.
 template <typename S>
 struct TurnScales {
-  static_assert(S::kThreads == S::BA + S::BB, "a thread for every row");
-  static constexpr int kBytes = S::kThreads * 8;
-  rsrc_t r;
+  static constexpr int kRows = (S::BA + S::BB + S::kThreads - 1) / S::kThreads;   // of a thread, kThreads apart
+  static constexpr int kBytes = kRows * S::kThreads * 8;
+  rsrc_t r[kRows];
   int nb;
-  uint32_t off;
-  u32x2 raw;
-  uint32_t more;
+  uint32_t off[kRows];
+  u32x4 raw[kRows];
+  uint32_t more[kRows];
+  bool shifted;   // some row does not begin at a dword
   template <typename RowA, typename RowB>
   __device__ __forceinline__ void init(const MxScales& m, int blocks, RowA row_a, RowB row_b) {
-    const int t = threadIdx.x;
-    const bool is_a = __builtin_amdgcn_readfirstlane(wave_id()) * 64 < S::BA;   // whole waves
-    r = make_rsrc_uniform(is_a ? m.sa : m.sb, (uint32_t)(((is_a ? m.na : m.nb) + 3) & ~(int64_t)3));
     nb = blocks;
-    const int row = is_a ? row_a(t) : row_b(t - S::BA);
-    off = row >= 0 ? (uint32_t)row * m.pitch + m.first : (uint32_t)kOob;
+    shifted = m.pitch & 3;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      more[i] = 0;
+      const int t = threadIdx.x + i * S::kThreads;
+      // whole waves belong to one operand
+      const bool is_a = __builtin_amdgcn_readfirstlane(wave_id()) * 64 + i * S::kThreads < S::BA;
+      r[i] = make_rsrc_uniform(is_a ? m.sa : m.sb, (uint32_t)(((is_a ? m.na : m.nb) + 3) & ~(int64_t)3));
+      const int row = is_a ? row_a(t) : t - S::BA < S::BB ? row_b(t - S::BA) : -1;
+      off[i] = row >= 0 ? (uint32_t)row * m.pitch + m.first : (uint32_t)kOob;
+    }
   }
-  __device__ __forceinline__ void load(int turn) {
-    const int at = (int)((off & ~3u) + 8 * turn);
-    raw = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
-    more = buf_load_b32(r, at + 8);
+  // of turns 2 pair and 2 pair + 1
+  __device__ __forceinline__ void load(int pair) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int at = (int)((off[i] & ~3u) + 16 * pair);
+      raw[i] = buf_load_b128(r[i], at);
+      if (shifted) more[i] = buf_load_b32(r[i], at + 16);
+    }
   }
   __device__ __forceinline__ void store(int turn, uint8_t* lds) const {
     const int left = nb - 8 * turn;   // blocks of this turn
-    const uint32_t sh = off & 3;
-    u32x2 v = {__builtin_amdgcn_alignbyte(raw[1], raw[0], sh), __builtin_amdgcn_alignbyte(more, raw[1], sh)};
+    const bool odd = turn & 1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = left - 4 * i;
-      v[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+    for (int i = 0; i < kRows; ++i) {
+      const uint32_t sh = off[i] & 3;
+      const uint32_t d0 = odd ? raw[i][2] : raw[i][0], d1 = odd ? raw[i][3] : raw[i][1], d2 = odd ? more[i] : raw[i][2];
+      u32x2 v = {__builtin_amdgcn_alignbyte(d1, d0, sh), __builtin_amdgcn_alignbyte(d2, d1, sh)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = left - 4 * h;
+        v[h] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+      }
+      reinterpret_cast<u32x2*>(lds)[threadIdx.x + i * S::kThreads] = v;
     }
-    reinterpret_cast<u32x2*>(lds)[threadIdx.x] = v;
   }
   // of a tile row: the bytes of the lane's half in the turn's four 64-k units
   static __device__ __forceinline__ uint32_t get(const uint8_t* lds, int row) {
@@ -80,48 +98,65 @@ struct TurnScales {
 
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
 
-// one 64-k MFMA of a weight operand (e2m1) with activations in e4m3 or e2m1; the scales are the low
-// bytes
+// one 64-k MFMA of a weight operand (e2m1) with activations in e4m3 or e2m1; the scales are byte
+// `unit` (a constant once the loops are unrolled) of sa and sb
 template <int XF, typename FB>
-__device__ __forceinline__ f32x16 mfma_scaled(i32x4 a, FB b, f32x16 c, uint32_t sa, uint32_t sb) {
-  if constexpr (XF == kX8)
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), b, c, 4, 0, 0, (int)sa, 0, (int)sb);
-  else
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), widen(b), c, 4, 4, 0, (int)sa, 0, (int)sb);
+__device__ __forceinline__ f32x16 mfma_scaled(i32x4 a, FB b, f32x16 c, int unit, uint32_t sa, uint32_t sb) {
+  constexpr int kB = XF == kX8 ? 0 : 4;
+  i32x8 bw;
+  if constexpr (XF == kX8) bw = b;
+  else bw = widen(b);
+  switch (unit) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), bw, c, 4, kB, 0, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), bw, c, 4, kB, 1, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), bw, c, 4, kB, 2, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), bw, c, 4, kB, 3, (int)sa, 3, (int)sb);
+  }
 }
 
-template <typename S, int XF>
-using WLoader = Loader<kOpRow, S::BA, S::kThreads, LinK<XF>::kRbA>;
+template <typename S>
+using WLoader = Loader<kOpRow, S::BA, S::kThreads, 128>;
 template <typename S>
 using XLoader = Loader<kOpRow, S::BB, S::kThreads, 128>;
 
-// The k loop: acc += W x^T. Two stages; a k-tile's loads go out between the MFMAs, part behind the
-// barrier that frees their stage, part at the next tile's beginning; the operands of a step are
-// read from LDS while the step before multiplies.
+// LDS: two turns of the weight, two or four k-tiles of activations (the epilogue stages its tile there
+// too), two turns of scales
+template <typename S, int XF>
+struct LinLds {
+  static constexpr int kA = S::BA * 128, kB = S::BB * 128;
+  static constexpr int kStages = S::BB == 256 || XF == kX4 ? 2 : 4;   // of activations
+  static constexpr int kScales = 2 * kA + kStages * kB;
+  static_assert(kScales >= S::kLds, "the epilogue's staging fits");
+  static constexpr int kBytes = kScales + 2 * TurnScales<S>::kBytes;
+};
+
+// The k loop: acc += W x^T. Loads go out between the MFMAs, all of a stage's behind the barrier that
+// frees it (8192 MXFP8 tokens at 4096 139 us, and 151 with half of them at the beginning of the next
+// k-tile; bf16 in four stages the other way round, 61 and 60, and so); the operands of a step are read
+// from LDS while the step before multiplies.
 template <typename S, int XF, typename RowA, typename RowB>
-__device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* lds, const WLoader<S, XF>& la,
+__device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* lds, const WLoader<S>& la,
                                          const XLoader<S>& lb, int K, const MxScales& mx, RowA row_a,
                                          RowB row_b) {
   using P = LinK<XF>;
-  constexpr int kA = S::BA * P::kRbA, kStage = kA + S::BB * 128;
-  static_assert(2 * kStage <= S::kLds, "the stages fit");
-  constexpr int kSub = P::kSub, kSteps = P::kSteps;
+  using M = LinLds<S, XF>;
+  constexpr int kSub = P::kSub, kSteps = P::kSteps, kN = M::kStages;
+  constexpr int kEarly = XF == kXB && kN > 2 ? 4 : 8;   // 8ths of a stage's loads behind the barrier
+  uint8_t* const ldb = lds + 2 * M::kA;
   const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
   const int wa = w % S::WA, wb = w / S::WA, r = l & 31, half = l >> 5;
   const int turns = (K + 255) / 256;
-  // first byte of the lane's row, and the place of its first chunk there
-  const int arow = (wa * S::TA * 32 + r) * P::kRbA, brow = (wb * S::TB * 32 + r) * 128;
-  const int akey = P::kRbA == 128 ? (r >> 1) & 7 : P::kRbA == 64 ? (r >> 2) & 3 : (r >> 3) & 1;
-  const int bkey = (r >> 1) & 7;
-  // weights: 16 bytes of step s (bf16: of the whole k-tile)
-  auto read_a = [&](const uint8_t* st, int t, int s) {
-    const int chunk = XF == kXB ? half : 2 * s + half;
-    return *reinterpret_cast<const i32x4*>(st + arow + t * 32 * P::kRbA + ((chunk ^ akey) * 16));
+  // first byte of the lane's rows, and what their chunks' places are swizzled by
+  const int arow = (wa * S::TA * 32 + r) * 128, brow = (wb * S::TB * 32 + r) * 128, key = (r >> 1) & 7;
+  // weights: 16 bytes of step s of the turn's k-tile h (bf16: of the whole k-tile)
+  auto read_a = [&](const uint8_t* st, int t, int h, int s) {
+    const int chunk = XF == kXB ? 2 * h + half : 2 * (kSteps * h + s) + half;
+    return *reinterpret_cast<const i32x4*>(st + arow + t * 32 * 128 + ((chunk ^ key) * 16));
   };
   using FB = std::conditional_t<XF == kX8, i32x8, i32x4>;
   auto read_b = [&](const uint8_t* st, int t, int s) {
-    const uint8_t* p = st + kA + brow + t * 32 * 128;
-    auto chunk = [&](int c) { return *reinterpret_cast<const i32x4*>(p + ((c ^ bkey) * 16)); };
+    const uint8_t* p = st + brow + t * 32 * 128;
+    auto chunk = [&](int c) { return *reinterpret_cast<const i32x4*>(p + ((c ^ key) * 16)); };
     if constexpr (XF == kXB) return chunk(4 * half + s);      // 8 k of the half's block
     else if constexpr (XF == kX4) return chunk(2 * s + half);  // 32 k
     else   // k = 32 c + 16 half .. + 15 in the c-th 16 bytes
@@ -130,7 +165,7 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
   i32x4 fa[S::TA];
   FB fb[2][S::TB];
   TurnScales<S> sc;
-  uint8_t* const sclds = lds + S::kLds;
+  uint8_t* const sclds = lds + M::kScales;
   uint32_t xa[S::TA], xb[S::TB], na[S::TA], nb[S::TB];
   auto next_scales = [&](int turn) {
     const uint8_t* p = sclds + (turn & 1) * TurnScales<S>::kBytes;
@@ -141,14 +176,15 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
       for (int u = 0; u < S::TB; ++u) nb[u] = sc.get(p, S::BA + (wb * S::TB + u) * 32 + r);
     }
   };
-  constexpr int kLa = WLoader<S, XF>::kLoads, kLoads = kLa + XLoader<S>::kLoads, kEarly = kLoads / 2;
-  auto issue = [&](int kt, int i0, int i1, uint8_t* st) {
+  // loads [n0, n1) of 8ths of a turn of weights, of a k-tile of activations
+  constexpr int kLa = WLoader<S>::kLoads, kLb = XLoader<S>::kLoads;
+  auto issue_a = [&](int turn, int n0, int n1) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      if (i < i0 || i >= i1) continue;
-      if (i < kLa) la.template issue<false>(kt, i, st);
-      else lb.template issue<false>(kt, i - kLa, st + kA);
-    }
+    for (int i = kLa * n0 / 8; i < kLa * n1 / 8; ++i) la.template issue<false>(turn, i, lds + (turn & 1) * M::kA);
+  };
+  auto issue_b = [&](int kt, int n0, int n1, uint8_t* st) {
+#pragma unroll
+    for (int i = kLb * n0 / 8; i < kLb * n1 / 8; ++i) lb.template issue<false>(kt, i, st);
   };
 #pragma unroll
   for (int i = 0; i < S::TA; ++i)
@@ -159,19 +195,21 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
 
   sc.init(mx, K / 32, row_a, row_b);
   sc.load(0);
-  TurnScales<S> first = sc;
-  sc.load(1);
-  issue(0, 0, kLoads, lds);
-  issue(1, 0, kEarly, lds + kStage);
-  wait_vmcnt<kEarly>();
-  first.store(0, sclds);
+  issue_a(0, 0, 8);
+  issue_b(0, 0, 8, ldb);
+  issue_a(1, 0, kEarly);
+#pragma unroll
+  for (int i = 1; i < kN; ++i) issue_b(i, 0, i < kN - 1 ? 8 : kEarly, ldb + i * M::kB);
+  wait_vmcnt<kLa * kEarly / 8 + (kN - 2) * kLb + kLb * kEarly / 8>();
+  sc.store(0, sclds);
   wait_lgkm0();
   lds_barrier();
   next_scales(0);
 #pragma unroll
-  for (int t = 0; t < S::TA; ++t) fa[t] = read_a(lds, t, 0);
+  for (int t = 0; t < S::TA; ++t) fa[t] = read_a(lds, t, 0, 0);
 #pragma unroll
-  for (int t = 0; t < S::TB; ++t) fb[0][t] = read_b(lds, t, 0);
+  for (int t = 0; t < S::TB; ++t) fb[0][t] = read_b(ldb, t, 0);
+  int at_cur = 0, at_prev = (kN - 1) * M::kB;   // this k-tile's stage, and the one before
   for (int kp = 0; kp < turns; ++kp) {
 #pragma unroll
     for (int t = 0; t < S::TA; ++t) xa[t] = na[t];
@@ -180,24 +218,32 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
       for (int u = 0; u < S::TB; ++u) xb[u] = nb[u];
     }
     sc.store(kp + 1, sclds + ((kp + 1) & 1) * TurnScales<S>::kBytes);
-    sc.load(kp + 2);
+    if (!(kp & 1)) sc.load(kp / 2 + 1);
+    const uint8_t* const cur_a = lds + (kp & 1) * M::kA;
+    const uint8_t* const nxt_a = lds + ((kp + 1) & 1) * M::kA;
 #pragma unroll
     for (int h = 0; h < kSub; ++h) {
-      const int kt = kp * kSub + h, par = kSub > 1 ? h & 1 : kp & 1;
-      uint8_t* const cur = lds + par * kStage;
-      uint8_t* const nxt = lds + (par ^ 1) * kStage;
+      const int kt = kp * kSub + h, at_nxt = at_cur == (kN - 1) * M::kB ? 0 : at_cur + M::kB;
+      uint8_t *const cur = ldb + at_cur, *const nxt = ldb + at_nxt, *const prev = ldb + at_prev;
+      at_prev = at_cur;
+      at_cur = at_nxt;
+      const bool end = h == kSub - 1;   // of the turn
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const bool last = s == kSteps - 1;
-        const int sn = (s + 1) % kSteps;
+        const int sn = (s + 1) % kSteps, hn = last ? (h + 1) % kSub : h;
         const uint8_t* from = last ? nxt : cur;
+        const uint8_t* from_a = last && end ? nxt_a : cur_a;
         if (last) {
           // the tile's barrier: the wave's loads of the next tile have landed, its reads of this one
           // are done, and so are the others'
-          wait_vmcnt<0>();
+          // (activations of kN - 2 tiles more may be in flight, at a turn's end those asked for after the
+          // next turn's weights)
+          if (end) wait_vmcnt<(kN - 2 < kSub - 1 ? kN - 2 : kSub - 1) * kLb>();
+          else wait_vmcnt<(kN - 2) * kLb>();
           wait_lgkm0();
           lds_barrier();
-          if (h == kSub - 1) next_scales(kp + 1);
+          if (end) next_scales(kp + 1);
         }
         // (past the last tile: stale values, read and never used)
 #pragma unroll
@@ -218,16 +264,23 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
             for (int u = 0; u < S::TB; ++u)
               acc[t][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(bf16x8, fb[s & 1][u]),
                                                                   acc[t][u], 0, 0, 0);
-            if (last) fa[t] = read_a(nxt, t, 0);
+            if (last) fa[t] = read_a(from_a, t, hn, 0);
           } else {
 #pragma unroll
             for (int u = 0; u < S::TB; ++u)
-              acc[t][u] = mfma_scaled<XF>(fa[t], fb[s & 1][u], acc[t][u], xa[t] >> (8 * unit), xb[u] >> (8 * unit));
-            fa[t] = read_a(from, t, sn);
+              acc[t][u] = mfma_scaled<XF>(fa[t], fb[s & 1][u], acc[t][u], unit, xa[t], xb[u]);
+            fa[t] = read_a(from_a, t, hn, sn);
           }
-          if (last) issue(kt + 2, kEarly * t / S::TA, kEarly * (t + 1) / S::TA, cur);
-          if (s == 0)
-            issue(kt + 1, kEarly + (kLoads - kEarly) * t / S::TA, kEarly + (kLoads - kEarly) * (t + 1) / S::TA, nxt);
+          const int n0 = kEarly * t / S::TA, n1 = kEarly * (t + 1) / S::TA;
+          const int m0 = kEarly + (8 - kEarly) * t / S::TA, m1 = kEarly + (8 - kEarly) * (t + 1) / S::TA;
+          if (last) {
+            issue_b(kt + kN, n0, n1, cur);
+            if (end) issue_a(kp + 2, n0, n1);
+          }
+          if (s == 0) {
+            issue_b(kt + kN - 1, m0, m1, prev);
+            if (h == 0) issue_a(kp + 1, m0, m1);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -235,9 +288,6 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
   }
   wait_vmcnt<0>();   // the zeros of the tiles past the last, before the stages are used again
 }
-
-template <typename S>
-constexpr int kLinLds = S::kLds + 2 * TurnScales<S>::kBytes;
 
 // FfnProduct: A the weight (p codes, s scales), B the activations; K in values
 template <typename S, int XF>
@@ -253,7 +303,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_linear(const FfnProduct p) {
   const int turns = (p.K + 255) / 256, parts = S::kSplits ? p.splits : 1;
   const int t0 = (int)((int64_t)turns * split / parts), t1 = (int)((int64_t)turns * (split + 1) / parts);
   const int K = min(t1 * 256, p.K) - t0 * 256;
-  WLoader<S, XF> la;
+  WLoader<S> la;
   XLoader<S> lb;
   const Operand A = {static_cast<const uint8_t*>(p.A.p) + (int64_t)t0 * 128, nullptr, p.K / 2, p.na};
   const Operand B = {static_cast<const uint8_t*>(p.B.p) + LinK<XF>::bytes(256) * t0, nullptr,
@@ -576,30 +626,52 @@ hipError_t launch_skinny(const FfnProduct& p, hipStream_t s) {
   return run(std::integral_constant<int, 1>{});
 }
 
+// 256 x 128 of eight waves, 128 x 64 of four (two workgroups per CU)
+using TileMid = TileShape<4, 2, 2, 2>;
+using TileSmall = TileShape<2, 2, 2, 1>;
+
+// Which tiles, by rounds of the chip (256 tiles of 256 x 256 or 256 x 128, 512 of 128 x 64), a round of
+// them taking about 15, 8 and 5 units. Us, bf16: N = K = 4096, 2048 tokens 89 (half a round) and 60, 1024 37 with the
+// smallest; MXFP8 509 tokens at 2880 (one round of each, mostly empty) 27 with 256 x 128, 15 with 128 x 64.
+enum { kLarge, kMid, kSmall };
+int lin_tiles(int64_t na, int64_t nb) {
+  auto rounds = [](int64_t n, int64_t at_once) { return (n + at_once - 1) / at_once; };
+  const int64_t large = 15 * rounds(tiles_of<Tile256>(na, nb), 256), mid = 8 * rounds(tiles_of<TileMid>(na, nb), 256),
+                small = 5 * rounds(tiles_of<TileSmall>(na, nb), 512);
+  return large <= mid && large <= small ? kLarge : mid <= small ? kMid : kSmall;
+}
+
+// Parts of k where the smallest tiles leave half of the CUs without one: as many as give each one,
+// each of at least 512 k, 1024 or 2048 (the same time on the matrix cores, which pays for the launch
+// that joins them: with every CU busy, 509 tokens at 2880, two parts take 14 us instead of 15, and the
+// join 5).
+int64_t most_lin_splits(int K, int x_format) {
+  return std::min<int64_t>((K + 255) / 256 / (x_format == kXB ? 2 : x_format == kX8 ? 4 : 8), kMostSplits);
+}
+int lin_splits(int64_t na, int64_t nb, int K, int x_format) {
+  if (lin_tiles(na, nb) != kSmall) return 1;
+  const int64_t s = std::min<int64_t>(256 / tiles_of<TileSmall>(na, nb), most_lin_splits(K, x_format));
+  return s < 2 ? 1 : (int)s;
+}
+
 template <int XF>
 hipError_t launch_tiled(const FfnProduct& p, hipStream_t s) {
-  auto run = [&](auto* k, int64_t tiles, int threads, int bytes) {
-    hipError_t e = allow_lds(k, bytes);
+  auto run = [&](auto sc) {
+    using S = decltype(sc);
+    auto* k = &k_linear<S, XF>;
+    hipError_t e = allow_lds(k, LinLds<S, XF>::kBytes);
     if (e != hipSuccess) return e;
-    k<<<(uint32_t)(tiles * p.splits), threads, bytes, s>>>(p);
+    k<<<(uint32_t)(tiles_of<S>(p.na, p.nb) * p.splits), S::kThreads, LinLds<S, XF>::kBytes, s>>>(p);
     return hipGetLastError();
   };
-  if (p.splits == 1 && large_tiles_for(p.na, p.nb))
-    return run(&k_linear<Tile256, XF>, tiles_of<Tile256>(p.na, p.nb), Tile256::kThreads, kLinLds<Tile256>);
-  hipError_t e = run(&k_linear<Tile128, XF>, tiles_of<Tile128>(p.na, p.nb), Tile128::kThreads, kLinLds<Tile128>);
+  const int tiles = lin_tiles(p.na, p.nb);
+  if (tiles == kLarge) return run(Tile256{});
+  if (tiles == kMid) return run(TileMid{});
+  hipError_t e = run(TileSmall{});
   if (e != hipSuccess || p.splits == 1) return e;
   JoinArgs j = {};
   j.p[0] = p;
   return launch_join(j, 1, s);
-}
-
-// Parts of k for n tiles of 128 x 128 that leave most of a round (512) empty: as many as fill it,
-// each of at least 512 k, 1024 or 2048 (the same time on the matrix cores, which pays for the
-// launch that joins them).
-int lin_splits(int64_t n128, int K, int x_format) {
-  const int64_t turns = (K + 255) / 256, most = 512 / n128;
-  const int64_t s = std::min(most, turns / (x_format == kXB ? 2 : x_format == kX8 ? 4 : 8));
-  return s < 2 ? 1 : (int)std::min<int64_t>(s, kMostSplits);
 }
 
 int linear_variant(const moe4_linear& l, int64_t T) {
@@ -611,7 +683,7 @@ int linear_variant(const moe4_linear& l, int64_t T) {
 
 size_t linear_ws_bytes(const moe4_linear& l, int64_t T, bool backward) {
   if (!backward) {
-    const int64_t most = (l.N + 127) / 128 > 256 ? 1 : std::min<int64_t>((l.K + 255) / 256 / 2, kMostSplits);
+    const int64_t most = (l.N + 127) / 128 > 128 ? 1 : most_lin_splits(l.K, kXB);
     return (size_t)part_bytes(l.N, T, most);
   }
   return align_up((size_t)part_bytes(l.K, T, most_k_splits(l.K, l.N, 2)), 256) + (size_t)kColParts * l.N * 4;
@@ -633,7 +705,7 @@ hipError_t launch_linear_forward(const moe4_linear& l, const void* x, int x_form
   p.add_dtype = residual ? res_dtype : MOE4_DTYPE_BF16;
   p.out = out;
   p.out_dtype = out_dtype;
-  p.splits = lin_splits(tiles_of<Tile128>(l.N, T), l.K, x_format);
+  p.splits = lin_splits(l.N, T, l.K, x_format);
   p.part = static_cast<float*>(ws);
   *variant = linear_variant(l, T);
   auto go = [&](auto fc) {
