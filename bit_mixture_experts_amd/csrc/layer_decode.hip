@@ -2,10 +2,11 @@
 //   1. k_layer_up: every workgroup routes all tokens itself, from which it knows the experts that
 //      were chosen and their rows, and takes an even share of their gate/up pairs. h goes to the
 //      workspace, with the list of experts and rows.
-//   2. k_layer_down: every workgroup takes 8 output columns and runs over all experts that were
-//      chosen, so the weighted sum over a token's slots stays inside it.
-// No counter, flag or order of arrival between workgroups decides anything: sums are in a fixed
-// order.
+//   2. k_layer_down: a panel, 8 or 16 output columns of 8 tokens, is a sum over all experts that those
+//      chose. Few units of work: a workgroup to a panel; many: the units of all panels are dealt to
+//      the workgroups in equal runs, and the one that comes last to a panel that was cut adds its
+//      parts, in their order.
+// Sums are in a fixed order: which workgroup comes last decides who adds, not what.
 //
 // Both stream 4-bit weights for a handful of rows. One tile of either is 8 weight rows, and a step
 // 256 k of them: its two halves of 128 k as the 16 columns (c, q) of a 16x16x32 MFMA, against 8
@@ -86,8 +87,11 @@ __device__ __forceinline__ void fill_lut(uint8_t* lut, const float* book) {
     }
   }
 }
-__device__ __forceinline__ u32x2 lookup(const uint8_t* lut, uint32_t w, int byte, uint32_t lane8) {
-  return *reinterpret_cast<const u32x2*>(lut + __builtin_amdgcn_perm(w, lane8, 0x0C0C0000u | (4 + byte) << 8));
+// (the table begins LDS, so that the byte and the lane's place are the address: the kernels have no
+// static LDS, and their dynamic LDS begins with it)
+__device__ __forceinline__ u32x2 lookup(uint32_t w, int byte, uint32_t lane8) {
+  typedef const u32x2 __attribute__((address_space(3))) entry_t;
+  return *reinterpret_cast<entry_t*>(__builtin_amdgcn_perm(w, lane8, 0x0C0C0000u | (4 + byte) << 8));
 }
 
 // 4x4 transpose of dwords across the four 16-lane rows of a wave: row g holds D[g][0..3] before and
@@ -243,37 +247,46 @@ __device__ __forceinline__ int act_k(int i) {
   const int g = lane_id() >> 4;
   return FMT == MOE4_FMT_MXFP4 ? 32 * g + 8 * i : 32 * i + 8 * g;
 }
-// off: byte offset of the lane's row in the resource (kOob: no row); its step starts at k
+// off: byte offset of the lane's row in the resource (kOob: no row); its half of the step starts at k.
+// The lane's 32 k are all in K, or NF4's two blocks of 64 each are, or not.
 template <int FMT>
-__device__ __forceinline__ void load_acts(Acts<FMT>& x, rsrc_t r, int off, int k, int K) {
+__device__ __forceinline__ void load_acts(u32x4 (&x)[4], rsrc_t r, int off, int k, int K) {
+  constexpr int kEach = FMT == MOE4_FMT_MXFP4 ? 4 : 2;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int kk = k + act_k<FMT>(i);
-    x.set(i, buf_load_b128(r, off != kOob && kk < K ? off + 2 * kk : kOob));
+  for (int i = 0; i < 4; i += kEach) {
+    const int kk = k + act_k<FMT>(i), at = off != kOob && kk < K ? off + 2 * kk : kOob;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) x[i + j] = buf_load_b128(r, at + 2 * (act_k<FMT>(i + j) - act_k<FMT>(i)));
   }
 }
 
-// acc += one step's products of TT tiles; s0, s1: their scales (NF4 two fp32, MXFP4 the four bytes in
+// acc += one step's products of TT tiles (which share their activations, or with NX = TT are so many
+// steps of one tile, whose acc are to be added); s0, s1: their scales (NF4 two fp32, MXFP4 the four bytes in
 // s0). MXFP4: the lane's 32 k are one block, each weight exact in bf16. NF4: the codes are put in
 // MFMA order, so that two dwords of a lane make a block; lookups run ahead of the MFMAs that take
 // them, by as much as covers LDS' latency, and the two blocks and the tiles take turns, so that no
 // MFMA waits for the one before it. (Left to the compiler, which looked four bytes up, waited and
 // multiplied, the first launch took 59 us for 16 tokens through
-// 81 of 128 experts of 2048 x 768, and takes 53 so.)
-template <int FMT, int TT>
+// 81 of 128 experts of 2048 x 768, and 53 so.)
+template <int FMT, int TT, int NX>
 __device__ __forceinline__ void step(const u32x4 (&codes)[TT], const uint32_t (&s0)[TT], const uint32_t (&s1)[TT],
-                                     const Acts<FMT>& x, const uint8_t* lut, f32x4 (&acc)[TT]) {
+                                     const Acts<FMT> (&x)[NX], uint32_t lane8, f32x4 (&acc)[TT]) {
   if constexpr (FMT == MOE4_FMT_MXFP4) {
+    uint32_t byte[TT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < TT; ++j) byte[j] = s0[j] >> (8 * (lane_id() >> 4)) & 255u;
+    // (conversions a product ahead of it: a matrix instruction waits for operands just written)
+    u32x4 b = mx4_bf16x8(codes[0][0], byte[0]);
 #pragma unroll
-      for (int j = 0; j < TT; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, x.v[i]),
-            __builtin_bit_cast(bf16x8, mx4_bf16x8(codes[j][i], s0[j] >> (8 * (lane_id() >> 4)) & 255u)), acc[j], 0, 0, 0);
+    for (int i = 0; i < 4 * TT; ++i) {
+      const int j = i % TT, jn = (i + 1) % TT, in = (i + 1) / TT;
+      const u32x4 now = b;
+      if (i + 1 < 4 * TT) b = mx4_bf16x8(codes[jn][in], byte[jn]);
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[NX == 1 ? 0 : j].v[i / TT]),
+                                                       __builtin_bit_cast(bf16x8, now), acc[j], 0, 0, 0);
+    }
   } else {
     constexpr int kAhead = TT >= 4 ? 1 : 4 / TT;
-    const uint32_t lane8 = 8 * (lane_id() & (kLutCopies - 1));
     u32x4 w[TT];
     u32x2 v[kAhead + 1][TT][2];
     f32x4 d[TT][2];
@@ -288,7 +301,7 @@ __device__ __forceinline__ void step(const u32x4 (&codes)[TT], const uint32_t (&
       for (int j = 0; j < TT; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          v[m % (kAhead + 1)][j][h] = lookup(lut, w[j][i / 2], 2 * (i & 1) + h, lane8);
+          v[m % (kAhead + 1)][j][h] = lookup(w[j][i / 2], 2 * (i & 1) + h, lane8);
     };
 #pragma unroll
     for (int m = 0; m < kAhead; ++m) look(m);
@@ -300,7 +313,7 @@ __device__ __forceinline__ void step(const u32x4 (&codes)[TT], const uint32_t (&
       for (int j = 0; j < TT; ++j) {
         const u32x2* e = v[m % (kAhead + 1)][j];
         d[j][m & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, x.v[4 * (m & 1) + m / 2]),
+            __builtin_bit_cast(bf16x8, x[NX == 1 ? 0 : j].v[4 * (m & 1) + m / 2]),
             __builtin_bit_cast(bf16x8, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3)), d[j][m & 1], 0, 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -323,8 +336,8 @@ __device__ __forceinline__ int entry_rows(uint32_t v) { return (v >> 10) & 15; }
 __device__ __forceinline__ int entry_first(uint32_t v) { return (v >> 14) & 511; }
 static_assert(MOE4_LAYER_MOST_SLOTS <= 512, "an entry holds a row in 9 bits");
 
-// What the second launch knows of an expert and a group of 8 tokens: the expert (10 bits), the group
-// (2), the expert's first row (9); and all tokens of the expert as bits
+// What the second launch knows of an expert that some of a group of 8 tokens chose: the expert (12
+// bits), its first row; and all tokens of the expert as bits
 struct Use {
   uint32_t what, tokens;
 };
@@ -343,15 +356,16 @@ struct LayerArgs {
   int out_dtype;
   int32_t* user_idx;
   float* user_w;
-  // runs of steps of the second launch: how many, of how many, 2^32 / runs plus one
-  int runs, run_steps;
-  uint32_t per_run;
+  int runs, run_steps;   // runs of steps of the second launch: how many, of how many
   // workspace
   uint16_t* h;       // [rows = T * k][I], weighted
   int32_t* idx;      // [T * k] experts of the slots
   float* w;          // [T * k] and their weights
-  Use* uses;         // [T * k]
-  int32_t* count;    // [1] how many
+  Use* uses;         // [T * k], by groups of 8 tokens
+  int32_t* count;    // [4] how many of each group
+  float* part;       // [2 workgroups][8][64] parts of panels
+  int32_t* arrived;  // [panels] how many of a panel's parts are there
+  int panels;
 };
 
 // A logit as an unsigned number of moe4_route's order: larger first, +0 as -0, NaN below all; 0 is
@@ -383,13 +397,14 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
 template <int NPL>
 struct Keys {
   uint32_t key[NPL];
+  float v[NPL];   // as loaded
   __device__ __forceinline__ void load(const float* row, int E) {
-    const int l = lane_id();
-    float v[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = row[min(l + kWave * i, E - 1)];
+    for (int i = 0; i < NPL; ++i) v[i] = row[min(lane_id() + kWave * i, E - 1)];
+  }
+  __device__ __forceinline__ void order(int E) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) key[i] = l + kWave * i < E ? order_key(v[i]) : 0u;
+    for (int i = 0; i < NPL; ++i) key[i] = lane_id() + kWave * i < E ? order_key(v[i]) : 0u;
   }
   // takes the first expert of the order out; its key in *k
   __device__ __forceinline__ int pick(uint32_t* k) {
@@ -416,11 +431,13 @@ struct Keys {
 // time over all of k: the activations' operands serve all four, and no wave waits for another
 // after the routing. (The waves of a workgroup splitting k of the same tiles, with a barrier
 // and a sum through LDS for each 16 pairs, took as
-// long for many tokens and 2 us more for one.)
+// long for many tokens and 2 us more for one.) Us: 16 tokens through 81 of 128 NF4 experts of 2048 x
+// 768 51 (143 MB; 9 of them routing and table), 8 through 20 of 32 MXFP4 experts of 2880 x 2880 50 (180
+// MB), one token 13. Without the arithmetic and the activations the loads alone take 41, 42 and 9.
 
 // LDS of the first launch, after the table: tokens of an expert [E] as bits, its first
-// row [E], entries [S], tokens and weights of the rows [S], experts and weights of the slots [S]
-__host__ __device__ constexpr int route_lds(int E, int S) { return 8 * E + 20 * S; }
+// row [E], entries [S], tokens and weights of the rows [S], experts and weights of the slots [S], how many entries
+__host__ __device__ constexpr int route_lds(int E, int S) { return 8 * E + 20 * S + 4; }
 
 template <int FMT, int NPL>
 __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
@@ -436,15 +453,18 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
   float* row_w = reinterpret_cast<float*>(row_t + S);
   int* slot_e = reinterpret_cast<int*>(row_w + S);
   float* slot_w = reinterpret_cast<float*>(slot_e + S);
-  __shared__ int s_count;
+  int& s_count = *reinterpret_cast<int*>(slot_w + S);
   const int steps = steps_of(a.H);
   const int c = l & 7, q = (l >> 3) & 1, g = l >> 4;   // a weight column (c, q), an activation row (t, q)
   const bool writer = blockIdx.x == 0;                 // hands the routing on
 
   // ---- routing: a token by one wave
+  // (its logits are on their way while the table is filled, or the token before is routed)
+  Keys<NPL> keys;
+  auto fetch = [&](int t) { keys.load(a.logits + (int64_t)min(t, a.T - 1) * a.E, a.E); };
   auto route = [&](int t) {
-    Keys<NPL> keys;
-    keys.load(a.logits + (int64_t)t * a.E, a.E);
+    keys.order(a.E);
+    fetch(t + nw);
     float all = 0.0f, some = 0.0f, top = 0.0f;
     if (!a.renorm) {   // softmax over all experts, not over the chosen alone
       uint32_t m = keys.key[0];
@@ -490,6 +510,8 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
       }
     }
   };
+  fetch(wv);
+  for (int i = blockIdx.x * 512 + threadIdx.x; i < a.panels; i += gridDim.x * 512) a.arrived[i] = 0;
   if (a.T == 1) {
     // an expert's rows are one row each, in the order of the choice
     if (wv == 0) {
@@ -502,19 +524,19 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
       }
       if (l == 0) {
         s_count = a.k;
-        if (writer) a.count[0] = a.k;
+        if (writer) a.count[0] = a.k, a.count[1] = a.count[2] = a.count[3] = 0;
       }
     }
     fill_lut<FMT>(lut, a.gu.book);
     __syncthreads();
   } else {
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) chose[i] = 0;
-    __syncthreads();
-    for (int t = wv; t < a.T; t += nw) route(t);
     fill_lut<FMT>(lut, a.gu.book);
     __syncthreads();
+    for (int t = wv; t < a.T; t += nw) route(t);
+    __syncthreads();
     if (wv == 0) {
-      int rows = 0, count = 0, uses = 0;
+      int rows = 0, count = 0;
       for (int e0 = 0; e0 < a.E; e0 += kWave) {
         const int e = e0 + l;
         const uint32_t bits = e < a.E ? chose[e] : 0u;
@@ -524,26 +546,26 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
         for (int i = 0; i < m; ++i)
           entries[count + p - m + i] =
               make_entry(e, min(n - i * kRowsPass, kRowsPass), rows + r - n + i * kRowsPass);
-        if (writer) {
-          int groups = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) groups += (bits >> (8 * i) & 255u) != 0;
-          const int u = wave_scan_dpp(groups);
-          int at = uses + u - groups;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (bits >> (8 * i) & 255u) a.uses[at++] = {(uint32_t)(e | i << 10 | (rows + r - n) << 12), bits};
-          uses += __builtin_amdgcn_readlane(u, 63);
-        }
         rows += __builtin_amdgcn_readlane(r, 63);
         count += __builtin_amdgcn_readlane(p, 63);
       }
-      if (l == 0) {
-        s_count = count;
-        if (writer) a.count[0] = uses;
-      }
+      if (l == 0) s_count = count;
     }
     __syncthreads();
+    if (writer && wv == 0) {
+      int uses = 0;
+      for (int i = 0; i < 4; ++i) {
+        const int from = uses;
+        for (int e0 = 0; e0 < a.E; e0 += kWave) {
+          const int e = e0 + l;
+          const uint32_t bits = e < a.E ? chose[e] : 0u;
+          const int here = (bits >> (8 * i) & 255u) != 0, u = wave_scan_dpp(here);
+          if (here) a.uses[uses + u - 1] = {(uint32_t)(e | base[e] << 12), bits};
+          uses += __builtin_amdgcn_readlane(u, 63);
+        }
+        if (l == 0) a.count[i] = uses - from;
+      }
+    }
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
       const int t = s / a.k, e = slot_e[s];
       const int r = base[e] + __popc(chose[e] & ((1u << t) - 1));
@@ -561,6 +583,7 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
   const rsrc_t rx = make_rsrc_uniform(a.x, (uint32_t)(a.T * a.H * 2));
   const float* book = FMT == MOE4_FMT_NF4_DQ ? reinterpret_cast<const float*>(lut + 2048 * kLutCopies) : nullptr;
   const float off = FMT == MOE4_FMT_NF4_DQ ? a.gu.soff[0] : 0.0f;
+  const uint32_t lane8 = 8 * (l & (kLutCopies - 1));
   Stream<FMT> in;
   in.place(a.H, c < 4 ? gate_row(a.layout, a.I, c & 3) : up_row(a.layout, a.I, c & 3), q);
   // TT tiles (n of them there) from tile j0 of an entry on
@@ -569,7 +592,7 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
     constexpr int kDepth = TT > 2 ? 2 : 4;   // steps in flight
     const int rows = entry_rows(entry);
     in.open(a.gu, entry_expert(entry), 4 * j0 * mult, true);
-    const int xoff = c < rows ? row_t[entry_first(entry) + c] * a.H * 2 + 2 * in.k0 : kOob;
+    const int xoff = c < rows ? row_t[entry_first(entry) + c] * a.H * 2 : kOob;
     // the lane's tile, pair and tokens at the end: tile 2 (g / 2) + q, pair c & 3 (gates in lanes c < 4),
     // tokens 4 (g % 2) ...
     const int mj = 2 * (g >> 1) + q, pair = 4 * (j0 + mj) + (c & 3);
@@ -584,13 +607,10 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
     auto load = [&](int d, int st) {
 #pragma unroll
       for (int j = 0; j < TT; ++j) w[d][j] = in.codes(a.H, st, 4 * j * mult, j < n);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = kStep * st + act_k<FMT>(i);
-        xr[d][i] = buf_load_b128(rx, xoff != kOob && in.k0 + k < a.H ? xoff + 2 * k : kOob);
-      }
+      load_acts<FMT>(xr[d], rx, xoff, in.k0 + kStep * st, a.H);
     };
-    f32x4 acc[TT];
+    f32x4 acc[TT], pair_acc[2];
+    pair_acc[0] = pair_acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
       acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -605,27 +625,52 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
         in.finish(sc[j], a.H, s0, book, off);
         in.scales(next[j], a.H, s0 + 4, 4 * j * mult, j < n);
       }
-      auto one = [&](auto ic) {   // (steps past the last: zeros)
-        constexpr int i = decltype(ic)::value, d = i % kDepth;
-        Acts<FMT> x;
+      // (steps past the last: zeros)
+      if constexpr (TT == 1) {   // two steps at a time, for something to do while one waits
+        auto two = [&](auto ic) {
+          constexpr int i = decltype(ic)::value;
+          Acts<FMT> x[2];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) x.set(v, xr[d][v]);
-        uint32_t lo[TT], hi[TT];
+          for (int v = 0; v < 4; ++v) {
+            x[0].set(v, xr[i][v]);
+            x[1].set(v, xr[i + 1][v]);
+          }
+          const u32x4 both[2] = {w[i][0], w[i + 1][0]};
+          const uint32_t lo[2] = {from_row<i>(sc[0].v[0]), from_row<i + 1>(sc[0].v[0])};
+          const uint32_t hi[2] = {FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i>(sc[0].v[1]),
+                                  FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i + 1>(sc[0].v[1])};
+          step<FMT, 2, 2>(both, lo, hi, x, lane8, pair_acc);
+          __builtin_amdgcn_sched_barrier(0);
+          load(i, s0 + i + 4);
+          load(i + 1, s0 + i + 5);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        two(std::integral_constant<int, 0>{});
+        two(std::integral_constant<int, 2>{});
+      } else {
+        auto one = [&](auto ic) {
+          constexpr int i = decltype(ic)::value, d = i % kDepth;
+          Acts<FMT> x[1];
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          lo[j] = from_row<i>(sc[j].v[0]);
-          hi[j] = FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i>(sc[j].v[1]);
-        }
-        step<FMT, TT>(w[d], lo, hi, x, lut, acc);
-        __builtin_amdgcn_sched_barrier(0);
-        load(d, s0 + i + kDepth);
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      one(std::integral_constant<int, 0>{});
-      one(std::integral_constant<int, 1>{});
-      one(std::integral_constant<int, 2>{});
-      one(std::integral_constant<int, 3>{});
+          for (int v = 0; v < 4; ++v) x[0].set(v, xr[d][v]);
+          uint32_t lo[TT], hi[TT];
+#pragma unroll
+          for (int j = 0; j < TT; ++j) {
+            lo[j] = from_row<i>(sc[j].v[0]);
+            hi[j] = FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i>(sc[j].v[1]);
+          }
+          step<FMT, TT, 1>(w[d], lo, hi, x, lane8, acc);
+          __builtin_amdgcn_sched_barrier(0);
+          load(d, s0 + i + kDepth);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        one(std::integral_constant<int, 0>{});
+        one(std::integral_constant<int, 1>{});
+        one(std::integral_constant<int, 2>{});
+        one(std::integral_constant<int, 3>{});
+      }
     }
+    if constexpr (TT == 1) acc[0] = pair_acc[0] + pair_acc[1];
     // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2. The halves' sum of
     // tile mj to the lanes of mj.
     float v[4];
@@ -681,169 +726,241 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
 
 // ------------------------------------------------------------------ launch 2
 
-// 8 output columns to a workgroup. A unit is one expert's rows of a group of 8 tokens and a run of its
-// steps (1 KiB of weights each); wave v takes the units v, v + waves, ...,
-// step after step, DEPTH steps ahead of the arithmetic. A token's row of activations stands at the
-// token's place in the MFMA's first operand (zeros where it did not choose the expert), and h is
-// weighted, so a wave's sums over all experts stay in its accumulators, one set for each group. The
-// waves' sums are added in their order.
-template <int FMT, int GROUPS, int DEPTH, int THREADS>
-__global__ __launch_bounds__(THREADS) void k_layer_down(const LayerArgs a) {
+// A panel is 8 TT kSide output columns of a group of 8 tokens; its units are the experts that some of them
+// chose, each cut into runs of RS steps. kSide waves of a workgroup take 8 TT columns each of the same
+// unit, the others the units between; a unit's loads are asked for while the unit before is multiplied. A token's row
+// of activations stands at the token's place in the MFMA's first operand (zeros where it did not
+// choose the expert), and h is weighted, so a wave's sums over its units stay in its accumulators.
+// The waves' sums are added in their order.
+//
+// CUT: the units of all panels, in a row, are dealt evenly to the workgroups, which leaves none idle
+// where the panels are few or no multiple of the chip's 256 (8 tokens through 20 of 32 MXFP4 experts of
+// 2880 x 2880, 360 panels of 8 columns with a workgroup each, took 40 us, and 32 so; 16 tokens through
+// 81 NF4 experts of 2048 x 768, 256 panels, 34 either way). A panel that was cut is written in parts; who comes last (a counter for each panel, zeroed
+// by the first launch) adds them.
+template <int FMT, int TT, int RS, bool CUT>
+__global__ __launch_bounds__(512) void k_layer_down(const LayerArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  constexpr int nw = THREADS / 64;
+  // waves side by side in a panel, and those that share its units
+  constexpr int kSide = CUT ? 4 : 1, nw = 8 / kSide, kCols = 8 * TT * kSide;
   const int S = a.T * a.k;
-  const int wv = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-  // LDS: table | sums [nw][2][8 GROUPS][8] | uses [S]
+  const int wid = __builtin_amdgcn_readfirstlane(wave_id()), wv = wid / kSide, side = wid % kSide, l = lane_id();
+  // LDS: table | sums [nw][8][kCols] | uses [S] | experts and weights of the slots [S] (biases)
   uint8_t* lut = smem;
   float* sums = reinterpret_cast<float*>(smem + lut_bytes(FMT));
-  Use* uses = reinterpret_cast<Use*>(sums + nw * 2 * GROUPS * 64);
-  const int c0 = blockIdx.x * 8;
+  Use* uses = reinterpret_cast<Use*>(sums + nw * 8 * kCols);
+  int* slot_e = reinterpret_cast<int*>(uses + S);
+  float* slot_w = reinterpret_cast<float*>(slot_e + S);
+  int& s_last = *reinterpret_cast<int*>(slot_w + S);
   const int c = l & 7, q = (l >> 3) & 1, g = l >> 4;
-  const int count = a.count[0];
-  for (int i = threadIdx.x; i < S; i += THREADS)
-    if (i < count) uses[i] = a.uses[i];
+  int cnt[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) cnt[i] = __builtin_amdgcn_readfirstlane(a.count[i]);
+  const int used = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+  for (int i = threadIdx.x; i < S; i += 512) {
+    if (i < used) uses[i] = a.uses[i];
+    if (a.dn_bias) {
+      slot_e[i] = a.idx[i];
+      slot_w[i] = a.w[i];
+    }
+  }
   fill_lut<FMT>(lut, a.dn.book);
   __syncthreads();
-  // the biases' sum of the thread's output
-  float bias = 0.0f;
-  if (a.dn_bias && (int)threadIdx.x < a.T * 8) {
-    const int t = threadIdx.x >> 3, col = c0 + (threadIdx.x & 7);
-    for (int j = 0; j < a.k; ++j) {
-      const int s = t * a.k + j;
-      bias = fmaf(a.w[s], bf16_to_f32(a.dn_bias[(int64_t)a.idx[s] * a.H + col]), bias);
-    }
+  const int G = (a.H + kCols - 1) / kCols, steps = steps_of(a.I);
+  // this workgroup's units
+  const int64_t N = (int64_t)used * a.runs * G, W = min((int64_t)gridDim.x, N);
+  int64_t first, end;
+  if constexpr (CUT) {
+    if (blockIdx.x >= W) return;   // every workgroup that stays has a unit
+    first = N * blockIdx.x / W;
+    end = N * (blockIdx.x + 1) / W;
+  } else {
+    int tg = 0, skip = 0;
+    while ((int)blockIdx.x >= (tg + 1) * G) skip += cnt[tg++];
+    first = ((int64_t)skip * G + (int64_t)(blockIdx.x - tg * G) * cnt[tg]) * a.runs;
+    end = first + cnt[tg] * a.runs;
   }
-  const int steps = steps_of(a.I);
   const rsrc_t rh = make_rsrc_uniform(a.h, (uint32_t)(S * a.I * 2));
-  const int total = __builtin_amdgcn_readfirstlane(count) * a.runs;
   const float off = FMT == MOE4_FMT_NF4_DQ ? a.dn.soff[0] : 0.0f;
   const float* book = FMT == MOE4_FMT_NF4_DQ ? reinterpret_cast<const float*>(lut + 2048 * kLutCopies) : nullptr;
-  struct Step {
-    u32x4 w[1], x[4];
-    typename Stream<FMT>::Raw s;
-    int st, from;      // which of the run's steps, and the run's first
-    uint32_t tokens;   // of the group that chose the expert, as bits
-    int group;
-    bool first, last, on;
-  };
-  // where the loads are: unit, step, the end of its run, the lane's row
-  int at_u = wv, at_s = 0, from = 0, at_end = 0, group = 0, xoff = kOob;
-  uint32_t tokens = 0;
-  bool fresh = true;
+  const uint32_t lane8 = 8 * (l & (kLutCopies - 1));
   Stream<FMT> in;
   in.place(a.I, c, q);
-  auto open = [&] {
-    const bool on = at_u < total;
-    const int n = !on ? 0 : a.runs == 1 ? at_u : (int)__umulhi((uint32_t)at_u, a.per_run);   // at_u / runs
-    const int run = on ? at_u - n * a.runs : 0;
-    const uint32_t what = __builtin_amdgcn_readfirstlane(uses[n].what);
-    const uint32_t all = on ? __builtin_amdgcn_readfirstlane(uses[n].tokens) : 0u;
-    group = (what >> 10) & 3;
-    at_s = from = run * a.run_steps;
-    at_end = min(at_s + a.run_steps, steps);
-    fresh = true;
-    in.open(a.dn, what & 1023, c0, on);
-    tokens = all >> (8 * group) & 255u;
-    const int t = 8 * group + c;
-    const int r = (int)(what >> 12) + __popc(all & ((1u << t) - 1));
-    xoff = tokens >> c & 1 ? r * a.I * 2 : kOob;
-  };
-  auto load = [&](Step& u) {
-    u.on = at_u < total;
-    u.group = group;
-    u.tokens = tokens;
-    u.first = fresh;
-    fresh = false;
-    const int k = 128 * q + kStep * at_s;
-    u.w[0] = in.codes(a.I, at_s, 0, true);
-    u.st = at_s - from;
-    u.from = from;
-    in.scales(u.s, a.I, u.st ? steps + 4 : from, 0, true);   // (with a run's first step only)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // (MXFP4: the lane's 32 k are in K or not; NF4: a block of 64)
-      const int kk = FMT == MOE4_FMT_MXFP4 ? k + 32 * g : k + 64 * (i / 2);
-      u.x[i] = buf_load_b128(rh, xoff != kOob && kk < a.I ? xoff + 2 * (k + act_k<FMT>(i)) : kOob);
+
+  for (int64_t at = first; at < end;) {
+    // the panel that unit `at` belongs to: token group, column group, units, and where they begin
+    int tg = 0, skip = 0;
+    int64_t base = 0;
+    while (at >= base + (int64_t)cnt[tg] * a.runs * G) {
+      base += (int64_t)cnt[tg] * a.runs * G;
+      skip += cnt[tg++];
     }
-    u.last = ++at_s == at_end;
-    if (u.last && u.on) {
-      at_u += nw;
+    const int U = cnt[tg] * a.runs, cg = (int)((at - base) / U), u0 = (int)(at - base - (int64_t)cg * U);
+    const int n = (int)min(end - at, (int64_t)(U - u0)), c0 = cg * kCols, mine0 = c0 + 8 * TT * side;
+    // ---- the wave's units
+    u32x4 w[RS][TT], xr[RS][4];
+    typename Stream<FMT>::Raw raw[TT], sc[TT];
+    int u = u0 + wv, s0 = 0, xoff = kOob;
+    uint32_t tokens = 0;
+    auto open = [&] {
+      const bool on = u < u0 + n && mine0 < a.H;
+      const int i = on ? u / a.runs : 0;
+      const Use use = uses[skip + i];
+      const uint32_t what = __builtin_amdgcn_readfirstlane(use.what);
+      const uint32_t all = on ? __builtin_amdgcn_readfirstlane(use.tokens) : 0u;
+      s0 = on ? (u - i * a.runs) * a.run_steps : 0;
+      in.open(a.dn, what & 4095, on ? mine0 : 0, on);
+      tokens = all >> (8 * tg) & 255u;
+      const int r = (int)(what >> 12) + __popc(all & ((1u << (8 * tg + c)) - 1));
+      xoff = tokens >> c & 1 ? r * a.I * 2 : kOob;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) in.scales(raw[j], a.I, s0, 8 * j, on);
+    };
+    auto load = [&](int i) {   // (a run may have fewer steps than RS)
+      const int st = i < a.run_steps ? s0 + i : steps + 1;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) w[i][j] = in.codes(a.I, st, 8 * j, in.q_bytes != 0);
+      load_acts<FMT>(xr[i], rh, xoff, in.k0 + kStep * st, a.I);
+    };
+    f32x4 acc[TT], d[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    open();
+#pragma unroll
+    for (int i = 0; i < RS; ++i) load(i);
+    while (u < u0 + n) {
+      const uint32_t mine = tokens;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        sc[j] = raw[j];
+        in.finish(sc[j], a.I, s0, book, off);
+        d[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      u += nw;
       open();
-    }
-  };
-  f32x4 acc[GROUPS], d[1];
-  typename Stream<FMT>::Raw sc;
+      auto one = [&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i < RS) {
+          Acts<FMT> x[1];
 #pragma unroll
-  for (int i = 0; i < GROUPS; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto finish = [&](const Step& u) {
-    Acts<FMT> x;
+          for (int v = 0; v < 4; ++v) x[0].set(v, xr[i][v]);
+          uint32_t lo[TT], hi[TT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x.set(i, u.x[i]);
-    if (u.first) {
-      d[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      sc = u.s;
-      in.finish(sc, a.I, u.from, book, off);
-    }
-    const int at = (16 * u.st + (l & 15)) * 4;
-    const uint32_t s0[1] = {(uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)sc.v[0])};
-    const uint32_t s1[1] = {FMT == MOE4_FMT_MXFP4 ? 0u : (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)sc.v[1])};
-    step<FMT, 1>(u.w, s0, s1, x, lut, d);
-    if (u.last) {
-      // (a token that did not choose the expert takes nothing of it: its zeros times an infinite
-      // or NaN weight are no zeros)
-#pragma unroll
-      for (int i = 0; i < GROUPS; ++i)
-        if (GROUPS == 1 || u.group == i) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][r] += u.tokens >> (4 * (g & 1) + r) & 1 ? d[0][r] : 0.0f;
+          for (int j = 0; j < TT; ++j) {
+            lo[j] = from_row<i>(sc[j].v[0]);
+            hi[j] = FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i>(sc[j].v[1]);
+          }
+          step<FMT, TT, 1>(w[i], lo, hi, x, lane8, d);
+          __builtin_amdgcn_sched_barrier(0);
+          load(i);
+          __builtin_amdgcn_sched_barrier(0);
         }
+      };
+      one(std::integral_constant<int, 0>{});
+      one(std::integral_constant<int, 1>{});
+      one(std::integral_constant<int, 2>{});
+      one(std::integral_constant<int, 3>{});
+      // (a token that did not choose the expert takes nothing of it: its zeros times an infinite or
+      // NaN weight are no zeros)
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][r] += mine >> (4 * (g & 1) + r) & 1 ? d[j][r] : 0.0f;
     }
-  };
-  Step u[DEPTH];
-  open();
+    // ---- what the thread's output takes besides: residual, and the biases' sum
+    const int ot = 8 * tg + (int)threadIdx.x / kCols, oc = c0 + threadIdx.x % kCols;
+    const bool out = (int)threadIdx.x < 8 * kCols && ot < a.T && oc < a.H;
+    const int64_t oat = (int64_t)ot * a.H + oc;
+    float more = 0.0f;
+    if (out && a.dn_bias) {
+      for (int j0 = 0; j0 < a.k; j0 += 4) {
+        float b[4], v[4];
 #pragma unroll
-  for (int j = 0; j < DEPTH; ++j) load(u[j]);
-  while (u[0].on) {
+        for (int j = 0; j < 4; ++j) {
+          const int sl = ot * a.k + min(j0 + j, a.k - 1);
+          v[j] = j0 + j < a.k ? slot_w[sl] : 0.0f;
+          b[j] = bf16_to_f32(a.dn_bias[(int64_t)slot_e[sl] * a.H + oc]);
+        }
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) {
-      finish(u[j]);   // (a step past the last: zeros)
-      __builtin_amdgcn_sched_barrier(0);
-      load(u[j]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < 4; ++j) more = j0 + j < a.k ? fmaf(v[j], b[j], more) : more;
+      }
     }
-  }
-  // D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2
-  if ((g >> 1) == q) {
+    if (out && a.residual)
+      more += a.res_dtype == MOE4_DTYPE_F32 ? static_cast<const float*>(a.residual)[oat]
+                                            : bf16_to_f32(static_cast<const uint16_t*>(a.residual)[oat]);
+    // ---- D[m][n]: lane n = (c, q) holds rows m = 4 g .. 4 g + 3, those of half q' = g / 2. The halves'
+    // sum of tile mj to the lanes of mj.
+    const int mj = 2 * (g >> 1) + q;
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i)
+    for (int r = 0; r < 4; ++r) {
+      float v = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        sums[(((wv * 2 + q) * GROUPS + i) * 8 + 4 * (g & 1) + r) * 8 + c] = acc[i][r];
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < a.T * 8) {
-    const int t = threadIdx.x >> 3, col = c0 + (threadIdx.x & 7);
-    float v = bias;
+      for (int j = 0; j < TT; ++j) {
+        const uint32_t b = __float_as_uint(acc[j][r]);
+        const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);   // tokens' first, second half
+        const float own = __uint_as_float(q ? h[1] : h[0]);
+        const float sum = own + dpp_f32<0x128>(own);   // row_ror:8
+        v = j == 0 || mj == j ? sum : v;
+      }
+      if (mj < TT) sums[(wv * 8 + 4 * (g & 1) + r) * kCols + 8 * (TT * side + mj) + c] = v;
+    }
+    __syncthreads();
+    float v = 0.0f;
+    if ((int)threadIdx.x < 8 * kCols) {
 #pragma unroll
-    for (int p = 0; p < 2 * nw; ++p) v += sums[p * GROUPS * 64 + threadIdx.x];
-    const int64_t at = (int64_t)t * a.H + col;
-    if (a.residual)
-      v += a.res_dtype == MOE4_DTYPE_F32 ? static_cast<const float*>(a.residual)[at]
-                                         : bf16_to_f32(static_cast<const uint16_t*>(a.residual)[at]);
-    if (a.out_dtype == MOE4_DTYPE_F32) static_cast<float*>(a.out)[at] = v;
-    else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+      for (int p = 0; p < nw; ++p) v += sums[p * 8 * kCols + threadIdx.x];
+    }
+    bool done = true;
+    if constexpr (CUT) {
+      if (n < U) {
+        // workgroups i0 .. i1 have a part of the panel each, at place 2 i where it is the first thing
+        // they do, else (it is their last) at 2 i + 1
+        const int64_t p0 = base + (int64_t)cg * U;
+        const int64_t i0 = ((p0 + 1) * W - 1) / N, i1 = ((p0 + U) * W - 1) / N;
+        // Parts and counters are only touched by atomics of device scope, which go through to where
+        // all dies meet, in both directions; a part is there (its wave waits for that) before the
+        // barrier behind which the counter says so. (Fences of device scope, which write a die's whole
+        // cache back, took 140 us.)
+        if ((int)threadIdx.x < 8 * kCols) {
+          float* to = a.part + (2 * (int64_t)blockIdx.x + (at != first)) * 8 * kCols + threadIdx.x;
+          __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (threadIdx.x == 0)
+          s_last = __hip_atomic_fetch_add(&a.arrived[tg * G + cg], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == i1 - i0;
+        __syncthreads();
+        done = s_last;
+        if (done && (int)threadIdx.x < 8 * kCols) {
+          v = 0.0f;
+          for (int64_t i = i0; i <= i1; ++i) {
+            const float* from = a.part + (2 * i + (i == i0 && N * i / W < p0)) * 8 * kCols + threadIdx.x;
+            v += __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
+        }
+      }
+    }
+    if (done && out) {
+      if (a.out_dtype == MOE4_DTYPE_F32) static_cast<float*>(a.out)[oat] = v + more;
+      else static_cast<uint16_t*>(a.out)[oat] = f32_to_bf16(v + more);
+    }
+    at += n;
+    __syncthreads();   // the sums, and s_last, are used again
   }
 }
 
+constexpr int kDownRoom = 256;   // workgroups of the second launch where panels are cut
 struct LayerWs {
-  size_t idx, w, uses, count, end;
-  LayerWs(int I, int T, int k) {
+  size_t idx, w, uses, count, arrived, part, end;
+  LayerWs(int H, int I, int T, int k) {
     const size_t S = (size_t)T * k;
     idx = align_up(S * I * 2, 256);
     w = idx + align_up(S * 4, 256);
     uses = w + align_up(S * 4, 256);
     count = uses + align_up(S * sizeof(Use), 256);
-    end = count + 256;
+    arrived = count + 256;
+    part = arrived + align_up((size_t)((H + 63) / 64) * 4 * 4, 256);
+    end = part + (size_t)2 * kDownRoom * 8 * 64 * 4;
   }
 };
 
@@ -860,10 +977,14 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   const int S = a.T * a.k;
   constexpr bool kMx = FMT == MOE4_FMT_MXFP4;
   const int dsteps = steps_of(a.I);
-  a.runs = (dsteps + 3) / 4;
+  constexpr int kRun = kMx ? 4 : 3;   // (registers)
+  a.runs = (dsteps + kRun - 1) / kRun;
   a.run_steps = (dsteps + a.runs - 1) / a.runs;
   a.runs = (dsteps + a.run_steps - 1) / a.run_steps;
-  a.per_run = (uint32_t)(((uint64_t)1 << 32) / a.runs) + 1;
+  // two tiles share their activations where that leaves two units and more to every wave
+  const int groups = (a.T + 7) / 8;
+  const bool cut = (int64_t)(a.H / 16) * S * a.runs >= 2 * 8 * kDownRoom;
+  a.panels = cut ? (a.H + 63) / 64 * groups : 0;
   // as many workgroups as the chip holds at once, or a wave for every tile
   const int64_t tiles = (int64_t)S * (a.I / 4), room = 256;
   auto up = [&](auto* k) {
@@ -875,32 +996,34 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   };
   hipError_t e = a.E <= 128 ? up(&k_layer_up<FMT, 2>) : up(&k_layer_up<FMT, 16>);
   if (e != hipSuccess) return e;
-  auto down = [&](auto* k, int groups, int threads) {
-    const int bytes = lut_bytes(FMT) + threads / 64 * 2 * groups * 256 + S * (int)sizeof(Use);
+  auto down = [&](auto* k, int grid, int tt) {
+    const int bytes = lut_bytes(FMT) + 8 * 8 * 8 * tt * 4 + S * ((int)sizeof(Use) + 8) + 4;
     hipError_t r = allow_lds(k, bytes);
     if (r != hipSuccess) return r;
-    k<<<a.H / 8, threads, bytes, s>>>(a);
+    k<<<grid, 512, bytes, s>>>(a);
     return hipGetLastError();
   };
-  auto by_threads = [&](auto gc) {
-    constexpr int G = decltype(gc)::value;
-    return down(&k_layer_down<FMT, G, 3, 512>, G, 512);
+  auto by_steps = [&](auto rc) {
+    constexpr int RS = decltype(rc)::value;
+    if (cut) return down(&k_layer_down<FMT, 2, RS, true>, kDownRoom, 2);
+    return down(&k_layer_down<FMT, 1, RS, false>, a.H / 8 * groups, 1);
   };
-  if (a.T <= 8) return by_threads(std::integral_constant<int, 1>{});
-  if (a.T <= 16) return by_threads(std::integral_constant<int, 2>{});
-  return by_threads(std::integral_constant<int, 4>{});
+  if (a.run_steps <= 2) return by_steps(std::integral_constant<int, 2>{});
+  if constexpr (kRun == 4)
+    if (a.run_steps == 4) return by_steps(std::integral_constant<int, 4>{});
+  return by_steps(std::integral_constant<int, 3>{});
 }
 
 }  // namespace
 
-size_t layer_decode_ws_bytes(const moe4_experts& ex, int T, int k) { return LayerWs(ex.I, T, k).end; }
+size_t layer_decode_ws_bytes(const moe4_experts& ex, int T, int k) { return LayerWs(ex.H, ex.I, T, k).end; }
 
 hipError_t launch_layer_decode(const moe4_experts& ex, const uint16_t* x, const float* logits,
                                int T, int k, int renorm, const void* residual, int res_dtype,
                                void* out, int out_dtype, int32_t* topk_idx, float* topk_w,
                                void* ws, hipStream_t s) {
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
-  const LayerWs at(ex.I, T, k);
+  const LayerWs at(ex.H, ex.I, T, k);
   LayerArgs a = {};
   a.gu = {static_cast<const uint8_t*>(ex.gu_q), ex.gu_s, ex.gu_s2, ex.gu_soff, ex.dq_book, ex.H, 2 * ex.I};
   a.dn = {static_cast<const uint8_t*>(ex.dn_q), ex.dn_s, ex.dn_s2, ex.dn_soff, ex.dq_book, ex.I, ex.H};
@@ -929,6 +1052,8 @@ hipError_t launch_layer_decode(const moe4_experts& ex, const uint16_t* x, const 
   a.w = reinterpret_cast<float*>(w8 + at.w);
   a.uses = reinterpret_cast<Use*>(w8 + at.uses);
   a.count = reinterpret_cast<int32_t*>(w8 + at.count);
+  a.arrived = reinterpret_cast<int32_t*>(w8 + at.arrived);
+  a.part = reinterpret_cast<float*>(w8 + at.part);
   if (ex.format == MOE4_FMT_NF4) return launch_layer<MOE4_FMT_NF4>(a, s);
   if (ex.format == MOE4_FMT_MXFP4) return launch_layer<MOE4_FMT_MXFP4>(a, s);
   return launch_layer<MOE4_FMT_NF4_DQ>(a, s);

@@ -129,6 +129,71 @@ def test_layer_decode(fmt, E, k, H, I, layout, act, bias, T):
     check(Stacks("a", fmt, E, H, I, layout, act, bias), T, k, renorm=T != 7, res=(None, BF, F32)[T % 3])
 
 
+# enough units of work that the second launch cuts its panels: runs of 2, 3 and 4 steps, few and many
+# units to a panel (parts of one panel by many workgroups, many panels to one), groups of tokens
+@pytest.mark.parametrize("fmt,T,E,k,H,I,bias", [
+    ("nf4", 32, 24, 8, 1088, 320, True), ("nf4", 9, 64, 8, 2112, 832, False), ("nf4", 32, 128, 16, 256, 64, False),
+    ("nf4", 4, 128, 8, 2048, 768, True), ("mx4", 32, 40, 16, 160, 1312, True), ("mx4", 8, 32, 4, 2880, 1056, True),
+    ("mx4", 17, 300, 30, 160, 32, False), ("dq", 25, 12, 6, 1024, 1088, True), ("dq", 10, 64, 8, 1664, 448, False)])
+def test_layer_decode_many_units(fmt, T, E, k, H, I, bias):
+    assert (H // 16) * T * k >= 4096
+    st = Stacks("units", fmt, E, H, I, "interleaved" if bias else "halves", "clamped" if bias else "swiglu", bias)
+    x, lg, out = check(st, T, k, res=(BF, F32, None)[T % 3])
+    if T % 3 == 2:   # (without a residual) the same bits again, whoever came last
+        ws = st.ws(T, k)
+        for _ in range(3):
+            again = torch.full_like(out, float("nan"))
+            moe4.moe4_layer_decode(st.ex, x, to_dev(lg), k, again, ws=ws)
+            assert torch.equal(again, out)
+
+
+def test_many_units_of_one_expert_and_of_all():
+    for E, k in ((1, 1), (16, 16)):
+        st = Stacks("all", "mx4", E, 2080, 2080)
+        check(st, 32, k)
+
+
+def test_many_units_captured_and_two_at_once():
+    st = Stacks("cap", "nf4", 48, 1088, 256)
+    T, k = 16, 8
+    buf = [dict(x=torch.zeros((T, 1088), dtype=BF, device="cuda"), lg=torch.zeros((T, 48), device="cuda"),
+                out=torch.zeros((T, 1088), dtype=BF, device="cuda"), ws=st.ws(T, k)) for _ in range(2)]
+
+    def fill(b, key):
+        r = rng("cap fill", key)
+        b["x"].copy_(draw(r, (T, 1088))[0])
+        b["lg"].copy_(to_dev(r.standard_normal((T, 48)).astype(np.float32)))
+        b["out"].fill_(float("nan"))
+
+    def run(b, stream=None):
+        moe4.moe4_layer_decode(st.ex, b["x"], b["lg"], k, b["out"], ws=b["ws"], stream=stream)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(buf[0])
+    want = []
+    for key in range(3):
+        fill(buf[0], key)
+        g.replay()
+        torch.cuda.synchronize()
+        got = buf[0]["out"].clone()
+        buf[0]["out"].fill_(float("nan"))
+        run(buf[0])
+        assert torch.equal(got, buf[0]["out"]) and bool(torch.isfinite(got).all())
+    for i in (0, 1):
+        fill(buf[i], 10 + i)
+        run(buf[i])
+        want.append(buf[i]["out"].clone())
+        buf[i]["out"].fill_(float("nan"))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            run(buf[i], s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(buf[i]["out"], want[i]) for i in (0, 1))
+
+
 @pytest.mark.parametrize("fmt", ["nf4", "mx4", "dq"])
 def test_every_token_takes_the_same_experts(fmt):
     # rows of one expert over several passes of 8; every expert chosen (k = E); one expert
