@@ -39,6 +39,14 @@ struct RowWeight {
   }
 };
 
+// the sum of 8 squares, in pairs: three additions deep, not eight
+__device__ __forceinline__ float squares8(const float* v) {
+  float p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = fmaf(v[2 * i], v[2 * i], v[2 * i + 1] * v[2 * i + 1]);
+  return (p[0] + p[1]) + (p[2] + p[3]);
+}
+
 struct JoinNormArgs {
   const void *b, *res;
   float res_scale, block_scale;
@@ -88,8 +96,7 @@ __global__ __launch_bounds__(kNormThreads<W>) void k_join_norm(const JoinNormArg
       for (int i = 0; i < NV; ++i) {
         float v[8];
         b[i].get(v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+        ss += squares8(v);
       }
       ss = row_sum<W>(ss, red, slot);
       slot ^= 1;
@@ -109,8 +116,7 @@ __global__ __launch_bounds__(kNormThreads<W>) void k_join_norm(const JoinNormArg
       for (int k = 0; k < 8; ++k) u[k] = fmaf(a.res_scale, u[k], c * (a.wo ? v[k] * w[k] : v[k]));
       r[i].set(u);
       r[i].get(u);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(u[k], u[k], ss);
+      ss += squares8(u);
     }
     if (a.sum) {
       const rsrc_t rs = row_rsrc<DS>(a.sum, row, a.H);
@@ -329,9 +335,11 @@ __global__ __launch_bounds__(kNormThreads<W>) void k_join_norm_bwd(const JoinNor
     }
 }
 
+// A workgroup to a row (us, us with at most 2048 workgroups: 4096 rows of 2880 25, 28, 16384 83, 100), but
+// for the widest rows, whose workgroups keep their weights (4096 of 16384: 135, 120 with 512).
 int join_blocks(int64_t T, int W) {
   const int64_t rows = W == 1 ? (T + 3) / 4 : T;
-  const int64_t most = W == 16 ? 512 : 2048;
+  const int64_t most = W == 16 ? 512 : 1 << 20;
   return (int)(rows < most ? rows : most);
 }
 // the backward's workgroups each leave two rows of partial sums: fewer of them
