@@ -366,6 +366,8 @@ struct GradCodes {
   }
 };
 
+// The k loop as of the bf16 product above, in two stages of 64 weight rows each: tile kt + 2 is
+// written to LDS (the weights) and asked for (the activations) as tile kt leaves it.
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_linear_dx(const FfnProduct p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
@@ -460,6 +462,33 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_linear_dx(const FfnProduct p
   }
   wait_vmcnt<0>();
   ffn_product_end<S>(p, acc, a0, b0, split, lds);
+}
+
+// Column sums of a bf16 matrix [T, N] of few rows, in one launch: 64 columns, a line, to a workgroup, whose
+// 32 groups of eight threads take every 32nd row and meet in LDS in their order.
+__global__ __launch_bounds__(256) void k_bias_grad(const uint16_t* m, int T, int N, void* out, int dtype) {
+  __shared__ __attribute__((aligned(16))) float red[32][68];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3, at = blockIdx.x * 64 + c * 8;
+  float s[8] = {};
+  if (at < N) {
+#pragma unroll 8
+    for (int r = g; r < T; r += 32) {
+      float v[8];
+      load8_bf16(m + (int64_t)r * N + at, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += v[i];
+    }
+  }
+  *reinterpret_cast<f32x4*>(&red[g][c * 8]) = f32x4{s[0], s[1], s[2], s[3]};
+  *reinterpret_cast<f32x4*>(&red[g][c * 8 + 4]) = f32x4{s[4], s[5], s[6], s[7]};
+  __syncthreads();
+  const int col = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || col >= N) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v += red[i][threadIdx.x];
+  if (dtype == MOE4_DTYPE_F32) static_cast<float*>(out)[col] = v;
+  else static_cast<uint16_t*>(out)[col] = f32_to_bf16(v);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -681,11 +710,12 @@ int linear_variant(const moe4_linear& l, int64_t T) {
 
 }  // namespace
 
+// where the bias gradient's one launch takes less than two (us at N 4096: 128 rows 4.0 and 6.8, 512 7.5 and 9.1)
+constexpr int kFewRows = 512;
+
 size_t linear_ws_bytes(const moe4_linear& l, int64_t T, bool backward) {
-  if (!backward) {
-    const int64_t most = (l.N + 127) / 128 > 128 ? 1 : most_lin_splits(l.K, kXB);
-    return (size_t)part_bytes(l.N, T, most);
-  }
+  // (forward: at most 256 workgroups, each of 128 columns or fewer)
+  if (!backward) return (size_t)part_bytes(l.N, T, (l.N + 127) / 128 > 128 ? 1 : most_lin_splits(l.K, kXB));
   return align_up((size_t)part_bytes(l.K, T, most_k_splits(l.K, l.N, 2)), 256) + (size_t)kColParts * l.N * 4;
 }
 
@@ -734,17 +764,19 @@ hipError_t launch_linear_backward(const moe4_linear& l, const uint16_t* dy, int 
     p.add_dtype = dx_add ? add_dtype : MOE4_DTYPE_BF16;
     p.out = dx;
     p.out_dtype = dx_dtype;
+    // (128 x 128 tiles and their rule: the smaller ones' conversions serve half the tokens, and 512
+    // tokens at 4096 took 50 us with them, 38 so; 256 x 128 80, 2048 tokens, and 77 so)
     p.splits = k_splits(tiles_of<Tile128>(l.K, T), l.N, 2);
     p.part = part;
-    auto run = [&](auto* k, int64_t tiles, int threads, int bytes) {
-      hipError_t e = allow_lds(k, bytes);
+    auto run = [&](auto sc) {
+      using S = decltype(sc);
+      auto* k = &k_linear_dx<S>;
+      hipError_t e = allow_lds(k, S::kLds);
       if (e != hipSuccess) return e;
-      k<<<(uint32_t)(tiles * p.splits), threads, bytes, s>>>(p);
+      k<<<(uint32_t)(tiles_of<S>(l.K, T) * p.splits), S::kThreads, S::kLds, s>>>(p);
       return hipGetLastError();
     };
-    hipError_t e = p.splits == 1 && large_tiles_for(l.K, T)
-                       ? run(&k_linear_dx<Tile256>, tiles_of<Tile256>(l.K, T), Tile256::kThreads, Tile256::kLds)
-                       : run(&k_linear_dx<Tile128>, tiles_of<Tile128>(l.K, T), Tile128::kThreads, Tile128::kLds);
+    hipError_t e = p.splits == 1 && large_tiles_for(l.K, T) ? run(Tile256{}) : run(Tile128{});
     if (e == hipSuccess && p.splits > 1) {
       JoinArgs j = {};
       j.p[0] = p;
@@ -753,6 +785,10 @@ hipError_t launch_linear_backward(const moe4_linear& l, const uint16_t* dy, int 
     if (e != hipSuccess) return e;
   }
   if (!db) return hipSuccess;
+  if (T <= kFewRows) {
+    k_bias_grad<<<(l.N + 63) / 64, 256, 0, s>>>(dy, T, l.N, db, db_dtype);
+    return hipGetLastError();
+  }
   return launch_col_sums(dy, T, l.N, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + parts), db, db_dtype, s);
 }
 
