@@ -289,7 +289,10 @@ __device__ __forceinline__ void lin_loop(f32x16 (&acc)[S::TA][S::TB], uint8_t* l
   wait_vmcnt<0>();   // the zeros of the tiles past the last, before the stages are used again
 }
 
-// FfnProduct: A the weight (p codes, s scales), B the activations; K in values
+// FfnProduct: A the weight (p codes, s scales), B the activations; K in values. Bf16, 2048 tokens at N = K =
+// 4096: 60 us, 1.15 PFLOP/s (a library bf16 product of the same shape 59, and 47 here without the loads).
+// MXFP4, 8192 tokens, N 8192, K 4096: 170 us, 3.2 PFLOP/s: a 256 x 256 tile takes 64 KiB from L2 for every
+// 2048 cycles of its matrix instructions, and the chip's tiles together 6.3 TB/s.
 template <typename S, int XF>
 __global__ __launch_bounds__(S::kThreads, 2) void k_linear(const FfnProduct p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
@@ -367,7 +370,8 @@ struct GradCodes {
 };
 
 // The k loop as of the bf16 product above, in two stages of 64 weight rows each: tile kt + 2 is
-// written to LDS (the weights) and asked for (the activations) as tile kt leaves it.
+// written to LDS (the weights) and asked for (the activations) as tile kt leaves it. 4095 tokens at 4096:
+// 112 us, 1.23 PFLOP/s, 60% of the cycles of the matrix cores at the clock the load allows.
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_linear_dx(const FfnProduct p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t stage_mem[];
@@ -496,7 +500,9 @@ __global__ __launch_bounds__(256) void k_bias_grad(const uint16_t* m, int T, int
 // One workgroup takes 16 RT weight rows and NT tiles of 16 tokens; its eight waves split K, 128 k
 // (four blocks) a step, and meet in LDS in their order. A lane holds a block of its weight row a
 // step, as the operands of four MFMAs, and its tokens' same 32 k; all are multiplied as bf16
-// (MXFP8 and MXFP4 are exact there). The next batch of steps is in flight while one is multiplied.
+// (MXFP8 and MXFP4 are exact there). The next batch of steps is in flight while one is multiplied. One
+// token, N 5760, K 2880 (8.8 MB): 5.6 us, of which a launch takes 2.1 and the bytes 1.7 at a copy's rate;
+// the rest is one round trip to HBM and the waves' meeting.
 template <int RT, int NT, int XF>
 struct LinSkinny {
   static constexpr int KS = 8, kThreads = KS * 64;
@@ -650,8 +656,12 @@ hipError_t launch_skinny(const FfnProduct& p, hipStream_t s) {
     k<<<dim3((p.na + 16 * RT - 1) / (16 * RT), (p.nb + 16 * NT - 1) / (16 * NT)), 512, C::kLds, s>>>(p);
     return hipGetLastError();
   };
-  // more row tiles save token loads, as long as there is a workgroup for most CUs
-  if (p.na >= 32 * 192) return run(std::integral_constant<int, 2>{});
+  // More row tiles save token loads, as long as there is a workgroup for most CUs. Us with 1, 2 and 4, bf16:
+  // N 4096, K 4096 T 1 5.5 7.3 11.1; N 5760, K 2880 T 1 5.9 5.6 7.9, 16 9.1 7.5 10.2; N 16384, K 4096 T 1
+  // 13.9 14.2 13.5, 16 24 20 16.6; MXFP8 there T 1 12.9 12.0 13.4, 16 21 16 16.
+  if constexpr (XF != kX8 || NT == 1)   // (the other's operands do not fit the registers)
+    if (p.na >= 64 * 192 && p.nb > 8) return run(std::integral_constant<int, 4>{});
+  if (p.na >= 32 * 160) return run(std::integral_constant<int, 2>{});
   return run(std::integral_constant<int, 1>{});
 }
 
@@ -703,9 +713,14 @@ hipError_t launch_tiled(const FfnProduct& p, hipStream_t s) {
   return launch_join(j, 1, s);
 }
 
+// Tiles or few tokens: a tile costs the same for one token as for its 64, the skinny kernels read the
+// tokens for every 16 to 64 weight rows. Us, skinny and tiled, bf16: N 5760, K 2880, T 16 7.5 12.3, 32 10.1
+// 12.8; N 4096, K 4096, T 32 11.8 13.4, 48 17.8 14.7; N 16384, K 4096, T 16 16.6 18.7, 32 21.1 19.2; N 1024,
+// K 1024, T 64 4.7 8.4 (MXFP8 4.8 7.0, MXFP4 4.3 6.2).
 int linear_variant(const moe4_linear& l, int64_t T) {
   if (l.variant != MOE4_VARIANT_AUTO) return l.variant;
-  return T <= 32 ? MOE4_VARIANT_SKINNY : MOE4_VARIANT_TILED;
+  const bool few = T <= 32 && T * l.N <= 384 << 10, small = T <= 64 && (T + 31) / 32 * ((l.N + 15) / 16) <= 256;
+  return few || small ? MOE4_VARIANT_SKINNY : MOE4_VARIANT_TILED;
 }
 
 }  // namespace

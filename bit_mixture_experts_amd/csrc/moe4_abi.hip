@@ -1098,8 +1098,8 @@ static int check_linear(const moe4_linear* l, int32_t T) {
     return fail(MOE4_ESHAPE, "T = %d: the skinny variant takes at most 2^20 tokens", T);
   if (T * (wide / 32) >= kByteSpan)
     return fail(MOE4_ESHAPE, "T = %d: the activations' scales must stay under 2 GiB", T);
-  // workgroups of the smallest tiles, 256 threads each, in one 32-bit launch
-  if (((int64_t)T + 127) / 128 * ((wide + 127) / 128) >= (int64_t)1 << 23)
+  // workgroups of the smallest tiles (128 x 64), 256 threads each, in one 32-bit launch
+  if (((int64_t)T + 63) / 64 * ((wide + 127) / 128) >= (int64_t)1 << 23)
     return fail(MOE4_ESHAPE, "T = %d with max(N, K) = %lld is beyond one launch", T, (long long)wide);
   return MOE4_OK;
 }

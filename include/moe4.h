@@ -685,11 +685,13 @@ enum { MOE4_LAYER_MOST_TOKENS = 32, MOE4_LAYER_MOST_SLOTS = 512 };
  *   top-k of the logits as moe4_route takes it, then for each slot
  *   h = act(W_gu[e] x + b_gu[e]), and
  *   out[t] = sum_j w[t, j] * (W_d[e] h + b_d[e]) (+ residual[t])
- * Each expert that tokens chose is read once for every 8 of them. Weights are not
- * rounded (MXFP4 is exact, NF4's level * absmax is multiplied to 2^-17, where
+ * W_gu of an expert that tokens chose is read once for every 8 of them, W_d once
+ * for every group of 8 tokens (0 .. 7, 8 .. 15, ...) that holds one. Weights are
+ * not rounded (MXFP4 is exact, NF4's level * absmax is multiplied to 2^-17, where
  * moe4_expert_forward rounds the product to bf16), sums are fp32 in a fixed order,
- * h is rounded once to bf16, out once to its type. A token's NaN stays with it. For more tokens, adapters, or what a backward pass needs:
- * moe4_route_permute, moe4_expert_forward_gather and moe4_combine.
+ * w h is rounded once to bf16, out once to its type. A token's NaN stays with it.
+ * For more tokens, adapters, or what a backward pass needs: moe4_route_permute,
+ * moe4_expert_forward_gather and moe4_combine.
  *   ex: without adapters (else MOE4_EUNSUPPORTED); variant AUTO or SKINNY; NF4_DQ
  *   with H and I up to 16384
  *   x bf16 [T, H] (16-byte aligned), logits f32 [T, E], 1 <= k <= E, T <=

@@ -67,7 +67,7 @@ def check(wt, fmt, T, variant, out_dtype, res_dtype, key=0):
     return used
 
 
-CASES = [(1, 8, 32), (1, 64, 64), (2, 72, 96), (3, 16, 288), (16, 264, 160), (17, 136, 544), (31, 6152, 96),
+CASES = [(1, 8, 32), (1, 64, 64), (9, 12296, 64), (32, 12328, 160), (2, 72, 96), (3, 16, 288), (16, 264, 160), (17, 136, 544), (31, 6152, 96),
          (5, 6168, 288), (32, 40, 2880), (33, 520, 256), (64, 136, 320), (127, 392, 1056), (129, 264, 512),
          (300, 200, 1312), (513, 392, 800)]
 
@@ -77,7 +77,7 @@ CASES = [(1, 8, 32), (1, 64, 64), (2, 72, 96), (3, 16, 288), (16, 264, 160), (17
 def test_linear_forward(T, N, K, fmt):
     wt = Weight("fwd", N, K, bias=T % 2 == 1)
     used = check(wt, fmt, T, moe4.MOE4_VARIANT_AUTO, BF, BF if N % 16 else F32)
-    assert used == (SKINNY if T <= 32 else TILED)
+    assert used == (SKINNY if T <= 32 and T * N <= 384 * 1024 or T <= 64 and N <= 2048 else TILED)
     for v in (SKINNY, TILED):
         assert check(wt, fmt, T, v, F32, F32 if T % 3 else None) == v
 
