@@ -260,6 +260,23 @@ __device__ __forceinline__ void load_acts(u32x4 (&x)[4], rsrc_t r, int off, int 
   }
 }
 
+// the same from a row in LDS; past K zeros
+template <int FMT>
+__device__ __forceinline__ void read_acts(u32x4 (&x)[4], const uint8_t* row, int k, int K) {
+  constexpr int kEach = FMT == MOE4_FMT_MXFP4 ? 4 : 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += kEach) {
+    const int kk = k + act_k<FMT>(i);
+    const bool on = kk < K;
+    const uint8_t* p = row + (on ? 2 * kk : 0);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + (on ? 2 * (act_k<FMT>(i + j) - act_k<FMT>(i)) : 0));
+      x[i + j] = on ? v : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+}
+
 // acc += one step's products of TT tiles (which share their activations, or with NX = TT are so many
 // steps of one tile, whose acc are to be added); s0, s1: their scales (NF4 two fp32, MXFP4 the four bytes in
 // s0). MXFP4: the lane's 32 k are one block, each weight exact in bf16. NF4: the codes are put in
@@ -432,14 +449,22 @@ struct Keys {
 // after the routing. (The waves of a workgroup splitting k of the same tiles, with a barrier
 // and a sum through LDS for each 16 pairs, took as
 // long for many tokens and 2 us more for one.) Us: 16 tokens through 81 of 128 NF4 experts of 2048 x
-// 768 51 (143 MB; 9 of them routing and table), 8 through 20 of 32 MXFP4 experts of 2880 x 2880 50 (180
+// 768 51 (143 MB; 9 of them routing and table), 8 through 20 of 32 MXFP4 experts of 2880 x 2880 46 (180
 // MB), one token 13. Without the arithmetic and the activations the loads alone take 41, 42 and 9.
 
 // LDS of the first launch, after the table: tokens of an expert [E] as bits, its first
 // row [E], entries [S], tokens and weights of the rows [S], experts and weights of the slots [S], how many entries
 __host__ __device__ constexpr int route_lds(int E, int S) { return 8 * E + 20 * S + 4; }
 
-template <int FMT, int NPL>
+//
+// XL (MXFP4): the tokens' activations stand in LDS (x_lds bytes), where they fit, instead of being loaded
+// by every wave in the matrix instruction's layout, which takes four loads beside a step's weights (8
+// tokens through 20 experts of 2880 x 2880 50 us, 46 so; NF4, whose lookups keep LDS busy, 51 either
+// way).
+constexpr int kXPad = 32;   // bytes between rows: the rows of a read in different banks
+__host__ __device__ constexpr int x_lds(int T, int H) { return T * (2 * H + kXPad); }
+
+template <int FMT, int NPL, bool XL>
 __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   constexpr int nw = 8;
@@ -454,6 +479,7 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
   int* slot_e = reinterpret_cast<int*>(row_w + S);
   float* slot_w = reinterpret_cast<float*>(slot_e + S);
   int& s_count = *reinterpret_cast<int*>(slot_w + S);
+  uint8_t* const xs = smem + (lut_bytes(FMT) + route_lds(a.E, S) + 15) / 16 * 16;
   const int steps = steps_of(a.H);
   const int c = l & 7, q = (l >> 3) & 1, g = l >> 4;   // a weight column (c, q), an activation row (t, q)
   const bool writer = blockIdx.x == 0;                 // hands the routing on
@@ -511,6 +537,20 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
     }
   };
   fetch(wv);
+  if constexpr (XL) {
+    const int per = a.H / 8;   // 16-byte pieces of a row
+    for (int i0 = threadIdx.x; i0 < a.T * per; i0 += 4 * 512) {
+      u32x4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        v[u] = reinterpret_cast<const u32x4*>(a.x)[min(i0 + u * 512, a.T * per - 1)];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * 512, t = i / per;
+        if (i < a.T * per) *reinterpret_cast<u32x4*>(xs + t * (2 * a.H + kXPad) + (i - t * per) * 16) = v[u];
+      }
+    }
+  }
   for (int i = blockIdx.x * 512 + threadIdx.x; i < a.panels; i += gridDim.x * 512) a.arrived[i] = 0;
   if (a.T == 1) {
     // an expert's rows are one row each, in the order of the choice
@@ -589,10 +629,13 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
   // TT tiles (n of them there) from tile j0 of an entry on
   auto run = [&](auto tc, uint32_t entry, int j0, int n) {
     constexpr int TT = decltype(tc)::value;
-    constexpr int kDepth = TT > 2 ? 2 : 4;   // steps in flight
+    constexpr int kDepth = TT > 2 ? 2 : 4;               // steps in flight
+    constexpr int kX = !XL ? kDepth : TT == 1 ? 2 : 1;   // of activations (in LDS: those of the next product)
     const int rows = entry_rows(entry);
     in.open(a.gu, entry_expert(entry), 4 * j0 * mult, true);
-    const int xoff = c < rows ? row_t[entry_first(entry) + c] * a.H * 2 : kOob;
+    // the lane's row of activations (XL: of those that are there, which the product has no more rows than)
+    const int tok = row_t[entry_first(entry) + (c < rows ? c : 0)];
+    const int xoff = XL ? tok * (2 * a.H + kXPad) : c < rows ? tok * a.H * 2 : kOob;
     // the lane's tile, pair and tokens at the end: tile 2 (g / 2) + q, pair c & 3 (gates in lanes c < 4),
     // tokens 4 (g % 2) ...
     const int mj = 2 * (g >> 1) + q, pair = 4 * (j0 + mj) + (c & 3);
@@ -602,12 +645,15 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
       const int at = c < 4 ? gate_row(a.layout, a.I, pair) : up_row(a.layout, a.I, pair);
       bias = __builtin_amdgcn_raw_buffer_load_b16(rb, mj < n ? 2 * at : kOob, 0, 0);
     }
-    u32x4 w[kDepth][TT], xr[kDepth][4];
+    u32x4 w[kDepth][TT], xr[kX][4];
     typename Stream<FMT>::Raw sc[TT], next[TT];
-    auto load = [&](int d, int st) {
+    auto load_w = [&](int d, int st) {
 #pragma unroll
       for (int j = 0; j < TT; ++j) w[d][j] = in.codes(a.H, st, 4 * j * mult, j < n);
-      load_acts<FMT>(xr[d], rx, xoff, in.k0 + kStep * st, a.H);
+    };
+    auto load_x = [&](int d, int st) {
+      if constexpr (XL) read_acts<FMT>(xr[d], xs + xoff, in.k0 + kStep * st, a.H);
+      else load_acts<FMT>(xr[d], rx, xoff, in.k0 + kStep * st, a.H);
     };
     f32x4 acc[TT], pair_acc[2];
     pair_acc[0] = pair_acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -617,7 +663,10 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
       in.scales(next[j], a.H, 0, 4 * j * mult, j < n);
     }
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(d, d);
+    for (int d = 0; d < kDepth; ++d) {
+      load_w(d, d);
+      if (d < kX) load_x(d, d);
+    }
     for (int s0 = 0; s0 < steps; s0 += 4) {
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
@@ -632,8 +681,12 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
           Acts<FMT> x[2];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            x[0].set(v, xr[i][v]);
-            x[1].set(v, xr[i + 1][v]);
+            x[0].set(v, xr[i % kX][v]);
+            x[1].set(v, xr[(i + 1) % kX][v]);
+          }
+          if constexpr (XL) {
+            load_x(0, s0 + i + 2);
+            load_x(1, s0 + i + 3);
           }
           const u32x4 both[2] = {w[i][0], w[i + 1][0]};
           const uint32_t lo[2] = {from_row<i>(sc[0].v[0]), from_row<i + 1>(sc[0].v[0])};
@@ -641,8 +694,12 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
                                   FMT == MOE4_FMT_MXFP4 ? 0u : from_row<i + 1>(sc[0].v[1])};
           step<FMT, 2, 2>(both, lo, hi, x, lane8, pair_acc);
           __builtin_amdgcn_sched_barrier(0);
-          load(i, s0 + i + 4);
-          load(i + 1, s0 + i + 5);
+          load_w(i, s0 + i + 4);
+          load_w(i + 1, s0 + i + 5);
+          if constexpr (!XL) {
+            load_x(i, s0 + i + 4);
+            load_x(i + 1, s0 + i + 5);
+          }
           __builtin_amdgcn_sched_barrier(0);
         };
         two(std::integral_constant<int, 0>{});
@@ -652,7 +709,8 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
           constexpr int i = decltype(ic)::value, d = i % kDepth;
           Acts<FMT> x[1];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) x[0].set(v, xr[d][v]);
+          for (int v = 0; v < 4; ++v) x[0].set(v, xr[d % kX][v]);
+          if constexpr (XL) load_x(0, s0 + i + 1);
           uint32_t lo[TT], hi[TT];
 #pragma unroll
           for (int j = 0; j < TT; ++j) {
@@ -661,7 +719,8 @@ __global__ __launch_bounds__(512) void k_layer_up(const LayerArgs a) {
           }
           step<FMT, TT, 1>(w[d], lo, hi, x, lane8, acc);
           __builtin_amdgcn_sched_barrier(0);
-          load(d, s0 + i + kDepth);
+          load_w(d, s0 + i + kDepth);
+          if constexpr (!XL) load_x(d, s0 + i + kDepth);
           __builtin_amdgcn_sched_barrier(0);
         };
         one(std::integral_constant<int, 0>{});
@@ -758,7 +817,7 @@ __global__ __launch_bounds__(512) void k_layer_down(const LayerArgs a) {
   for (int i = 0; i < 4; ++i) cnt[i] = __builtin_amdgcn_readfirstlane(a.count[i]);
   const int used = cnt[0] + cnt[1] + cnt[2] + cnt[3];
   for (int i = threadIdx.x; i < S; i += 512) {
-    if (i < used) uses[i] = a.uses[i];
+    uses[i] = a.uses[i];   // (those past the last are never looked at; not to wait for how many there are)
     if (a.dn_bias) {
       slot_e[i] = a.idx[i];
       slot_w[i] = a.w[i];
@@ -985,16 +1044,21 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   const int groups = (a.T + 7) / 8;
   const bool cut = (int64_t)(a.H / 16) * S * a.runs >= 2 * 8 * kDownRoom;
   a.panels = cut ? (a.H + 63) / 64 * groups : 0;
-  // as many workgroups as the chip holds at once, or a wave for every tile
+  // as many workgroups as the chip holds at once (some of their waves idle where tiles are few), or one
+  // for every tile
   const int64_t tiles = (int64_t)S * (a.I / 4), room = 256;
+  const int lds = (lut_bytes(FMT) + route_lds(a.E, S) + 15) / 16 * 16;
+  const bool xl = kMx && lds + x_lds(a.T, a.H) <= 160 * 1024;
   auto up = [&](auto* k) {
-    const int bytes = lut_bytes(FMT) + route_lds(a.E, S);
+    const int bytes = lds + (xl ? x_lds(a.T, a.H) : 0);
     hipError_t e = allow_lds(k, bytes);
     if (e != hipSuccess) return e;
-    k<<<(uint32_t)((tiles + 7) / 8 < room ? (tiles + 7) / 8 : room), 512, bytes, s>>>(a);
+    k<<<(uint32_t)(tiles < room ? tiles : room), 512, bytes, s>>>(a);
     return hipGetLastError();
   };
-  hipError_t e = a.E <= 128 ? up(&k_layer_up<FMT, 2>) : up(&k_layer_up<FMT, 16>);
+  hipError_t e;
+  if (xl) e = a.E <= 128 ? up(&k_layer_up<FMT, 2, kMx>) : up(&k_layer_up<FMT, 16, kMx>);
+  else e = a.E <= 128 ? up(&k_layer_up<FMT, 2, false>) : up(&k_layer_up<FMT, 16, false>);
   if (e != hipSuccess) return e;
   auto down = [&](auto* k, int grid, int tt) {
     const int bytes = lut_bytes(FMT) + 8 * 8 * 8 * tt * 4 + S * ((int)sizeof(Use) + 8) + 4;

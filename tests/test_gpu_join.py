@@ -323,3 +323,41 @@ def test_join_norm_no_rows_and_refusals():
                        ((None, None, b, None, None, b), {}, moe4.Moe4Error)):
         with pytest.raises(err):
             moe4.moe4_join_norm_backward(*a, **kw)
+
+
+def test_join_offsets_past_32_bits():
+    # tensors of more than 2^32 bytes: the last rows are those of a call on them alone
+    H, T, tail = 2048, 1_060_000, 300
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    b = torch.randn((T, H), generator=gen, device="cuda", dtype=BF)
+    res = torch.randn((T, H), generator=gen, device="cuda", dtype=BF)
+    w = torch.ones(H, device="cuda", dtype=BF)
+    e = lambda n, *s, dtype=BF: torch.empty((n, *s), dtype=dtype, device="cuda")   # noqa: E731
+
+    def run(b, res, n):
+        s, q, qs = e(n, H), e(n, H // 32, 16, dtype=torch.uint8), e(n, H // 32, dtype=torch.uint8)
+        ro, ri = e(n, dtype=F32), e(n, dtype=F32)
+        moe4.moe4_join_norm(b, w, 1e-6, residual=res, w_post=w, sum_out=s, out_q=q, out_s=qs, rstd_post=ro, rstd_pre=ri)
+        return s, q, qs, ro, ri
+    big, small = run(b, res, T), run(b[-tail:].clone(), res[-tail:].clone(), tail)
+    # (another number of rows takes another split of the row's sum: c = rstd differs by few steps of
+    # 2^-24 of H terms, s by that and, where it falls at a border, by one bf16 step)
+    assert torch.allclose(big[3][-tail:], small[3], rtol=2 * (H + 8) * U32, atol=0)
+    assert torch.allclose(big[0][-tail:].float(), small[0].float(), rtol=2.0 ** -7, atol=1e-4)
+    assert (big[1][-tail:] != small[1]).float().mean() < 1e-2 and (big[2][-tail:] != small[2]).float().mean() < 1e-2
+    x = big[0]
+    q, qs = e(T, H // 32, 16, dtype=torch.uint8), e(T, H // 32, dtype=torch.uint8)
+    moe4.moe4_quantize_mxfp4(x, q, qs)
+    q2, s2 = e(tail, H // 32, 16, dtype=torch.uint8), e(tail, H // 32, dtype=torch.uint8)
+    moe4.moe4_quantize_mxfp4(x[-tail:].clone(), q2, s2)
+    assert torch.equal(q[-tail:], q2) and torch.equal(qs[-tail:], s2)
+    db, dres = torch.empty_like(b), torch.empty_like(b)
+    kw = dict(w_post=w)
+    moe4.moe4_join_norm_backward(res, x, b, w, big[4], db, dres=dres, rstd_post=big[3], **kw)
+    d2, r2 = e(tail, H), e(tail, H)
+    moe4.moe4_join_norm_backward(res[-tail:].clone(), x[-tail:].clone(), b[-tail:].clone(), w, big[4][-tail:].clone(), d2,
+                                 dres=r2, rstd_post=big[3][-tail:].clone(), **kw)
+    # rows are independent of each other; the sums' split may differ, by 2 (H + 8) 2^-24 of the terms'
+    # magnitudes (of order one here), and a rounding to bf16 then by a step
+    for a, c in ((db, d2), (dres, r2)):
+        assert torch.allclose(a[-tail:].float(), c.float(), rtol=2.0 ** -7, atol=1e-3)
