@@ -1040,9 +1040,11 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   a.runs = (dsteps + kRun - 1) / kRun;
   a.run_steps = (dsteps + a.runs - 1) / a.runs;
   a.runs = (dsteps + a.run_steps - 1) / a.run_steps;
-  // two tiles share their activations where that leaves two units and more to every wave
+  // Panels are cut (and two tiles share their activations) from so many units on. Us cut and not: NF4
+  // experts of 2048 x 768, 8 each, 4 tokens 17.4 14.1, 8 (8192 by this count) 21.8 19.5, 16 34 39; MXFP4
+  // 2880 x 2880, 4 each, 2 tokens 18.9 16.6, 4 (8640) 25.2 25.0, 8 32 37.
   const int groups = (a.T + 7) / 8;
-  const bool cut = (int64_t)(a.H / 16) * S * a.runs >= 2 * 8 * kDownRoom;
+  const bool cut = (int64_t)(a.H / 16) * S * a.runs >= 12288;
   a.panels = cut ? (a.H + 63) / 64 * groups : 0;
   // as many workgroups as the chip holds at once (some of their waves idle where tiles are few), or one
   // for every tile

@@ -130,11 +130,14 @@ def test_layer_decode(fmt, E, k, H, I, layout, act, bias, T):
 
 
 # enough units of work that the second launch cuts its panels: runs of 2, 3 and 4 steps, few and many
-# units to a panel (parts of one panel by many workgroups, many panels to one), groups of tokens
+# units to a panel (parts of one panel by many workgroups, many panels to one), groups of tokens; and some
+# that are just too few
 @pytest.mark.parametrize("fmt,T,E,k,H,I,bias", [
-    ("nf4", 32, 24, 8, 1088, 320, True), ("nf4", 9, 64, 8, 2112, 832, False), ("nf4", 32, 128, 16, 256, 64, False),
-    ("nf4", 4, 128, 8, 2048, 768, True), ("mx4", 32, 40, 16, 160, 1312, True), ("mx4", 8, 32, 4, 2880, 1056, True),
-    ("mx4", 17, 300, 30, 160, 32, False), ("dq", 25, 12, 6, 1024, 1088, True), ("dq", 10, 64, 8, 1664, 448, False)])
+    ("nf4", 32, 24, 8, 1088, 320, True), ("nf4", 9, 64, 8, 2112, 832, False), ("nf4", 32, 128, 16, 512, 64, False),
+    ("nf4", 32, 128, 16, 256, 64, False), ("nf4", 4, 128, 8, 2048, 768, True), ("mx4", 32, 40, 16, 416, 1312, True),
+    ("mx4", 8, 32, 4, 2880, 2080, True), ("mx4", 17, 300, 30, 416, 32, False), ("mx4", 32, 16, 16, 416, 1024, True),
+    ("mx4", 32, 40, 16, 160, 1312, True), ("dq", 25, 12, 6, 1024, 1088, True), ("dq", 32, 16, 16, 512, 448, False),
+    ("dq", 10, 64, 8, 1664, 448, False)])
 def test_layer_decode_many_units(fmt, T, E, k, H, I, bias):
     assert (H // 16) * T * k >= 4096
     st = Stacks("units", fmt, E, H, I, "interleaved" if bias else "halves", "clamped" if bias else "swiglu", bias)
@@ -154,14 +157,14 @@ def test_many_units_of_one_expert_and_of_all():
 
 
 def test_many_units_captured_and_two_at_once():
-    st = Stacks("cap", "nf4", 48, 1088, 256)
+    st = Stacks("cap", "nf4", 48, 1600, 256)
     T, k = 16, 8
-    buf = [dict(x=torch.zeros((T, 1088), dtype=BF, device="cuda"), lg=torch.zeros((T, 48), device="cuda"),
-                out=torch.zeros((T, 1088), dtype=BF, device="cuda"), ws=st.ws(T, k)) for _ in range(2)]
+    buf = [dict(x=torch.zeros((T, 1600), dtype=BF, device="cuda"), lg=torch.zeros((T, 48), device="cuda"),
+                out=torch.zeros((T, 1600), dtype=BF, device="cuda"), ws=st.ws(T, k)) for _ in range(2)]
 
     def fill(b, key):
         r = rng("cap fill", key)
-        b["x"].copy_(draw(r, (T, 1088))[0])
+        b["x"].copy_(draw(r, (T, 1600))[0])
         b["lg"].copy_(to_dev(r.standard_normal((T, 48)).astype(np.float32)))
         b["out"].fill_(float("nan"))
 
