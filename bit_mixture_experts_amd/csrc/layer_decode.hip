@@ -32,8 +32,10 @@ static_assert(MOE4_LAYER_MOST_TOKENS <= 32, "an expert's tokens are the bits of 
 
 // ---------------------------------------------------------------- weights
 
-// NF4 without rounding: a level is the sum of two bf16 (to 2^-17 of it), both multiply the
-// activations exactly, and the block's absmax is applied to the fp32 sums of its 64 products.
+// NF4 without rounding: a level is the sum of two bf16 (to 8.1e-6 of it, 2^-16.9, and all but one to
+// 2^-17), both multiply the activations exactly, and the block's absmax is applied to the fp32 sums of
+// its 64 products. Both parts of a level but 0 have its sign and are not zero, +-1's too, so that an infinite
+// activation gives the infinity that the level would, not the NaN of opposite ones or of infinity * 0.
 // byte -> (high parts of its two levels, low parts): 8 bytes. LDS holds 32 copies of an entry, a row
 // of 256 bytes, and lane l reads copy l mod 32: no two lanes of a half wave meet in a bank, and a
 // lookup's address is its byte beside the lane's own (one v_perm).
@@ -50,7 +52,8 @@ constexpr Nf4Split make_nf4_split() {
   for (int i = 0; i < 256; ++i)
     for (int h = 0; h < 2; ++h) {
       const float f = kNf4Levels[h ? i >> 4 : i & 15];
-      const uint32_t hi = bf16_rne(f);
+      // the bf16 next to it towards zero
+      const uint32_t hi = f == 0.0f ? 0u : (bits_of(f) - 1) >> 16;
       const uint32_t lo = bf16_rne(f - __builtin_bit_cast(float, hi << 16));
       s.v[2 * i] |= hi << (16 * h);
       s.v[2 * i + 1] |= lo << (16 * h);

@@ -687,9 +687,11 @@ enum { MOE4_LAYER_MOST_TOKENS = 32, MOE4_LAYER_MOST_SLOTS = 512 };
  *   out[t] = sum_j w[t, j] * (W_d[e] h + b_d[e]) (+ residual[t])
  * W_gu of an expert that tokens chose is read once for every 8 of them, W_d once
  * for every group of 8 tokens (0 .. 7, 8 .. 15, ...) that holds one. Weights are
- * not rounded (MXFP4 is exact, NF4's level * absmax is multiplied to 2^-17, where
+ * not rounded (MXFP4 is exact, NF4's level * absmax is multiplied to 2^-16.9, where
  * moe4_expert_forward rounds the product to bf16), sums are fp32 in a fixed order,
- * w h is rounded once to bf16, out once to its type. A token's NaN stays with it.
+ * w h is rounded once to bf16, out once to its type. A token's NaN or infinity
+ * stays with it; an infinite activation takes each weight's sign, as in the formulas
+ * (0 times it is a NaN).
  * For more tokens, adapters, or what a backward pass needs: moe4_route_permute,
  * moe4_expert_forward_gather and moe4_combine.
  *   ex: without adapters (else MOE4_EUNSUPPORTED); variant AUTO or SKINNY; NF4_DQ
