@@ -113,7 +113,11 @@ __global__ __launch_bounds__(kNormThreads<W>) void k_join_norm(const JoinNormArg
       r[i].get(u);
       if (a.wo) wo.get(i, col(i), w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = fmaf(a.res_scale, u[k], c * (a.wo ? v[k] * w[k] : v[k]));
+      for (int k = 0; k < 8; ++k) {
+        // (b * rstd first: b * w_post may leave fp32's range where their product with rstd does not)
+        v[k] *= c;
+        u[k] = fmaf(a.res_scale, u[k], a.wo ? v[k] * w[k] : v[k]);
+      }
       r[i].set(u);
       r[i].get(u);
       ss += squares8(u);
