@@ -222,14 +222,6 @@ inline bool large_tiles_for(int64_t na, int64_t nb) {
   return large_tiles(tiles_of<Tile256>(na, nb), tiles_of<Tile128>(na, nb));
 }
 
-// dynamic LDS above 64 KiB has to be asked for once per kernel and device
-template <typename K>
-inline hipError_t allow_lds(K* kernel, int bytes) {
-  return bytes <= 64 * 1024 ? hipSuccess
-                            : hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 // Parts of k for n tiles of 128 x 128 that leave most of a round (512) empty: as many as fill it,
 // each with at least eight k-tiles of 128 bytes (in bf16 a part's own first loads, the launch that
 // joins and its reads cost about as much as eight). Us of a forward, whole and in parts, bf16: 64
@@ -275,7 +267,7 @@ inline hipError_t launch_product(const FfnProduct& p, hipStream_t s) {
   const int64_t n = tiles_of<S>(p.na, p.nb) * p.splits;
   auto* k = &k_ffn_product<S, MA, MB, FP8>;
   constexpr int kBytes = FP8 ? S::kLdsMx : S::kLds;
-  hipError_t e = allow_lds(k, kBytes);
+  hipError_t e = allow_lds<kBytes>(k);
   if (e != hipSuccess) return e;
   k<<<(uint32_t)n, S::kThreads, kBytes, s>>>(p);
   return hipGetLastError();

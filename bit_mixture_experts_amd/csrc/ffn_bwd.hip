@@ -174,7 +174,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ffn_grads(const GradArgs a) 
 template <typename S>
 hipError_t launch_grads(GradArgs a, int n, hipStream_t s) {
   auto* k = &k_ffn_grads<S>;
-  hipError_t e = allow_lds(k, S::kLds);
+  hipError_t e = allow_lds<S::kLds>(k);
   if (e != hipSuccess) return e;
   a.first[0] = 0;
   for (int i = 0; i < 3; ++i)
@@ -259,7 +259,7 @@ constexpr int kMostGradSplits = 32;
 template <typename S, int LAYOUT, int ACT>
 hipError_t launch_dh(const DhArgs& a, hipStream_t s) {
   auto* k = &k_ffn_dh<S, LAYOUT, ACT>;
-  hipError_t e = allow_lds(k, S::kLds);
+  hipError_t e = allow_lds<S::kLds>(k);
   if (e != hipSuccess) return e;
   k<<<(uint32_t)(tiles_of<S>(a.I, a.T) * a.splits), S::kThreads, S::kLds, s>>>(a);
   e = hipGetLastError();

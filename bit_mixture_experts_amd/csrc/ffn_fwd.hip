@@ -457,7 +457,7 @@ hipError_t launch_skinny(const GateUpArgs& g, const FfnProduct& d, hipStream_t s
     constexpr int kRt = FP8 ? 4 : decltype(rc)::value;
     using G = Skinny<kRt, 8, NT, FP8>;
     auto* k = &k_ffn_gate_up_skinny<kRt, 8, NT, FP8>;
-    hipError_t e = allow_lds(k, G::kLds);
+    hipError_t e = allow_lds<G::kLds>(k);
     if (e != hipSuccess) return e;
     k<<<dim3((g.I + 8 * kRt - 1) / (8 * kRt), nt), G::kThreads, G::kLds, s>>>(g);
     return hipGetLastError();
@@ -470,7 +470,7 @@ hipError_t launch_skinny(const GateUpArgs& g, const FfnProduct& d, hipStream_t s
     constexpr int kRt = decltype(rc)::value;
     using D = Skinny<kRt, 8, NT, FP8>;
     auto* k = &k_ffn_down_skinny<kRt, 8, NT, FP8>;
-    hipError_t r = allow_lds(k, D::kLds);
+    hipError_t r = allow_lds<D::kLds>(k);
     if (r != hipSuccess) return r;
     k<<<dim3((d.na + 16 * kRt - 1) / (16 * kRt), nt), D::kThreads, D::kLds, s>>>(d);
     return hipGetLastError();
@@ -482,7 +482,7 @@ hipError_t launch_gate_up(const GateUpArgs& g, hipStream_t s) {
   return with_kind(g.layout, g.act.act, [&](auto l, auto c) {
     auto* k = &k_ffn_gate_up<S, FP8, decltype(l)::value, decltype(c)::value>;
     constexpr int kBytes = FP8 ? S::kLdsMx : S::kLds;
-    hipError_t e = allow_lds(k, kBytes);
+    hipError_t e = allow_lds<kBytes>(k);
     if (e != hipSuccess) return e;
     k<<<(uint32_t)(tiles_of<S>(2 * (int64_t)g.I, g.T) * g.splits), S::kThreads, kBytes, s>>>(g);
     return hipGetLastError();

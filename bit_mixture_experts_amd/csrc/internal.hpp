@@ -180,6 +180,16 @@ hipError_t launch_layer_decode(const moe4_experts& ex, const uint16_t* x, const 
                                void* out, int out_dtype, int32_t* topk_idx, float* topk_w,
                                void* ws, hipStream_t s);
 
+// Dynamic LDS above 64 KiB has to be asked for, once per kernel and device. It is the process's
+// setting, so a kernel asks for one number, the most that any launch of it takes: with a call's own,
+// a thread that asks for less between another's asking and launching would have that launch refused.
+template <int BYTES, typename K>
+inline hipError_t allow_lds(K* kernel) {
+  return BYTES <= 64 * 1024 ? hipSuccess
+                            : hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+}
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace moe4

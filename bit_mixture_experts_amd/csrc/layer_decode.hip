@@ -1026,13 +1026,7 @@ struct LayerWs {
   }
 };
 
-// dynamic LDS above 64 KiB has to be asked for once per kernel and device
-template <typename K>
-hipError_t allow_lds(K* kernel, int bytes) {
-  return bytes <= 64 * 1024 ? hipSuccess
-                            : hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
+constexpr int kLdsAll = 160 * 1024;   // of a CU
 
 template <int FMT>
 hipError_t launch_layer(LayerArgs a, hipStream_t s) {
@@ -1053,10 +1047,11 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   // for every tile
   const int64_t tiles = (int64_t)S * (a.I / 4), room = 256;
   const int lds = (lut_bytes(FMT) + route_lds(a.E, S) + 15) / 16 * 16;
-  const bool xl = kMx && lds + x_lds(a.T, a.H) <= 160 * 1024;
+  static_assert(lut_bytes(FMT) + route_lds(1024, MOE4_LAYER_MOST_SLOTS) + 16 <= kLdsAll, "any call's first launch fits");
+  const bool xl = kMx && lds + x_lds(a.T, a.H) <= kLdsAll;
   auto up = [&](auto* k) {
     const int bytes = lds + (xl ? x_lds(a.T, a.H) : 0);
-    hipError_t e = allow_lds(k, bytes);
+    hipError_t e = allow_lds<kLdsAll>(k);
     if (e != hipSuccess) return e;
     k<<<(uint32_t)(tiles < room ? tiles : room), 512, bytes, s>>>(a);
     return hipGetLastError();
@@ -1067,7 +1062,7 @@ hipError_t launch_layer(LayerArgs a, hipStream_t s) {
   if (e != hipSuccess) return e;
   auto down = [&](auto* k, int grid, int tt) {
     const int bytes = lut_bytes(FMT) + 8 * 8 * 8 * tt * 4 + S * ((int)sizeof(Use) + 8) + 4;
-    hipError_t r = allow_lds(k, bytes);
+    hipError_t r = allow_lds<kLdsAll>(k);
     if (r != hipSuccess) return r;
     k<<<grid, 512, bytes, s>>>(a);
     return hipGetLastError();

@@ -651,7 +651,7 @@ hipError_t launch_skinny(const FfnProduct& p, hipStream_t s) {
     constexpr int RT = decltype(rc)::value;
     using C = LinSkinny<RT, NT, XF>;
     auto* k = &k_linear_skinny<RT, NT, XF>;
-    hipError_t e = allow_lds(k, C::kLds);
+    hipError_t e = allow_lds<C::kLds>(k);
     if (e != hipSuccess) return e;
     k<<<dim3((p.na + 16 * RT - 1) / (16 * RT), (p.nb + 16 * NT - 1) / (16 * NT)), 512, C::kLds, s>>>(p);
     return hipGetLastError();
@@ -698,7 +698,7 @@ hipError_t launch_tiled(const FfnProduct& p, hipStream_t s) {
   auto run = [&](auto sc) {
     using S = decltype(sc);
     auto* k = &k_linear<S, XF>;
-    hipError_t e = allow_lds(k, LinLds<S, XF>::kBytes);
+    hipError_t e = allow_lds<LinLds<S, XF>::kBytes>(k);
     if (e != hipSuccess) return e;
     k<<<(uint32_t)(tiles_of<S>(p.na, p.nb) * p.splits), S::kThreads, LinLds<S, XF>::kBytes, s>>>(p);
     return hipGetLastError();
@@ -786,7 +786,7 @@ hipError_t launch_linear_backward(const moe4_linear& l, const uint16_t* dy, int 
     auto run = [&](auto sc) {
       using S = decltype(sc);
       auto* k = &k_linear_dx<S>;
-      hipError_t e = allow_lds(k, S::kLds);
+      hipError_t e = allow_lds<S::kLds>(k);
       if (e != hipSuccess) return e;
       k<<<(uint32_t)(tiles_of<S>(l.K, T) * p.splits), S::kThreads, S::kLds, s>>>(p);
       return hipGetLastError();
