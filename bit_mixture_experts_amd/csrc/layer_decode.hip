@@ -91,7 +91,7 @@ __device__ __forceinline__ void fill_lut(uint8_t* lut, const float* book) {
   }
 }
 // (the table begins LDS, so that the byte and the lane's place are the address: the kernels have no
-// static LDS, and their dynamic LDS begins with it)
+// static LDS, and their dynamic LDS begins with it; tests/test_layer_resources.py holds them to that)
 __device__ __forceinline__ u32x2 lookup(uint32_t w, int byte, uint32_t lane8) {
   typedef const u32x2 __attribute__((address_space(3))) entry_t;
   return *reinterpret_cast<entry_t*>(__builtin_amdgcn_perm(w, lane8, 0x0C0C0000u | (4 + byte) << 8));
