@@ -20,6 +20,10 @@ constexpr int kWave = 64;
 // size returns zeros, which takes the place of per-lane bounds branches.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr int kOob = 0x7FFFFFF0;   // offset past the end of any resource used here
+// an offset, kOob too, `by` bytes further on: unsigned, as the hardware compares it (a signed sum would
+// overflow)
+__host__ __device__ constexpr int offset_past(int off, uint32_t by) { return (int)((uint32_t)off + by); }
+static_assert((uint32_t)offset_past(kOob, 1024) > (uint32_t)kOob, "still past the end");
 // cache-policy operand of the raw buffer builtins: the non-temporal bit
 constexpr int kCpolNt = 2;
 

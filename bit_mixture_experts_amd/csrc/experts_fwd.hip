@@ -188,7 +188,7 @@ __device__ __forceinline__ void skinny_load(SkinnyBatch<NRT>& bt, const SkinnyLa
     if constexpr (FULL) {
       const int base = live ? sl.aoff + (rt * 16 * K + kb) * 2 : kOob;
 #pragma unroll
-      for (int st = 0; st < 4; ++st) bt.av[rt][st] = buf_load_b128(sl.ra, base + 64 * st);
+      for (int st = 0; st < 4; ++st) bt.av[rt][st] = buf_load_b128(sl.ra, offset_past(base, 64 * st));
     } else {
 #pragma unroll
       for (int st = 0; st < 4; ++st) {

@@ -259,7 +259,8 @@ __device__ __forceinline__ void load_acts(u32x4 (&x)[4], rsrc_t r, int off, int 
   for (int i = 0; i < 4; i += kEach) {
     const int kk = k + act_k<FMT>(i), at = off != kOob && kk < K ? off + 2 * kk : kOob;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) x[i + j] = buf_load_b128(r, at + 2 * (act_k<FMT>(i + j) - act_k<FMT>(i)));
+    for (int j = 0; j < kEach; ++j)
+      x[i + j] = buf_load_b128(r, offset_past(at, 2 * (act_k<FMT>(i + j) - act_k<FMT>(i))));
   }
 }
 

@@ -70,7 +70,7 @@ struct TurnScales {
     for (int i = 0; i < kRows; ++i) {
       const int at = (int)((off[i] & ~3u) + 16 * pair);
       raw[i] = buf_load_b128(r[i], at);
-      if (shifted) more[i] = buf_load_b32(r[i], at + 16);
+      if (shifted) more[i] = buf_load_b32(r[i], offset_past(at, 16));
     }
   }
   __device__ __forceinline__ void store(int turn, uint8_t* lds) const {
