@@ -611,8 +611,10 @@ size_t moe4_grad_workspace_size(int32_t n);
  * power of two, from 2^-127 on, that brings the block's largest magnitude to at
  * most 7, which is half a step past the largest code 6; codes are value / scale
  * rounded to nearest even, 7 and what lies between it and 6 to 6, so no value
- * is off by more than half a step. A block that holds an infinity or a NaN takes
- * scale byte 255 (NaN) and codes 0.
+ * is off by more than half a step. (The microscaling specification's own conversion
+ * takes the power of two under the largest magnitude over 4: where that lies between
+ * 7 and 8 times the scale it is clipped to 6, here the block takes the next scale.) A block that
+ * holds an infinity or a NaN takes scale byte 255 (NaN) and codes 0.
  *   x [R, K] of x_dtype (16-byte aligned); K % 32 == 0
  *   blocks u8 [R, K/32, 16] out (16-byte aligned), scales u8 [R, K/32] out
  *   values bf16 [R, K] out (16-byte aligned) or NULL: what the codes stand for
