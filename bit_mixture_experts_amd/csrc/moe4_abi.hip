@@ -1177,13 +1177,14 @@ static int check_layer_decode(const moe4_experts* ex, int32_t T, int32_t k) {
     return fail(MOE4_EUNSUPPORTED, "moe4_layer_decode: adapters (lora_A) take moe4_expert_forward");
   if (ex->variant == MOE4_VARIANT_TILED)
     return fail(MOE4_EUNSUPPORTED, "moe4_layer_decode: moe4_experts.variant TILED");
+  // the width up to which the other calls decode both levels of the absmax in place; beyond it they
+  // expand them into their workspace, which this one does not
   if (ex->format == MOE4_FMT_NF4_DQ && (ex->H > 16384 || ex->I > 16384))
     return fail(MOE4_EUNSUPPORTED, "moe4_layer_decode: double-quantised rows of H = %d, I = %d "
                 "beyond 16384", ex->H, ex->I);
-  // one launch's grid: slots x groups of 16 pairs
+  // all rows of h (512 of I bf16 values) and all tokens stand in one buffer each, of 32-bit byte offsets
   if (ex->H > 1 << 20 || ex->I > 1 << 20)
     return fail(MOE4_ESHAPE, "moe4_layer_decode: H = %d, I = %d beyond 2^20", ex->H, ex->I);
-  // the scales and the activations are addressed with 32-bit byte offsets too
   if (T < 0 || T > MOE4_LAYER_MOST_TOKENS)
     return fail(MOE4_ESHAPE, "T = %d outside [0, %d]", T, (int)MOE4_LAYER_MOST_TOKENS);
   if (k < 1 || k > ex->E) return fail(MOE4_ESHAPE, "k = %d outside [1, E = %d]", k, ex->E);

@@ -694,15 +694,22 @@ enum { MOE4_LAYER_MOST_TOKENS = 32, MOE4_LAYER_MOST_SLOTS = 512 };
  *   out[t] = sum_j w[t, j] * (W_d[e] h + b_d[e]) (+ residual[t])
  * W_gu of an expert that tokens chose is read once for every 8 of them, W_d once
  * for every group of 8 tokens (0 .. 7, 8 .. 15, ...) that holds one. Weights are
- * not rounded (MXFP4 is exact, NF4's level * absmax is multiplied to 2^-16.9, where
- * moe4_expert_forward rounds the product to bf16), sums are fp32 in a fixed order,
- * w h is rounded once to bf16, out once to its type. A token's NaN or infinity
- * stays with it; an infinite activation takes each weight's sign, as in the formulas
- * (0 times it is a NaN).
+ * not rounded (MXFP4 is exact below 2^128; NF4's level * absmax is multiplied to
+ * 2^-16.9, where moe4_expert_forward rounds the product to bf16), sums are fp32 in
+ * a fixed order, w h is rounded once to bf16, out once to its type. A token's NaN or
+ * infinity stays with it; an infinite activation takes each weight's sign, as in the
+ * formulas (0 times it is a NaN).
  * For more tokens, adapters, or what a backward pass needs: moe4_route_permute,
- * moe4_expert_forward_gather and moe4_combine.
- *   ex: without adapters (else MOE4_EUNSUPPORTED); variant AUTO or SKINNY; NF4_DQ
- *   with H and I up to 16384
+ * moe4_expert_forward_gather and moe4_combine. They are also the faster way from
+ * about 9 tokens on in NF4 and 17 in MXFP4, as they read an expert's weights once
+ * for all of its tokens. Us, this call and those in a captured graph: 128 NF4 experts
+ * of 2048 x 768, 8 each, 1 token 19.7 22.0, 4 36 42, 8 51 59, 12 72 68, 16 79 75,
+ * 32 115 95 (double-quantised 19.8 23.1, 40 41, 59 59, 83 69, 92 73, 135 94); 32
+ * MXFP4 experts of 2880 x 2880, 4 each, 1 token 27.6 29.5, 4 62 67, 8 82 88,
+ * 16 110 111, 24 132 123, 32 162 130.
+ *   ex: without adapters (else MOE4_EUNSUPPORTED); variant AUTO or SKINNY; H and I
+ *   up to 2^20, NF4_DQ up to 16384, where moe4_expert_forward decodes its absmax in
+ *   place
  *   x bf16 [T, H] (16-byte aligned), logits f32 [T, E], 1 <= k <= E, T <=
  *   MOE4_LAYER_MOST_TOKENS, T * k <= MOE4_LAYER_MOST_SLOTS (else MOE4_ESHAPE);
  *   NaN logits give unspecified (but some k distinct) experts
