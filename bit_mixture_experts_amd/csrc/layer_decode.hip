@@ -389,16 +389,6 @@ struct LayerArgs {
   int panels;
 };
 
-// A logit as an unsigned number of moe4_route's order: larger first, +0 as -0, NaN below all; 0 is
-// no candidate. Equal ones: the lower expert first.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
-  return v != v ? 1u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_logit(uint32_t o) {
-  return o == 1u ? __uint_as_float(0x7FC00000u)
-                 : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
-}
 template <int CTRL>
 __device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
   return max(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xF, 0xF, false));
@@ -414,7 +404,8 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
   return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// A token's keys in a wave: lane l holds experts l, l + 64, ...
+// A token's keys (route.hpp's order) in a wave: lane l holds experts l, l + 64, ... 0 is no candidate, a
+// NaN 1. Of equal logits the lower expert is taken first, by where the key is found.
 template <int NPL>
 struct Keys {
   uint32_t key[NPL];
@@ -425,7 +416,7 @@ struct Keys {
   }
   __device__ __forceinline__ void order(int E) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) key[i] = lane_id() + kWave * i < E ? order_key(v[i]) : 0u;
+    for (int i = 0; i < NPL; ++i) key[i] = lane_id() + kWave * i < E ? max(order_key(v[i]), 1u) : 0u;
   }
   // takes the first expert of the order out; its key in *k
   __device__ __forceinline__ int pick(uint32_t* k) {

@@ -6,23 +6,26 @@
 namespace moe4 {
 
 // Selection order: larger logit first, then lower expert index; +0 == -0.
-// Each candidate becomes one 64-bit key that is unique and ordered the same
-// way: the logit's bits mapped to an unsigned order (negative values have all
-// bits flipped, the others get the sign bit set; -0 is taken as +0), then the
-// inverted expert index. NaN maps to the lowest value (order 0), so the k
-// chosen experts are always distinct and in range. Key 0 marks a lane slot
-// with no candidate (past E, or already chosen).
-__device__ __forceinline__ uint64_t select_key(float v, int e) {
+// order_key maps a logit's bits to an unsigned order (negative values have all
+// bits flipped, the others get the sign bit set; -0 is taken as +0). NaN maps to
+// the lowest value (0; the next one up is -infinity's 0x7FFFFF), so the k
+// chosen experts are always distinct and in range.
+__device__ __forceinline__ uint32_t order_key(float v) {
   uint32_t u = __float_as_uint(v);
   if (u == 0x80000000u) u = 0u;
   uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   if (v != v) o = 0u;
-  return ((uint64_t)o << 32) | (uint32_t)~(uint32_t)e;
+  return o;
 }
-// The logit a key was made from (-0 comes back as +0, NaN as a NaN).
-__device__ __forceinline__ float key_value(uint64_t key) {
-  const uint32_t o = (uint32_t)(key >> 32);
+// The logit a key was made from (-0 comes back as +0, and below -infinity's key are NaNs).
+__device__ __forceinline__ float key_logit(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+// Each candidate becomes one 64-bit key that is unique and ordered the same
+// way: its logit's, then the inverted expert index. Key 0 marks a lane slot
+// with no candidate (past E, or already chosen).
+__device__ __forceinline__ uint64_t select_key(float v, int e) {
+  return ((uint64_t)order_key(v) << 32) | (uint32_t)~(uint32_t)e;
 }
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
@@ -119,9 +122,7 @@ __device__ __forceinline__ void route_token(const float* __restrict__ row, int E
     best = wave_max_u64(best);
     // the same in every lane: take it into scalar registers
     const uint32_t be = ~(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)best);
-    const float bv = key_value(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(
-                                    (int)(uint32_t)(best >> 32)))
-                               << 32);
+    const float bv = key_logit((uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(best >> 32)));
     if (j == 0) top = bv;
     if ((int)(be & (kWave - 1)) == l) {
 #pragma unroll
