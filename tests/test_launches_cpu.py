@@ -1,4 +1,7 @@
-"""Grids and LDS of the launches, without a GPU."""
+"""Grids, LDS and workspaces of the launches, without a GPU."""
+import math
+import random
+
 import pytest
 
 from tests.launches import LDS, first_lds, record, second_cut, table_lds
@@ -72,3 +75,32 @@ def test_the_layer_launches_what_its_rules_say(recorded):
         cuts.add((fmt, cut))
     assert inside == {("nf4", False), ("dq", False), ("mx4", False), ("mx4", True)}
     assert cuts == {(f, c) for f in FMT for c in (False, True)}
+
+
+def test_parts_of_linear_products_fit_the_workspace(tmp_path):
+    # a product cut along k leaves `splits` sums of all its outputs: read off the grid, for drawn sizes
+    r = random.Random(7)
+    size = lambda lo, hi, m: max(m, round(math.exp(r.uniform(math.log(lo), math.log(hi)))) // m * m)   # noqa: E731
+    calls, what = [], []
+    while len(what) < 400:
+        N, K, T = size(8, 30000, 8), size(32, 30000, 32), size(1, 20000, 1)
+        lin = dict(struct="Moe4Linear", N=N, K=K, variant=r.choice([0, moe4.MOE4_VARIANT_TILED]), w_q=P, w_s=P)
+        f = r.choice([moe4.MOE4_X_BF16, moe4.MOE4_X_MXFP8, moe4.MOE4_X_MXFP4])
+        calls += [["moe4_linear_workspace_size", [dict(lin), T, 0]],
+                  ["moe4_linear_forward", [dict(lin), P, f, None if f == moe4.MOE4_X_BF16 else P, T, None, 0, P, BF, P, 1 << 40, None]],
+                  ["moe4_linear_workspace_size", [dict(lin), T, 1]],
+                  ["moe4_linear_backward", [dict(lin), P, T, None, 0, P, BF, P, BF, P, 1 << 40, None]]]
+        what += [(N, T, 64, 0), (K, T, 128, 128 * N * 4 if T > 512 else 0)]   # outputs, rows, rows of a tile, more
+    got, cut = record(calls, tmp_path), 0
+    for (cols, rows, tile, more), bytes_, call in zip(what, got[0::2], got[1::2]):
+        assert call["rc"] == 0
+        first = [e for e in call["events"] if e["allowed"] < 0][0]
+        tiles = -(-cols // 128) * -(-rows // tile)
+        if first["block"][0] != 256 or first["grid"][1] != 1:
+            continue   # few tokens, or the larger tiles, which are not cut
+        splits, rest = divmod(first["grid"][0], tiles)
+        assert rest == 0 and splits >= 1
+        part = splits * rows * cols * 4 if splits > 1 else 0
+        assert (-(-part // 256) * 256 + more if more else part) <= bytes_["rc"], (cols, rows, splits)
+        cut += splits > 1
+    assert cut > 50
