@@ -841,7 +841,8 @@ def moe4_layer_decode(ex, x, logits, k, out, residual=None, topk_idx=None, topk_
                       renormalize=True, ws=None, stream=None):
     """The whole routed layer for up to MOE4_LAYER_MOST_TOKENS tokens: x bf16 [T, H], logits f32
     [T, E] -> out bf16 or f32 [T, H] (+ residual bf16 or f32); topk_idx i32 and topk_w f32 [T, k]
-    take the routing."""
+    take the routing. From about 9 tokens on in NF4, 17 in MXFP4, moe4_route_permute,
+    moe4_expert_forward_gather and moe4_combine are faster."""
     c = _Call("layer_decode")
     T, H = x.shape[0], ex.H
     if T >> 31:
